@@ -100,6 +100,48 @@ class defrag_monitor_report(ctypes.Structure):
                 ("seconds_to_full", ctypes.c_double)]
 
 
+class defrag_kv_cache(ctypes.Structure):
+    _fields_ = [("arena_dev", ctypes.c_void_p), ("arena_bytes", ctypes.c_uint64),
+                ("pages_dev", ctypes.c_void_p), ("page_stride", ctypes.c_uint64),
+                ("lens_dev", ctypes.c_void_p), ("batch", ctypes.c_uint32),
+                ("heads", ctypes.c_uint32), ("dim", ctypes.c_uint32), ("codes", ctypes.c_int32),
+                ("n_invalid_dev", ctypes.c_void_p)]
+
+
+class defrag_kv_append_args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(defrag_kv_cache)), ("k_dev", ctypes.c_void_p),
+                ("v_dev", ctypes.c_void_p), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("max_new", ctypes.c_uint32), ("tokens", ctypes.c_uint64),
+                ("starts_dev", ctypes.c_void_p), ("weight_dev", ctypes.c_void_p),
+                ("pos_dev", ctypes.c_void_p), ("first_pos_dev", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_uint64)]
+
+
+class defrag_kv_attend_args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(defrag_kv_cache)), ("q_dev", ctypes.c_void_p),
+                ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("group", ctypes.c_uint32), ("tokens", ctypes.c_uint64),
+                ("starts_dev", ctypes.c_void_p), ("max_new", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32), ("out_dev", ctypes.c_void_p),
+                ("lse_dev", ctypes.c_void_p), ("weight_dev", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_uint64)]
+
+
+class defrag_kv_evict_args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(defrag_kv_cache)), ("budget", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("sink", ctypes.c_int32), ("recent", ctypes.c_int32),
+                ("next_pos_dev", ctypes.c_void_p), ("weight_dev", ctypes.c_void_p),
+                ("pos_dev", ctypes.c_void_p), ("weight_stride", ctypes.c_uint64),
+                ("weight_out_dev", ctypes.c_void_p), ("pos_out_dev", ctypes.c_void_p),
+                ("weight_out_stride", ctypes.c_uint64), ("lens_out_dev", ctypes.c_void_p)]
+
+
+KV_PAGE_TOKENS = 64                # DEFRAG_KV_PAGE_TOKENS
+KV_CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}     # DEFRAG_KV_E4M3, DEFRAG_KV_INT8
+KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1}      # DEFRAG_KV_BF16, DEFRAG_KV_FP16
+
 LEVELS = {0: "OK", 1: "WARNING", 2: "CRITICAL"}
 ACTIONS = {0: "none", 1: "targeted", 2: "full", 3: "no_room"}
 
@@ -168,12 +210,22 @@ def _load() -> ctypes.CDLL:
                                         ctypes.POINTER(defrag_stats_t)]
     L.defrag_monitor.argtypes = [ctypes.POINTER(defrag_stats_t), ctypes.POINTER(defrag_monitor_cfg),
                                  ctypes.POINTER(defrag_monitor_report)]
+    L.defrag_kv_page_bytes.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
+    L.defrag_kv_append.argtypes = [ctypes.POINTER(defrag_kv_append_args), P]
+    L.defrag_kv_attend_workspace_bytes.argtypes = [ctypes.POINTER(defrag_kv_attend_args)]
+    L.defrag_kv_attend.argtypes = [ctypes.POINTER(defrag_kv_attend_args), P, S, P]
+    L.defrag_kv_evict_workspace_bytes.argtypes = [ctypes.POINTER(defrag_kv_evict_args)]
+    L.defrag_kv_evict.argtypes = [ctypes.POINTER(defrag_kv_evict_args), P, S, P]
+    for f in ("defrag_kv_page_bytes", "defrag_kv_attend_workspace_bytes",
+              "defrag_kv_evict_workspace_bytes"):
+        getattr(L, f).restype = S
     L.defrag_strerror.argtypes = [ctypes.c_int]
     L.defrag_strerror.restype = ctypes.c_char_p
     for f in ("defrag_stats", "defrag_first_fit", "defrag_plan", "defrag_plan_targeted",
               "defrag_move", "defrag_monitor", "defrag_compact", "defrag_compact_static",
               "defrag_move_status", "defrag_move_report", "defrag_plan_tiles",
-              "defrag_remap", "defrag_commit"):
+              "defrag_remap", "defrag_commit", "defrag_kv_append", "defrag_kv_attend",
+              "defrag_kv_evict"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -186,6 +238,8 @@ EXPORTS = ("defrag_workspace_bytes", "defrag_stats", "defrag_first_fit", "defrag
            "defrag_move_status", "defrag_move_report", "defrag_plan_tiles", "defrag_remap",
            "defrag_commit",
            "defrag_compact", "defrag_compact_static", "defrag_monitor",
+           "defrag_kv_page_bytes", "defrag_kv_append", "defrag_kv_attend_workspace_bytes",
+           "defrag_kv_attend", "defrag_kv_evict_workspace_bytes", "defrag_kv_evict",
            "defrag_strerror")
 
 
@@ -464,6 +518,202 @@ def defrag_monitor(stats: defrag_stats_t, warning_ratio: float = 0.85,
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_monitor")
     return out
+
+
+def defrag_kv_page_bytes(heads: int, dim: int) -> int:
+    """Bytes of a cache page (64 tokens of every head), a multiple of 32."""
+    nb = int(lib.defrag_kv_page_bytes(heads, dim))
+    if nb == 0:
+        raise DefragError(DEFRAG_EINVAL, "defrag_kv_page_bytes")
+    return nb
+
+
+def _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid) -> defrag_kv_cache:
+    """The defrag_kv_cache of a call and the checks of its tensors."""
+    _need(arena, torch.uint8, 0, "arena")
+    _need(pages, torch.int64, 0, "pages")
+    _need(lens, torch.int32, 0, "lens")
+    _need(n_invalid, torch.int64, 1, "n_invalid")
+    if codes not in KV_CODES:
+        raise ValueError(f"codes: {codes}, expected one of {list(KV_CODES)}")
+    if pages.dim() != 2 or lens.dim() != 1 or pages.shape[0] != lens.shape[0]:
+        raise ValueError("pages: [batch, pages] and lens: [batch] expected")
+    for t, what in ((pages, "pages"), (lens, "lens"), (n_invalid, "n_invalid")):
+        _same_device(t, arena, what)
+    return defrag_kv_cache(_ptr(arena), arena.numel(), _ptr(pages), pages.shape[1], _ptr(lens),
+                           pages.shape[0], heads, dim, KV_CODES[codes], _ptr(n_invalid))
+
+
+def _same_device(t, arena, what: str) -> None:
+    if t is not None and t.device != arena.device:
+        raise ValueError(f"{what}: on {t.device}, the arena is on {arena.device}")
+
+
+def _kv_rows(t, arena, what: str, dim: Optional[int] = None, heads: Optional[int] = None) -> None:
+    """A [tokens, heads, dim] tensor of 16 bits whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in KV_DTYPES:
+        raise ValueError(f"{what}: expected a tensor of {list(KV_DTYPES)}")
+    if t.dim() != 3 or (dim is not None and t.shape[2] != dim) or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}")
+    if not t.is_cuda or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what}: expected a GPU tensor with a dense last dimension")
+    _same_device(t, arena, what)
+
+
+def _kv_plane(t, arena, dtype, shape, what: str) -> int:
+    """Checks a contiguous [batch, heads, places] tensor; its number of places."""
+    if t is None:
+        return 0
+    _need(t, dtype, 0, what)
+    if t.dim() != 3 or tuple(t.shape[:2]) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, [{shape[0]}, {shape[1]}, places] expected")
+    _same_device(t, arena, what)
+    return t.shape[2]
+
+
+def _kv_new(starts, max_new, tokens: int, batch: int, arena) -> int:
+    """Checks starts and gives max_new its default."""
+    if starts is None:
+        if tokens != batch:
+            raise ValueError(f"starts: {tokens} tokens of {batch} sequences need it")
+        return min(1, tokens)
+    _need(starts, torch.int32, batch + 1, "starts")
+    _same_device(starts, arena, "starts")
+    return tokens if max_new is None else min(int(max_new), tokens)
+
+
+def _kv_scratch(nbytes: int, stream, device) -> torch.Tensor:
+    """Memory for one call, from the pool of the stream that it runs on."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Optional[int] = None,
+                     weight=None, pos=None, first_pos=None, n_invalid=None, stream=None) -> None:
+    """Quantise new tokens' keys and values [tokens, heads, dim] into the
+    pages of the cache.  arena: uint8; pages: int64 [batch, pages] byte offsets
+    in it; lens: int32 [batch], the lengths before the call (not changed);
+    codes: torch.float8_e4m3fn or torch.int8; starts: int32 [batch + 1], the
+    first new token of each sequence (None: one a sequence), at most max_new
+    each.  weight (float32) and pos (int32), [batch, heads, places], get 0 and
+    first_pos[b] + the token's number (default: its place)."""
+    _kv_rows(k, arena, "k")
+    tokens, heads, dim = k.shape
+    _kv_rows(v, arena, "v", dim, heads)
+    if v.shape[0] != tokens or v.dtype != k.dtype:
+        raise ValueError("v: another shape or dtype than k")
+    c = _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid)
+    batch = c.batch
+    most = _kv_new(starts, max_new, tokens, batch, arena)
+    cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
+    cap2 = _kv_plane(pos, arena, torch.int32, (batch, heads), "pos")
+    if weight is not None and pos is not None and cap != cap2:
+        raise ValueError("pos: another number of places than weight")
+    _need(first_pos, torch.int32, batch, "first_pos")
+    _same_device(first_pos, arena, "first_pos")
+    a = defrag_kv_append_args(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                              v.stride(0), v.stride(1), KV_DTYPES[k.dtype], most, tokens,
+                              _ptr(starts), _ptr(weight), _ptr(pos), _ptr(first_pos), cap or cap2)
+    rc = lib.defrag_kv_append(ctypes.byref(a), _stream(stream))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_append")
+
+
+def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
+                     max_new: Optional[int] = None, max_len: Optional[int] = None,
+                     scale: Optional[float] = None, out=None, lse=None, weight=None,
+                     n_invalid=None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the newest tokens' queries [tokens, query heads, dim] over
+    the cache; returns out, of q's type.  lens counts the new tokens too (call
+    defrag_kv_append first).  `heads` key/value heads, each read by an equal
+    share of the query heads.  max_len: no length exceeds it (default: what
+    the page table holds); scale: default dim ** -0.5.  lse: float32 [tokens,
+    query heads]; weight: float32 [batch, heads, places], increased by the
+    weight each cached token receives.  ws: workspace, allocated if None."""
+    _kv_rows(q, arena, "q")
+    tokens, q_heads, dim = q.shape
+    if heads < 1 or q_heads % heads:
+        raise ValueError(f"q: {q_heads} heads over {heads} key/value heads")
+    c = _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid)
+    batch = c.batch
+    most = _kv_new(starts, max_new, tokens, batch, arena)
+    if max_len is None:
+        max_len = pages.shape[1] * KV_PAGE_TOKENS
+    if out is None:
+        if stream is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out: another shape or dtype than q")
+    _same_device(out, arena, "out")
+    _need(lse, torch.float32, tokens * q_heads, "lse")
+    _same_device(lse, arena, "lse")
+    cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
+    a = defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
+                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _ptr(starts), most,
+                              max_len, dim ** -0.5 if scale is None else scale, 0, _ptr(out),
+                              _ptr(lse), _ptr(weight), cap)
+    if ws is None:
+        need = lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a))
+        if need == 0:
+            raise DefragError(DEFRAG_EINVAL, "defrag_kv_attend")
+        ws = _kv_scratch(need, stream, q.device)
+    _same_device(ws, arena, "ws")
+    rc = lib.defrag_kv_attend(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_attend")
+    return out
+
+
+def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, pos_out, lens_out,
+                    dim: int, codes, sink: int = 0, recent: int = 0, next_pos=None,
+                    max_len: Optional[int] = None, n_invalid=None,
+                    ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keep `budget` (a multiple of 64) tokens of every (sequence, head): those
+    whose position is below sink or at least next_pos - recent, then those of
+    largest weight; they end in the first budget / 64 pages.  weight (float32)
+    and pos (int32): [batch, heads, places]; weight_out, pos_out and lens_out
+    (int32 [batch]) receive the result.  next_pos: int32 [batch] (default:
+    lens); max_len: no length exceeds it (default: what table and planes
+    hold)."""
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 3:
+        raise ValueError("weight: [batch, heads, places] expected")
+    heads = weight.shape[1]
+    c = _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid)
+    batch = c.batch
+    cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
+    if _kv_plane(pos, arena, torch.int32, (batch, heads), "pos") != cap or pos is None:
+        raise ValueError("pos: another shape than weight")
+    cap_out = _kv_plane(weight_out, arena, torch.float32, (batch, heads), "weight_out")
+    if _kv_plane(pos_out, arena, torch.int32, (batch, heads), "pos_out") != cap_out or pos_out is None:
+        raise ValueError("pos_out: another shape than weight_out")
+    if lens_out is None or weight_out is None:
+        raise ValueError("weight_out, pos_out and lens_out are needed")
+    _need(lens_out, torch.int32, batch, "lens_out")
+    _same_device(lens_out, arena, "lens_out")
+    if next_pos is None:
+        next_pos = lens
+    _need(next_pos, torch.int32, batch, "next_pos")
+    _same_device(next_pos, arena, "next_pos")
+    if max_len is None:
+        max_len = min(pages.shape[1] * KV_PAGE_TOKENS, cap)
+    a = defrag_kv_evict_args(ctypes.pointer(c), budget, max_len, sink, recent, _ptr(next_pos),
+                             _ptr(weight), _ptr(pos), cap, _ptr(weight_out), _ptr(pos_out), cap_out,
+                             _ptr(lens_out))
+    if ws is None:
+        need = lib.defrag_kv_evict_workspace_bytes(ctypes.byref(a))
+        if need == 0:
+            raise DefragError(DEFRAG_EINVAL, "defrag_kv_evict")
+        ws = _kv_scratch(need, stream, arena.device)
+    _same_device(ws, arena, "ws")
+    rc = lib.defrag_kv_evict(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_evict")
 
 
 def defrag_strerror(code: int) -> str:

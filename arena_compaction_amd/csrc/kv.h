@@ -1,0 +1,114 @@
+// kv.h -- the 8-bit key/value cache: the layout of a page, its number
+// formats and the launches of its operators (kv_api.cpp checks arguments;
+// kv_append.hip, kv_attend.hip and kv_evict.hip hold the kernels).
+//
+// A page is one block of the arena with 64 tokens of every head.  For head h
+// a strip of 2 * 64 * D bytes: 64 x D key codes, token by token, and then
+// D x 64 value codes, dimension by dimension.  Behind the strips, H pairs of
+// float32 scales (key, value), each a power of two of at least 2^-64.
+//
+// Keys lie token by token and values dimension by dimension because a matrix
+// instruction wants, in each lane, consecutive elements along the axis it
+// sums over: dimensions for query x key, tokens for weight x value.  Both
+// codes are then fed to it as loaded, with no transpose.
+#ifndef ARENA_COMPACTION_KV_H
+#define ARENA_COMPACTION_KV_H
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+namespace ac {
+
+constexpr int kKvPage = 64;       // tokens of a page
+constexpr int kKvExpMin = -64;    // least exponent of a scale
+constexpr uint32_t kKvMaxDim = 256;
+
+inline __host__ __device__ uint64_t kv_page_bytes(uint32_t heads, uint32_t dim) {
+    return (uint64_t)heads * (2ull * kKvPage * dim + 8);
+}
+
+// What every operator is given: the cache, checked on the host.
+struct KvCache {
+    uint8_t *arena;
+    uint64_t arena_bytes;
+    const int64_t *pages;  // [batch][stride] byte offsets
+    uint64_t stride;
+    const int32_t *lens;
+    uint32_t batch, heads, dim;
+    unsigned long long *n_invalid;
+};
+
+struct KvAppend {
+    KvCache c;
+    const uint16_t *k, *v;  // 16-bit elements
+    int64_t k_row, k_head, v_row, v_head;  // strides in elements
+    uint64_t tokens;
+    const int32_t *starts;  // batch + 1, or null: one token a sequence
+    uint32_t max_new;
+    bool vec_k, vec_v;      // 16-byte loads are aligned
+    float *weight;          // [batch][heads][cap], or null
+    int32_t *pos;
+    const int32_t *first_pos;
+    uint64_t cap;
+};
+
+struct KvAttend {
+    KvCache c;
+    const uint16_t *q;
+    int64_t q_row, q_head;
+    uint64_t tokens;
+    const int32_t *starts;
+    uint32_t max_new, max_len, group;
+    bool vec_q;
+    float scale;
+    uint16_t *out;   // [tokens][heads * group][dim]
+    float *lse;      // [tokens][heads * group], or null
+    float *weight;   // [batch][heads][cap], or null
+    uint64_t cap;
+    // the plan (kv_attend_plan)
+    uint32_t splits, per_split;  // pieces of the cache, pages of each
+    uint32_t rows;               // query rows of a workgroup
+    uint32_t row_blocks;
+    float *part;     // [splits][tokens * heads * group][dim + 2]
+    float *scores;   // [batch][heads][pages][row_blocks * rows][64]
+    float *lse2;     // [tokens * heads * group], base-2 log of the sums
+};
+
+struct KvEvict {
+    KvCache c;
+    uint32_t budget, max_len;
+    int32_t sink, recent;
+    const int32_t *next_pos;
+    const float *weight;  // [batch][heads][cap]
+    const int32_t *pos;
+    uint64_t cap;
+    float *weight_out;    // [batch][heads][cap_out]
+    int32_t *pos_out;
+    uint64_t cap_out;
+    int32_t *lens_out;
+    int32_t *src;         // workspace: two lists [batch][heads][budget]
+};
+
+// Bytes of the two lists of an eviction.
+inline uint64_t kv_evict_ws(uint32_t batch, uint32_t heads, uint32_t budget) {
+    return (uint64_t)batch * heads * budget * 8;
+}
+
+struct KvAttendPlan {
+    uint32_t rows, row_blocks, splits, per_split;
+    uint64_t part_bytes, score_bytes, lse_bytes, total;
+};
+
+KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored);
+
+// codes: 0 e4m3, 1 int8; dtype: 0 bfloat16, 1 float16
+hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s);
+hipError_t launch_kv_zero(uint64_t *p, hipStream_t s);
+
+}  // namespace ac
+
+#endif

@@ -1,0 +1,212 @@
+// kv_api.cpp -- the C-ABI entry points of the 8-bit key/value cache:
+// argument checks, workspace layout, launches and error mapping.
+#include "../../include/arena_compaction.h"
+#include "kv.h"
+
+using namespace ac;
+
+namespace {
+
+// Tokens and places of a call: a grid's first axis holds fewer than 2^32
+// lanes, 2^24 workgroups of 256, and each covers a page.
+constexpr uint64_t kMaxTokens = 1u << 29;
+constexpr uint64_t kMaxGrid = (1u << 24) - 1;
+constexpr uint64_t kLeastWs = 256;  // so that 0 can mean "refused"
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+bool dim_ok(uint32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+// The parts of a cache that every call needs; lens_dev and pages_dev may be
+// null only where there is no sequence.
+int check_cache(const defrag_kv_cache *c) {
+    if (!c) return DEFRAG_EINVAL;
+    if (c->batch > 65535 || c->heads < 1 || c->heads > 65535 || !dim_ok(c->dim)) return DEFRAG_EINVAL;
+    if (c->codes != DEFRAG_KV_E4M3 && c->codes != DEFRAG_KV_INT8) return DEFRAG_EINVAL;
+    if (c->page_stride * kKvPage > kMaxTokens || c->page_stride > kMaxTokens) return DEFRAG_EINVAL;
+    if (!aligned(c->arena_dev, 32) || !aligned(c->pages_dev, 8) || !aligned(c->lens_dev, 4))
+        return DEFRAG_EINVAL;
+    if (c->batch && (!c->lens_dev || (c->page_stride && !c->pages_dev))) return DEFRAG_EINVAL;
+    if (c->arena_bytes && !c->arena_dev) return DEFRAG_EINVAL;
+    return DEFRAG_OK;
+}
+
+KvCache cache_of(const defrag_kv_cache *c) {
+    return KvCache{static_cast<uint8_t *>(c->arena_dev), c->arena_bytes, c->pages_dev, c->page_stride,
+                   c->lens_dev, c->batch, c->heads, c->dim,
+                   reinterpret_cast<unsigned long long *>(c->n_invalid_dev)};
+}
+
+// 16-bit rows read 8 elements at a time.
+bool can_vector(const void *p, int64_t row, int64_t head) {
+    return aligned(p, 16) && row % 8 == 0 && head % 8 == 0;
+}
+
+int dtype_ok(int32_t t) { return t == DEFRAG_KV_BF16 || t == DEFRAG_KV_FP16; }
+
+int check_new(const defrag_kv_cache *c, const int32_t *starts, uint64_t tokens, uint32_t max_new) {
+    if (tokens > kMaxTokens || !aligned(starts, 4)) return DEFRAG_EINVAL;
+    if (!starts && tokens != c->batch) return DEFRAG_EINVAL;
+    if (tokens && (c->batch == 0 || max_new == 0)) return DEFRAG_EINVAL;
+    if (max_new > tokens) return DEFRAG_EINVAL;
+    return DEFRAG_OK;
+}
+
+int check_attend(const defrag_kv_attend_args *a) {
+    if (!a) return DEFRAG_EINVAL;
+    int rc = check_cache(a->cache);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = check_new(c, a->starts_dev, a->tokens, a->max_new);
+    if (rc) return rc;
+    if (!dtype_ok(a->dtype) || a->group < 1 || a->group > 256 ||
+        (uint64_t)c->heads * a->group > 65535 || a->max_len > c->page_stride * kKvPage)
+        return DEFRAG_EINVAL;
+    if (!(a->scale - a->scale == 0.0f)) return DEFRAG_EINVAL;  // not finite
+    if (!aligned(a->q_dev, 2) || !aligned(a->out_dev, 16) || !aligned(a->lse_dev, 4) ||
+        !aligned(a->weight_dev, 4))
+        return DEFRAG_EINVAL;
+    if (a->tokens && (!a->q_dev || !a->out_dev)) return DEFRAG_EINVAL;
+    if (a->weight_dev && a->weight_stride < a->max_len) return DEFRAG_EINVAL;
+    return DEFRAG_OK;
+}
+
+KvAttendPlan plan_of(const defrag_kv_attend_args *a) {
+    return kv_attend_plan(a->cache->batch, a->cache->heads, a->group, a->cache->dim, a->tokens,
+                          a->max_new, a->max_len, a->weight_dev != nullptr);
+}
+
+int check_evict(const defrag_kv_evict_args *a) {
+    if (!a) return DEFRAG_EINVAL;
+    const int rc = check_cache(a->cache);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    if (a->budget == 0 || a->budget % kKvPage || a->budget > kMaxTokens)
+        return DEFRAG_EINVAL;
+    if (a->max_len > c->page_stride * kKvPage ||
+        a->max_len > a->weight_stride || a->recent < 0)
+        return DEFRAG_EINVAL;
+    const uint64_t kept = a->budget < a->max_len ? a->budget : a->max_len;
+    if (a->weight_out_stride < kept) return DEFRAG_EINVAL;
+    if (!aligned(a->weight_dev, 4) || !aligned(a->pos_dev, 4) || !aligned(a->next_pos_dev, 4) ||
+        !aligned(a->weight_out_dev, 4) || !aligned(a->pos_out_dev, 4) || !aligned(a->lens_out_dev, 4))
+        return DEFRAG_EINVAL;
+    if (c->batch && (!a->weight_dev || !a->pos_dev || !a->next_pos_dev || !a->weight_out_dev ||
+                     !a->pos_out_dev || !a->lens_out_dev))
+        return DEFRAG_EINVAL;
+    return DEFRAG_OK;
+}
+
+int clear_count(const defrag_kv_cache *c, hipStream_t s) {
+    if (!c->n_invalid_dev) return DEFRAG_OK;
+    if (!aligned(c->n_invalid_dev, 8)) return DEFRAG_EINVAL;
+    return launch_kv_zero(c->n_invalid_dev, s) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+int check_ws(const void *ws, size_t have, uint64_t need) {
+    if (!need) return DEFRAG_OK;
+    if (!ws || !aligned(ws, 256) || have < need) return DEFRAG_EWORKSPACE;
+    return DEFRAG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t defrag_kv_page_bytes(uint32_t heads, uint32_t dim) {
+    if (heads < 1 || heads > 65535 || !dim_ok(dim)) return 0;
+    return (kv_page_bytes(heads, dim) + 31) / 32 * 32;
+}
+
+int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
+    if (!a) return DEFRAG_EINVAL;
+    int rc = check_cache(a->cache);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = check_new(c, a->starts_dev, a->tokens, a->max_new);
+    if (rc) return rc;
+    if (!dtype_ok(a->dtype) || !aligned(a->k_dev, 2) || !aligned(a->v_dev, 2) ||
+        !aligned(a->weight_dev, 4) || !aligned(a->pos_dev, 4) || !aligned(a->first_pos_dev, 4))
+        return DEFRAG_EINVAL;
+    if (a->tokens && (!a->k_dev || !a->v_dev)) return DEFRAG_EINVAL;
+    rc = clear_count(c, stream);
+    if (rc || !a->tokens) return rc;
+    const KvAppend k{cache_of(c),
+                     static_cast<const uint16_t *>(a->k_dev), static_cast<const uint16_t *>(a->v_dev),
+                     a->k_row, a->k_head, a->v_row, a->v_head, a->tokens, a->starts_dev, a->max_new,
+                     can_vector(a->k_dev, a->k_row, a->k_head),
+                     can_vector(a->v_dev, a->v_row, a->v_head), a->weight_dev, a->pos_dev,
+                     a->first_pos_dev, a->weight_stride};
+    return launch_kv_append(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *a) {
+    if (check_attend(a)) return 0;
+    const uint64_t need = a->tokens ? plan_of(a).total : 0;
+    return need > kLeastWs ? need : kLeastWs;
+}
+
+int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_bytes,
+                     hipStream_t stream) {
+    int rc = check_attend(a);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    const KvAttendPlan p = plan_of(a);
+    if (a->tokens) {
+        if ((uint64_t)p.splits * p.row_blocks > kMaxGrid ||
+            (uint64_t)a->max_new * c->heads * a->group > 4 * kMaxGrid)
+            return DEFRAG_EINVAL;
+        rc = check_ws(ws_dev, ws_bytes, p.total);
+        if (rc) return rc;
+    }
+    rc = clear_count(c, stream);
+    if (rc || !a->tokens) return rc;
+    uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+    KvAttend k{};
+    k.c = cache_of(c);
+    k.q = static_cast<const uint16_t *>(a->q_dev);
+    k.q_row = a->q_row;
+    k.q_head = a->q_head;
+    k.tokens = a->tokens;
+    k.starts = a->starts_dev;
+    k.max_new = a->max_new;
+    k.max_len = a->max_len;
+    k.group = a->group;
+    k.vec_q = can_vector(a->q_dev, a->q_row, a->q_head);
+    k.scale = a->scale;
+    k.out = static_cast<uint16_t *>(a->out_dev);
+    k.lse = a->lse_dev;
+    k.weight = a->weight_dev;
+    k.cap = a->weight_stride;
+    k.splits = p.splits;
+    k.per_split = p.per_split;
+    k.rows = p.rows;
+    k.row_blocks = p.row_blocks;
+    k.part = reinterpret_cast<float *>(ws);
+    k.scores = reinterpret_cast<float *>(ws + p.part_bytes);
+    k.lse2 = p.lse_bytes ? reinterpret_cast<float *>(ws + p.part_bytes + p.score_bytes) : nullptr;
+    return launch_kv_attend(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+size_t defrag_kv_evict_workspace_bytes(const defrag_kv_evict_args *a) {
+    if (check_evict(a)) return 0;
+    const uint64_t need = kv_evict_ws(a->cache->batch, a->cache->heads, a->budget);
+    return need > kLeastWs ? need : kLeastWs;
+}
+
+int defrag_kv_evict(const defrag_kv_evict_args *a, void *ws_dev, size_t ws_bytes,
+                    hipStream_t stream) {
+    int rc = check_evict(a);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = check_ws(ws_dev, ws_bytes, kv_evict_ws(c->batch, c->heads, a->budget));
+    if (rc) return rc;
+    rc = clear_count(c, stream);
+    if (rc || !c->batch) return rc;
+    const KvEvict k{cache_of(c), a->budget, a->max_len, a->sink, a->recent, a->next_pos_dev,
+                    a->weight_dev, a->pos_dev, a->weight_stride, a->weight_out_dev, a->pos_out_dev,
+                    a->weight_out_stride, a->lens_out_dev, static_cast<int32_t *>(ws_dev)};
+    return launch_kv_evict(k, c->codes, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+}  // extern "C"

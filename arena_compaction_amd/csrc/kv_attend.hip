@@ -1,0 +1,499 @@
+// kv_attend.hip -- attention of new tokens' queries over the 8-bit cache.
+//
+// For query row r of head h (rows of all the query heads that share h) and
+// tokens j it may see, with q.k over key codes, ek and ev the page's scales:
+//   s_rj = scale * ek * q_r.k_j        p_rj = exp(s_rj) / sum_j exp(s_rj)
+//   out_r = sum_j p_rj * ev * v_j      lse_r = log sum_j exp(s_rj)
+//   weight_j += sum_r p_rj             (where asked for)
+//
+// Everything runs in powers of two, t_rj = log2(e) * s_rj + log2(ev): with
+// the value scale inside the exponent, w_rj = 2^(t_rj - m) multiplies value
+// codes of any page, and sum_j w_rj / ev is the softmax's sum, one factor a
+// page.  m is the running maximum of t less 14: float16 weights then reach
+// down to 2^-38 of the largest before they lose their last bit.
+//
+// A wave takes whole pages, one at a time, with its own running maximum and
+// sums; a page's key codes are loaded while the page before is summed, its
+// value codes while its own scores are made.  Scores come out of the matrix
+// instruction transposed (tokens x rows), so that a lane holds 16 tokens of
+// one row: the maximum needs two steps across lanes, the rescaling none, and
+// the weights are the next product's operand where they are.  Four waves
+// share a workgroup's rows and join through LDS; workgroups split a long
+// cache and k_kv_join joins their parts.
+#include "kv_mfma.h"
+
+namespace ac {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLift = 14.0f;
+#define KV_NEG_INF (-__builtin_inff())
+
+// Place of a call's sequence b: its new tokens, and how many tokens it holds.
+struct Seq {
+    uint64_t first;
+    int count, len, had;
+};
+
+__device__ inline Seq sequence(const KvAttend &a, uint32_t b, bool *bad) {
+    Seq s;
+    new_tokens(a.starts, a.tokens, a.max_new, b, &s.first, &s.count, bad);
+    s.len = a.c.lens[b];
+    if (s.len < 0 || (uint32_t)s.len > a.max_len) {  // as a sequence that holds nothing
+        *bad = true;
+        s.len = 0;
+    }
+    s.had = s.len - s.count;
+    return s;
+}
+
+// Pages that the rows of block rb may see (its last row sees most).
+__device__ inline int block_pages(const KvAttend &a, const Seq &s, int rb) {
+    const int rows = s.count * (int)a.group;
+    int last = (rb + 1) * (int)a.rows;
+    last = (last < rows ? last : rows) - 1;
+    const int see = s.had + last / (int)a.group + 1;
+    return see > 0 ? (see + kKvPage - 1) / kKvPage : 0;
+}
+
+template <int D, int CODES, int DTYPE, int R>
+__global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
+    constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 16 * R, kJoin = 4;
+    __shared__ f32x4 sm_o[kWaves][R * kJoin * 64];
+    __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
+    const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
+    const uint32_t h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
+    const int n = lane % 16, g = lane / 16, G = (int)a.group;
+    bool bad;
+    const Seq s = sequence(a, b, &bad);
+    if (bad && a.c.n_invalid && blockIdx.x == 0 && h == 0 && tid == 0) atomicAdd(a.c.n_invalid, 1ull);
+    const int rows = s.count * G;
+    if (rb * kRows >= rows) return;
+    const int pages = block_pages(a, s, rb);
+    const int per = (int)a.per_split;
+    const int active = pages > per ? (pages + per - 1) / per : 1;
+    if (split >= active) return;
+    const int p_lo = split * per, p_hi = p_lo + per < pages ? p_lo + per : pages;
+    const bool counts = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows && lane == 0;
+
+    // queries, and how many tokens each row sees
+    u32x4 q[R][kSteps];
+    int lim[R];
+    const int see_least = s.had + rb * kRows / G + 1;  // of the block's first row
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        const int r = rb * kRows + rt * 16 + n;
+        const bool real = r < rows;
+        const int t = real ? r / G : 0, hg = real ? r % G : 0;
+        lim[rt] = real ? s.had + t + 1 : 0;
+        const uint16_t *p = a.q + (int64_t)(s.first + t) * a.q_row + (int64_t)(h * G + hg) * a.q_head;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            q[rt][st] = u32x4{0, 0, 0, 0};
+            if (real) q[rt][st] = load_q8(p + dim_of<D>(st, g), a.vec_q);
+        }
+    }
+    f32x4 o[R][kTiles];
+    float m[R], l[R];
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        m[rt] = KV_NEG_INF;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt) o[rt][dt] = f32x4{0, 0, 0, 0};
+    }
+
+    uint32_t kraw[4][D / 16];
+    u32x4 vraw[kTiles];
+    auto load_values = [&](const uint8_t *strip) {
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt)
+            vraw[dt] = *reinterpret_cast<const u32x4 *>(strip + kKvPage * D + (dt * 16 + n) * kKvPage + g * 16);
+    };
+    auto strip_of = [&](const uint8_t *page) { return page + (uint64_t)h * 2 * kKvPage * D; };
+    int p = p_lo + wave;
+    uint8_t *page = p < p_hi ? wave_uniform(page_at(a.c, b, p)) : nullptr;
+    if (page) load_keys<D>(strip_of(page), lane, kraw);
+    for (; p < p_hi; p += kWaves) {
+        uint8_t *next = p + kWaves < p_hi ? wave_uniform(page_at(a.c, b, p + kWaves)) : nullptr;
+        if (!page) {
+            if (counts) atomicAdd(a.c.n_invalid, 1ull);
+            page = next;
+            if (page) load_keys<D>(strip_of(page), lane, kraw);
+            continue;
+        }
+        const float *sc = page_scales(a.c, page, h);
+        const float f = a.scale * kLog2e * sc[0];
+        int ei = exp_of_pow2(sc[1]);
+        ei = ei < -100 ? -100 : ei;
+        const float ev = (float)ei, un = pow2(-ei);
+        load_values(strip_of(page));
+        f32x4 w[R][4];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+            for (int rt = 0; rt < R; ++rt) w[rt][tt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                const u32x4 kk = widen8<CODES, DTYPE>(kraw[tt][2 * st], kraw[tt][2 * st + 1]);
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) w[rt][tt] = mfma16<DTYPE>(kk, q[rt][st], w[rt][tt]);
+            }
+        }
+        if (next) load_keys<D>(strip_of(next), lane, kraw);
+        const int base = p * kKvPage;
+        const bool edge = base + kKvPage > see_least;
+        u32x4 pw[R][2];
+#pragma unroll
+        for (int rt = 0; rt < R; ++rt) {
+            float top = KV_NEG_INF;
+            const int see = lim[rt] - base - g * 16;
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float t = __builtin_fmaf(w[rt][tt][i], f, ev);
+                    if (edge && tt * 4 + i >= see) t = KV_NEG_INF;
+                    w[rt][tt][i] = t;
+                    top = fmaxf(top, t);
+                }
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float mn = fmaxf(m[rt], top - kLift), ms = mn == KV_NEG_INF ? 0.0f : mn;
+            const float fade = __builtin_amdgcn_exp2f(m[rt] - ms);
+            m[rt] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[rt][tt][i] = __builtin_amdgcn_exp2f(w[rt][tt][i] - ms);
+                    sum += w[rt][tt][i];
+                }
+                pw[rt][tt / 2][tt % 2 * 2] = pack2<kFp16>(w[rt][tt][0], w[rt][tt][1]);
+                pw[rt][tt / 2][tt % 2 * 2 + 1] = pack2<kFp16>(w[rt][tt][2], w[rt][tt][3]);
+            }
+            l[rt] = l[rt] * fade + sum * un;
+            if (__builtin_amdgcn_ballot_w64(fade != 1.0f)) {
+#pragma unroll
+                for (int dt = 0; dt < kTiles; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[rt][dt][i] *= fade;
+            }
+        }
+        if (base + kKvPage > s.len) {  // places behind the last token may hold no numbers
+            const int there = s.len - base - g * 16;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int k = there - 4 * x;
+                const uint32_t mask = k >= 4 ? ~0u : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+#pragma unroll
+                for (int dt = 0; dt < kTiles; ++dt) vraw[dt][x] &= mask;
+            }
+        }
+        if constexpr (CODES == kE4m3) {
+            // a value that is no number must not reach rows that do not see
+            // its token (their weight is 0, and 0 x NaN is NaN)
+            uint32_t any = 0;
+            if (edge) {
+#pragma unroll
+                for (int dt = 0; dt < kTiles; ++dt)
+                    any |= nan_codes(vraw[dt][0]) | nan_codes(vraw[dt][1]) | nan_codes(vraw[dt][2]) |
+                           nan_codes(vraw[dt][3]);
+            }
+            if (__builtin_amdgcn_ballot_w64(any != 0)) {
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) {
+                    // whether the row sees each token, x whether its value is NaN
+                    const int see = lim[rt] - base - g * 16;
+                    u32x4 sees[2];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sees[i / 4][i % 4] = (2 * i < see ? 0x3C00u : 0u) | (2 * i + 1 < see ? 0x3C000000u : 0u);
+#pragma unroll
+                    for (int dt = 0; dt < kTiles; ++dt) {
+                        uint32_t one[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) one[x] = (nan_codes(vraw[dt][x]) >> 7) * 0x38u;
+                        f32x4 hit = {0, 0, 0, 0};
+                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[0], one[1]), sees[0], hit);
+                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[2], one[3]), sees[1], hit);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (hit[i] > 0.0f) o[rt][dt][i] = __builtin_nanf("");
+                    }
+                }
+#pragma unroll
+                for (int dt = 0; dt < kTiles; ++dt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) vraw[dt][x] &= ~((nan_codes(vraw[dt][x]) >> 7) * 255u);
+            }
+        }
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt) {
+            const u32x4 v0 = widen8<CODES, kFp16>(vraw[dt][0], vraw[dt][1]);
+            const u32x4 v1 = widen8<CODES, kFp16>(vraw[dt][2], vraw[dt][3]);
+#pragma unroll
+            for (int rt = 0; rt < R; ++rt) {
+                o[rt][dt] = mfma16<kFp16>(v0, pw[rt][0], o[rt][dt]);
+                o[rt][dt] = mfma16<kFp16>(v1, pw[rt][1], o[rt][dt]);
+            }
+        }
+        page = next;
+    }
+
+    // join the four waves
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        float sum = l[rt];
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (g == 0) {
+            sm_m[wave][rt * 16 + n] = m[rt];
+            sm_l[wave][rt * 16 + n] = sum;
+        }
+    }
+    __syncthreads();
+    const uint64_t heads = (uint64_t)a.c.heads * G, all = a.tokens * heads;
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        const int x = rt * 16 + n;
+        float top = fmaxf(fmaxf(sm_m[0][x], sm_m[1][x]), fmaxf(sm_m[2][x], sm_m[3][x]));
+        if (top == KV_NEG_INF) top = 0.0f;
+        const float fade = __builtin_amdgcn_exp2f(m[rt] - top);
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[rt][dt][i] *= fade;
+    }
+    for (int d0 = 0; d0 < kTiles; d0 += kJoin) {
+        if (d0) __syncthreads();
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt) {
+            if (dt >= d0 && dt < d0 + kJoin) {
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) sm_o[wave][(rt * kJoin + dt - d0) * 64 + lane] = o[rt][dt];
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < R * kJoin * 64; e += kThreads) {
+            const int rt = e / (kJoin * 64), dt = d0 + e / 64 % kJoin;
+            const int x = rt * 16 + n, r = rb * kRows + x;
+            if (r >= rows || dt >= kTiles) continue;
+            float mm[kWaves], top = KV_NEG_INF, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) top = fmaxf(top, mm[k] = sm_m[k][x]);
+            const float ts = top == KV_NEG_INF ? 0.0f : top;
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) sum += sm_l[k][x] * __builtin_amdgcn_exp2f(mm[k] - ts);
+            const f32x4 v = sm_o[0][e] + sm_o[1][e] + sm_o[2][e] + sm_o[3][e];
+            const uint64_t row = (s.first + r / G) * heads + (uint64_t)h * G + r % G;
+            const int d = dt * 16 + g * 4;
+            if (active == 1) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                u32x2 w;
+                w[0] = pack2<DTYPE>(v[0] * inv, v[1] * inv);
+                w[1] = pack2<DTYPE>(v[2] * inv, v[3] * inv);
+                *reinterpret_cast<u32x2 *>(a.out + row * D + d) = w;
+                if (d == 0) {
+                    const float l2 = sum == 0.0f ? KV_NEG_INF : ts + log2f(sum);
+                    if (a.lse) a.lse[row] = l2 * kLn2;
+                    if (a.lse2) a.lse2[row] = l2;
+                }
+            } else {
+                *reinterpret_cast<f32x4 *>(a.part + ((uint64_t)split * all + row) * D + d) = v;
+                if (d == 0) {
+                    float *ml = a.part + (uint64_t)a.splits * all * D + ((uint64_t)split * all + row) * 2;
+                    ml[0] = top;
+                    ml[1] = sum;
+                }
+            }
+        }
+    }
+}
+
+// Joins the parts of rows whose cache was split: one wave a row and head.
+template <int DTYPE>
+__global__ __launch_bounds__(kThreads) void k_kv_join(KvAttend a) {
+    const uint32_t b = blockIdx.y, D = a.c.dim;
+    const int lane = threadIdx.x % 64, G = (int)a.group;
+    const uint64_t heads = (uint64_t)a.c.heads * G, all = a.tokens * heads;
+    const uint64_t unit = (uint64_t)blockIdx.x * kWaves + threadIdx.x / 64;
+    const uint64_t t = unit / heads, hq = unit % heads;
+    bool bad;
+    const Seq s = sequence(a, b, &bad);
+    if (t >= (uint64_t)s.count) return;
+    const int pages = block_pages(a, s, (int)((t * G + hq % G) / a.rows));
+    const int active = (pages + (int)a.per_split - 1) / (int)a.per_split;
+    if (active <= 1) return;
+    const uint64_t row = (s.first + t) * heads + hq;
+    const float *ml = a.part + (uint64_t)a.splits * all * D + row * 2;
+    float top = KV_NEG_INF;
+    for (int k = 0; k < active; ++k) top = fmaxf(top, ml[k * all * 2]);
+    const float ts = top == KV_NEG_INF ? 0.0f : top;
+    float sum = 0.0f, v[kKvMaxDim / 64] = {};
+    for (int k = 0; k < active; ++k) {
+        const float fade = __builtin_amdgcn_exp2f(ml[k * all * 2] - ts);
+        sum += ml[k * all * 2 + 1] * fade;
+        const float *src = a.part + (k * all + row) * D;
+#pragma unroll
+        for (int i = 0; i < (int)kKvMaxDim / 64; ++i) {
+            const uint32_t d = lane + 64 * i;
+            if (d < D) v[i] += src[d] * fade;
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < (int)kKvMaxDim / 64; ++i) {
+        const uint32_t d = lane + 64 * i;
+        if (d < D) a.out[row * D + d] = (uint16_t)pack2<DTYPE>(v[i] * inv, 0.0f);
+    }
+    if (lane == 0) {
+        const float l2 = sum == 0.0f ? KV_NEG_INF : ts + log2f(sum);
+        if (a.lse) a.lse[row] = l2 * kLn2;
+        if (a.lse2) a.lse2[row] = l2;
+    }
+}
+
+// The weight every cached token receives.  It needs each row's whole sum, so
+// it makes the scores again: one workgroup a (page, head) holds the page's
+// keys and goes over all the rows that see it, the waves taking 16 rows at a
+// time in turn; sums run in one order whatever else runs.
+template <int D, int CODES, int DTYPE>
+__global__ __launch_bounds__(kThreads) void k_kv_weigh(KvAttend a) {
+    constexpr int kSteps = D / 32;
+    __shared__ float sm[kWaves][kKvPage];
+    const uint32_t h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
+    const int n = lane % 16, g = lane / 16, G = (int)a.group;
+    bool bad;
+    const Seq s = sequence(a, b, &bad);
+    const int p = blockIdx.x, base = p * kKvPage;
+    if (base >= s.len || s.count == 0) return;
+    uint8_t *page = wave_uniform(page_at(a.c, b, p));
+    if (!page) return;
+    uint32_t kraw[4][D / 16];
+    load_keys<D>(page + (uint64_t)h * 2 * kKvPage * D, lane, kraw);
+    const float f = a.scale * kLog2e * page_scales(a.c, page, h)[0];
+    u32x4 kk[4][kSteps];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+            kk[tt][st] = widen8<CODES, DTYPE>(kraw[tt][2 * st], kraw[tt][2 * st + 1]);
+    float acc[16] = {};
+    const int rows = s.count * G;
+    const int from = base > s.had ? (base - s.had) * G / 16 : 0;  // earlier rows see nothing here
+    const uint64_t heads = (uint64_t)a.c.heads * G;
+    for (int x = from + wave; x * 16 < rows; x += kWaves) {
+        const int r = x * 16 + n;
+        const bool real = r < rows;
+        const int t = real ? r / G : 0, hg = real ? r % G : 0;
+        const int see = real ? s.had + t + 1 - base - g * 16 : 0;
+        const float l2 = real ? a.lse2[(s.first + t) * heads + (uint64_t)h * G + hg] : 0.0f;
+        const uint16_t *qp = a.q + (int64_t)(s.first + t) * a.q_row + (int64_t)(h * G + hg) * a.q_head;
+        u32x4 q[kSteps];
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) q[st] = load_q8(qp + dim_of<D>(st, g), a.vec_q);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+            f32x4 w = {0, 0, 0, 0};
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) w = mfma16<DTYPE>(kk[tt][st], q[st], w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], f, -l2));
+                acc[tt * 4 + i] += tt * 4 + i < see ? e : 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float v = acc[i];
+        v += dpp_move<kDppQuadSwap1>(v);
+        v += dpp_move<kDppQuadSwap2>(v);
+        v += dpp_move<kDppRowHalfMirror>(v);
+        v += dpp_move<kDppRowMirror>(v);
+        if (n == 0) sm[wave][g * 16 + i] = v;
+    }
+    __syncthreads();
+    if (tid < kKvPage && base + tid < s.len && (uint64_t)(base + tid) < a.cap)
+        a.weight[((uint64_t)b * a.c.heads + h) * a.cap + base + tid] +=
+            sm[0][tid] + sm[1][tid] + sm[2][tid] + sm[3][tid];
+}
+
+template <int D, int CODES, int DTYPE>
+void attend_go(const KvAttend &a, hipStream_t s) {
+    const dim3 grid(a.splits * a.row_blocks, a.c.heads, a.c.batch);
+    if (a.rows == 16)
+        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1>), grid, dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2>), grid, dim3(kThreads), 0, s, a);
+    if (a.splits > 1) {
+        const uint64_t units = (uint64_t)a.max_new * a.c.heads * a.group;
+        hipLaunchKernelGGL((k_kv_join<DTYPE>), dim3((uint32_t)((units + kWaves - 1) / kWaves), a.c.batch),
+                           dim3(kThreads), 0, s, a);
+    }
+    if (a.weight)
+        hipLaunchKernelGGL((k_kv_weigh<D, CODES, DTYPE>),
+                           dim3((a.max_len + kKvPage - 1) / kKvPage, a.c.heads, a.c.batch),
+                           dim3(kThreads), 0, s, a);
+}
+
+template <int D, int CODES>
+void attend_dtype(const KvAttend &a, int dtype, hipStream_t s) {
+    if (dtype == kBf16)
+        attend_go<D, CODES, kBf16>(a, s);
+    else
+        attend_go<D, CODES, kFp16>(a, s);
+}
+
+template <int D>
+void attend_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
+    if (codes == kE4m3)
+        attend_dtype<D, kE4m3>(a, dtype, s);
+    else
+        attend_dtype<D, kInt8>(a, dtype, s);
+}
+
+}  // namespace
+
+KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
+    KvAttendPlan p{};
+    const uint64_t rows = (uint64_t)max_new * group;
+    p.rows = rows <= 16 ? 16 : 32;
+    p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
+    const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
+    const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
+    // enough workgroups for 4 on each of 256 compute units, and a page for
+    // each of a workgroup's waves
+    uint64_t splits = units ? (1024 + units - 1) / units : 1;
+    uint64_t per = splits ? (pages + splits - 1) / splits : pages;
+    if (per < kWaves) per = kWaves;
+    p.per_split = (uint32_t)per;
+    p.splits = (uint32_t)((pages + per - 1) / per);
+    if (p.splits < 1) p.splits = 1;
+    const uint64_t all = tokens * heads * group;
+    p.part_bytes = p.splits > 1 ? (p.splits * all * (dim + 2) * 4 + 255) / 256 * 256 : 0;
+    p.lse_bytes = scored ? (all * 4 + 255) / 256 * 256 : 0;
+    p.total = p.part_bytes + p.score_bytes + p.lse_bytes;
+    return p;
+}
+
+hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s) {
+    switch (a.c.dim) {
+        case 64: attend_codes<64>(a, codes, dtype, s); break;
+        case 96: attend_codes<96>(a, codes, dtype, s); break;
+        case 128: attend_codes<128>(a, codes, dtype, s); break;
+        case 192: attend_codes<192>(a, codes, dtype, s); break;
+        case 256: attend_codes<256>(a, codes, dtype, s); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ac

@@ -1,0 +1,152 @@
+// kv_device.h -- number formats and page access of the 8-bit cache's kernels.
+#ifndef ARENA_COMPACTION_KV_DEVICE_H
+#define ARENA_COMPACTION_KV_DEVICE_H
+#include "kv.h"
+#include "wave.h"
+
+namespace ac {
+namespace {
+
+constexpr int kE4m3 = 0, kInt8 = 1;
+constexpr int kBf16 = 0, kFp16 = 1;
+
+using half8 = __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16;
+using half4 = __attribute__((__vector_size__(4 * sizeof(_Float16)))) _Float16;
+using half2v = __attribute__((__vector_size__(2 * sizeof(_Float16)))) _Float16;
+using bf8 = __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16;
+using bf2 = __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16;
+using f32x4 = __attribute__((__vector_size__(16))) float;
+using f32x2 = __attribute__((__vector_size__(8))) float;
+using f32x16 = __attribute__((__vector_size__(64))) float;
+using u32x4 = __attribute__((__vector_size__(16))) uint32_t;
+using u32x2 = __attribute__((__vector_size__(8))) uint32_t;
+
+template <int DTYPE>
+__device__ inline float to_float(uint16_t x) {
+    if constexpr (DTYPE == kBf16) {
+        return __builtin_bit_cast(float, (uint32_t)x << 16);
+    } else {
+        return (float)__builtin_bit_cast(_Float16, x);
+    }
+}
+
+// to nearest, ties to even: half a step (bf16 2^-8, fp16 2^-11) is the only
+// rounding between the 32-bit result and the output
+template <int DTYPE>
+__device__ inline uint32_t pack2(float a, float b) {
+    const f32x2 v = {a, b};
+    if constexpr (DTYPE == kBf16) {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
+    } else {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2v));
+    }
+}
+
+__device__ inline float pow2(int e) {  // normal range only
+    return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
+
+__device__ inline int exp_of_pow2(float s) {
+    return (int)((__builtin_bit_cast(uint32_t, s) >> 23) & 255u) - 127;
+}
+
+// Least e with amax <= largest code * 2^e (448 = 1.75 * 2^8, 127 =
+// 1.984375 * 2^6), at least kKvExpMin; amax is finite and not negative.
+template <int CODES>
+__device__ inline int scale_exp(float amax) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+    const int k = CODES == kE4m3 ? 8 : 6;
+    const uint32_t top = CODES == kE4m3 ? 0x600000u : 0x7E0000u;
+    const int e = (int)(b >> 23) - 127 - k + ((b & 0x7FFFFFu) > top ? 1 : 0);
+    return e < kKvExpMin ? kKvExpMin : e;
+}
+
+// |x|, 0 for what is not finite (it takes no part in choosing a scale).
+__device__ inline float finite_abs(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? __builtin_bit_cast(float, b) : 0.0f;
+}
+
+// A code's value.
+template <int CODES, int BYTE>
+__device__ inline float code_value(uint32_t w) {
+    if constexpr (CODES == kE4m3) {
+        return __builtin_amdgcn_cvt_f32_fp8((int)w, BYTE);
+    } else {
+        return (float)(int8_t)(w >> (8 * BYTE));
+    }
+}
+
+// Four values in units of their scale to the nearest codes (ties to even),
+// what lies outside to the largest code.  A NaN stays one in e4m3 and is 0
+// in int8.
+template <int CODES>
+__device__ inline uint32_t to_codes4(float a, float b, float c, float d) {
+    if constexpr (CODES == kE4m3) {
+        auto lim = [](float x) {
+            const float y = __builtin_amdgcn_fmed3f(x, -448.0f, 448.0f);
+            return x != x ? x : y;
+        };
+        int r = __builtin_amdgcn_cvt_pk_fp8_f32(lim(a), lim(b), 0, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(lim(c), lim(d), r, true);
+        return (uint32_t)r;
+    } else {
+        auto q = [](float x) {
+            const float y = __builtin_rintf(__builtin_amdgcn_fmed3f(x, -127.0f, 127.0f));
+            return (uint32_t)(x != x ? 0 : (int)y) & 255u;
+        };
+        return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+    }
+}
+
+// Four codes times 2^shift, as codes again.
+template <int CODES>
+__device__ inline uint32_t requant4(uint32_t w, float f) {
+    return to_codes4<CODES>(code_value<CODES, 0>(w) * f, code_value<CODES, 1>(w) * f,
+                            code_value<CODES, 2>(w) * f, code_value<CODES, 3>(w) * f);
+}
+
+// The first byte of a page, or null where the table's entry is none: outside
+// the arena, or not on the arena's 32-byte grid.
+__device__ inline uint8_t *page_at(const KvCache &c, uint32_t b, uint64_t j) {
+    const int64_t off = c.pages[(uint64_t)b * c.stride + j];
+    const uint64_t need = kv_page_bytes(c.heads, c.dim);
+    if (off < 0 || (off & 31) || need > c.arena_bytes || (uint64_t)off > c.arena_bytes - need)
+        return nullptr;
+    return c.arena + off;
+}
+
+__device__ inline float *page_scales(const KvCache &c, uint8_t *page, uint32_t h) {
+    return reinterpret_cast<float *>(page + (uint64_t)c.heads * 2 * kKvPage * c.dim) + 2 * h;
+}
+
+// First token and number of new tokens of sequence b; none where `starts`
+// does not ascend inside [0, tokens] or brings more than max_new.
+__device__ inline void new_tokens(const int32_t *starts, uint64_t tokens, uint32_t max_new,
+                                  uint32_t b, uint64_t *first, int *count, bool *bad) {
+    if (!starts) {
+        *first = b;
+        *count = 1;
+        *bad = false;
+        return;
+    }
+    const int64_t s = starts[b], e = starts[b + 1];
+    *bad = s < 0 || e < s || (uint64_t)e > tokens || e - s > (int64_t)max_new;
+    *first = *bad ? 0 : (uint64_t)s;
+    *count = *bad ? 0 : (int)(e - s);
+}
+
+// The top bit of each of four e4m3 codes that is a NaN (0x7F or 0xFF).
+__device__ inline uint32_t nan_codes(uint32_t w) {
+    return ~(((w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;
+}
+
+// Largest of the wave's values (each at least 0), in every lane.
+__device__ inline float wave_max0(float x) {
+    return wave_reduce(x, [](float a, float b) { return fmaxf(a, b); });
+}
+
+}  // namespace
+}  // namespace ac
+
+#endif

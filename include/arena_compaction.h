@@ -478,6 +478,144 @@ typedef struct defrag_monitor_report {
 int defrag_monitor(const defrag_stats_t *stats, const defrag_monitor_cfg *cfg,
                    defrag_monitor_report *out);
 
+/* ---- The 8-bit key/value cache ------------------------------------------
+ *
+ * A cache page is one block of the arena (so a compaction moves it, and
+ * defrag_remap turns the page table's offsets into the new ones): 64 tokens
+ * of every head, keys and values in 8 bits.
+ *   page   : for each head h a strip of 2 * 64 * dim bytes -- 64 x dim key
+ *            codes, token by token, then dim x 64 value codes, dimension by
+ *            dimension -- and behind the strips heads pairs of float32 scales
+ *            (key, value).  defrag_kv_page_bytes gives its size, rounded up
+ *            to the table's 32 bytes.
+ *   scale  : a power of two 2^e, e >= -64, one for the keys and one for the
+ *            values of each (page, head); a number is code * scale.
+ *   codes  : E4M3 (OCP, largest 448, no infinity) or INT8 (-127 .. 127).
+ *   table  : pages_dev[b * page_stride + j] is the byte offset in the arena
+ *            of the page with tokens 64 j .. 64 j + 63 of sequence b.
+ * An entry that is negative, not a multiple of 32, or whose page would end
+ * behind the arena is no page: its tokens are passed over (append and attend)
+ * or its sequence is left alone (evict), and it is counted in *n_invalid_dev.
+ * A sequence whose length, or whose range in starts_dev, is out of range
+ * counts as one, and holds (or brings) no tokens; evict leaves it alone.
+ *
+ * All three calls run on the caller's stream and return at once; they
+ * allocate nothing, create no stream and may be captured into a graph.  A
+ * page that append or evict writes belongs to one sequence; pages that are
+ * only read may be shared.  Outputs may not overlap inputs.  Every argument
+ * is checked on the host before the first launch (DEFRAG_EINVAL,
+ * DEFRAG_EWORKSPACE).
+ */
+#define DEFRAG_KV_PAGE_TOKENS 64
+#define DEFRAG_KV_E4M3 0
+#define DEFRAG_KV_INT8 1
+#define DEFRAG_KV_BF16 0
+#define DEFRAG_KV_FP16 1
+
+typedef struct defrag_kv_cache {
+    void *arena_dev;          /* 32-byte aligned                              */
+    uint64_t arena_bytes;
+    const int64_t *pages_dev; /* batch x page_stride byte offsets             */
+    uint64_t page_stride;     /* at most 2^23                                 */
+    const int32_t *lens_dev;  /* batch: tokens of each sequence               */
+    uint32_t batch;           /* at most 65535                                */
+    uint32_t heads;           /* key/value heads                              */
+    uint32_t dim;             /* 64, 96, 128, 192 or 256                      */
+    int32_t codes;            /* DEFRAG_KV_E4M3 or DEFRAG_KV_INT8             */
+    uint64_t *n_invalid_dev;  /* NULL, or set to the number of bad entries    */
+} defrag_kv_cache;
+
+/* Bytes of a page; 0 for sizes that are not supported. */
+size_t defrag_kv_page_bytes(uint32_t heads, uint32_t dim);
+
+/* Quantises new tokens into the pages.  lens_dev holds the lengths before the
+ * call and is not changed.  Sequence b brings the tokens starts_dev[b] ..
+ * starts_dev[b + 1] - 1, at most max_new of them (starts_dev NULL: one token
+ * a sequence, token b).  For the keys and the values of each (page, head)
+ * touched, e is the least exponent that holds the new finite numbers, and at
+ * least the page's own where it holds older tokens, whose codes are brought
+ * to the new scale; numbers become the nearest code, ties to even, and what
+ * lies outside becomes the largest.  A NaN stays one in E4M3 and becomes 0 in
+ * INT8.  Where given, weight_dev and pos_dev (batch x heads x weight_stride)
+ * get 0 and the token's position first_pos_dev[b] + its number (first_pos_dev
+ * NULL: its place) at the token's place, where that is below weight_stride. */
+typedef struct defrag_kv_append_args {
+    const defrag_kv_cache *cache;
+    const void *k_dev, *v_dev;       /* tokens x heads x dim, 16-bit         */
+    int64_t k_row, k_head;           /* strides in elements; the last is 1   */
+    int64_t v_row, v_head;
+    int32_t dtype;                   /* DEFRAG_KV_BF16 or DEFRAG_KV_FP16     */
+    uint32_t max_new;                /* at most tokens                       */
+    uint64_t tokens;
+    const int32_t *starts_dev;       /* batch + 1, or NULL                   */
+    float *weight_dev;               /* NULL, or to be cleared               */
+    int32_t *pos_dev;                /* NULL, or to be filled                */
+    const int32_t *first_pos_dev;    /* batch, or NULL                       */
+    uint64_t weight_stride;
+} defrag_kv_append_args;
+
+int defrag_kv_append(const defrag_kv_append_args *args, hipStream_t stream);
+
+/* Softmax attention of the newest tokens' queries over the cache.  lens_dev
+ * counts the new tokens too (append first).  New token t of a sequence with n
+ * of them sees the places 0 .. len - n + t.  Query head i reads key/value
+ * head i / group.  out = softmax(scale * q k^T) v; lse_dev gets the natural
+ * logarithm of the softmax's sum; a row that sees nothing gives 0 and
+ * -infinity.  weight_dev (batch x heads x weight_stride), where given, is
+ * increased by the weight that each cached token receives from all rows of
+ * its head's group.  Sums are 32-bit and run in a fixed order. */
+typedef struct defrag_kv_attend_args {
+    const defrag_kv_cache *cache;
+    const void *q_dev;               /* tokens x heads * group x dim         */
+    int64_t q_row, q_head;           /* strides in elements; the last is 1   */
+    int32_t dtype;                   /* of q and out                         */
+    uint32_t group;                  /* query heads a key/value head, <= 256 */
+    uint64_t tokens;
+    const int32_t *starts_dev;       /* batch + 1, or NULL                   */
+    uint32_t max_new;                /* at most tokens                       */
+    uint32_t max_len;                /* no length exceeds it                 */
+    float scale;
+    uint32_t reserved;
+    void *out_dev;                   /* tokens x heads * group x dim, packed */
+    float *lse_dev;                  /* tokens x heads * group, or NULL      */
+    float *weight_dev;               /* or NULL                              */
+    uint64_t weight_stride;          /* at least max_len                     */
+} defrag_kv_attend_args;
+
+/* Bytes of workspace (256-byte aligned) that defrag_kv_attend needs (at
+ * least 256); 0 for arguments that it refuses. */
+size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *args);
+int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_bytes,
+                     hipStream_t stream);
+
+/* Keeps `budget` tokens of every (sequence, head) that holds more: first the
+ * safe ones, whose position is below sink or at least next_pos - recent, then
+ * those of largest weight (equal ones from the lowest place, NaN as
+ * +infinity).  Kept tokens in places below budget stay there; the others
+ * move, in order, into the places that became free.  A page of the first
+ * budget / 64 whose tokens changed gets a new scale and new codes; the pages
+ * behind them are free afterwards.  weight_out_dev, pos_out_dev and
+ * lens_out_dev describe the result (places behind lens_out are not written);
+ * a sequence of at most budget tokens is copied there as it is. */
+typedef struct defrag_kv_evict_args {
+    const defrag_kv_cache *cache;
+    uint32_t budget;                 /* a multiple of 64, not 0              */
+    uint32_t max_len;                /* no length exceeds it                 */
+    int32_t sink, recent;            /* recent is not negative               */
+    const int32_t *next_pos_dev;     /* batch: position of the next token    */
+    const float *weight_dev;         /* batch x heads x weight_stride        */
+    const int32_t *pos_dev;
+    uint64_t weight_stride;          /* at least max_len                     */
+    float *weight_out_dev;           /* batch x heads x weight_out_stride    */
+    int32_t *pos_out_dev;
+    uint64_t weight_out_stride;      /* at least min(budget, max_len)        */
+    int32_t *lens_out_dev;           /* batch                                */
+} defrag_kv_evict_args;
+
+size_t defrag_kv_evict_workspace_bytes(const defrag_kv_evict_args *args);
+int defrag_kv_evict(const defrag_kv_evict_args *args, void *ws_dev, size_t ws_bytes,
+                    hipStream_t stream);
+
 /* Short text for a return code. */
 const char *defrag_strerror(int code);
 
