@@ -1,9 +1,11 @@
 """Build libarena_compaction.so (gfx950) in-tree with hipcc."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -47,11 +49,20 @@ def run_hipcc(cmd) -> None:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    cmd = [hipcc()] + HIPCC_FLAGS + list(extra_flags) + \
-        [os.path.join(CSRC, s) for s in SOURCES] + ["-o", LIB_PATH + ".tmp"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    run_hipcc(cmd)
+    """Each source to an object, several at a time, then one link."""
+    flags = [hipcc()] + HIPCC_FLAGS + list(extra_flags)
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        compiles = [[f for f in flags if f != "-shared"] + ["-c", os.path.join(CSRC, s), "-o", o]
+                    for s, o in zip(SOURCES, objects)]
+        link = [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared"] + objects + ["-o", LIB_PATH + ".tmp"]
+        if verbose:
+            for cmd in compiles + [link]:
+                print(" ".join(cmd), flush=True)
+        jobs = min(8, os.cpu_count() or 1, int(os.environ.get("MAX_JOBS") or 8))
+        with concurrent.futures.ThreadPoolExecutor(max(1, jobs)) as pool:
+            list(pool.map(run_hipcc, compiles))
+        run_hipcc(link)
     os.replace(LIB_PATH + ".tmp", LIB_PATH)
     return LIB_PATH
 

@@ -87,13 +87,20 @@ struct KvEvict {
     int32_t *pos_out;
     uint64_t cap_out;
     int32_t *lens_out;
-    int32_t *src;         // workspace: two lists [batch][heads][budget]
+    // workspace (kv_evict_plan)
+    int32_t *src;    // [batch][heads][budget]: a kept place, or ~(number of the hole)
+    int32_t *moved;  // [batch][heads][budget]: place of the token for each hole
+    int32_t *fold;   // [batch][heads]: whether anything may move
+    uint8_t *rest;   // histograms of long rows
+    uint32_t piece, pieces;
 };
 
-// Bytes of the two lists of an eviction.
-inline uint64_t kv_evict_ws(uint32_t batch, uint32_t heads, uint32_t budget) {
-    return (uint64_t)batch * heads * budget * 8;
-}
+struct KvEvictPlan {
+    uint64_t list_bytes, fold_bytes, rest_bytes, total;
+    uint32_t piece, pieces;
+};
+
+KvEvictPlan kv_evict_plan(uint32_t batch, uint32_t heads, uint32_t budget, uint32_t max_len);
 
 struct KvAttendPlan {
     uint32_t rows, row_blocks, splits, per_split;

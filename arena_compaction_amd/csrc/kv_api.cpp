@@ -11,6 +11,7 @@ namespace {
 // lanes, 2^24 workgroups of 256, and each covers a page.
 constexpr uint64_t kMaxTokens = 1u << 29;
 constexpr uint64_t kMaxGrid = (1u << 24) - 1;
+constexpr uint64_t kMaxEvict = 1u << 25;  // tokens of an evicted sequence
 constexpr uint64_t kLeastWs = 256;  // so that 0 can mean "refused"
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -81,7 +82,7 @@ int check_evict(const defrag_kv_evict_args *a) {
     const int rc = check_cache(a->cache);
     if (rc) return rc;
     const defrag_kv_cache *c = a->cache;
-    if (a->budget == 0 || a->budget % kKvPage || a->budget > kMaxTokens)
+    if (a->budget == 0 || a->budget % kKvPage || a->budget > kMaxEvict || a->max_len > kMaxEvict)
         return DEFRAG_EINVAL;
     if (a->max_len > c->page_stride * kKvPage ||
         a->max_len > a->weight_stride || a->recent < 0)
@@ -190,7 +191,7 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
 
 size_t defrag_kv_evict_workspace_bytes(const defrag_kv_evict_args *a) {
     if (check_evict(a)) return 0;
-    const uint64_t need = kv_evict_ws(a->cache->batch, a->cache->heads, a->budget);
+    const uint64_t need = kv_evict_plan(a->cache->batch, a->cache->heads, a->budget, a->max_len).total;
     return need > kLeastWs ? need : kLeastWs;
 }
 
@@ -199,13 +200,32 @@ int defrag_kv_evict(const defrag_kv_evict_args *a, void *ws_dev, size_t ws_bytes
     int rc = check_evict(a);
     if (rc) return rc;
     const defrag_kv_cache *c = a->cache;
-    rc = check_ws(ws_dev, ws_bytes, kv_evict_ws(c->batch, c->heads, a->budget));
+    const KvEvictPlan p = kv_evict_plan(c->batch, c->heads, a->budget, a->max_len);
+    rc = check_ws(ws_dev, ws_bytes, p.total);
     if (rc) return rc;
     rc = clear_count(c, stream);
     if (rc || !c->batch) return rc;
-    const KvEvict k{cache_of(c), a->budget, a->max_len, a->sink, a->recent, a->next_pos_dev,
-                    a->weight_dev, a->pos_dev, a->weight_stride, a->weight_out_dev, a->pos_out_dev,
-                    a->weight_out_stride, a->lens_out_dev, static_cast<int32_t *>(ws_dev)};
+    uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+    KvEvict k{};
+    k.c = cache_of(c);
+    k.budget = a->budget;
+    k.max_len = a->max_len;
+    k.sink = a->sink;
+    k.recent = a->recent;
+    k.next_pos = a->next_pos_dev;
+    k.weight = a->weight_dev;
+    k.pos = a->pos_dev;
+    k.cap = a->weight_stride;
+    k.weight_out = a->weight_out_dev;
+    k.pos_out = a->pos_out_dev;
+    k.cap_out = a->weight_out_stride;
+    k.lens_out = a->lens_out_dev;
+    k.src = reinterpret_cast<int32_t *>(ws);
+    k.moved = reinterpret_cast<int32_t *>(ws + p.list_bytes);
+    k.fold = reinterpret_cast<int32_t *>(ws + 2 * p.list_bytes);
+    k.rest = ws + 2 * p.list_bytes + p.fold_bytes;
+    k.piece = p.piece;
+    k.pieces = p.pieces;
     return launch_kv_evict(k, c->codes, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
 }
 

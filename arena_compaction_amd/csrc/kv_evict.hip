@@ -6,14 +6,23 @@
 // places stay where they are; the places of dropped ones (holes) take the
 // kept tokens behind the budget, both in ascending order.
 //
-//   k_kv_select  one workgroup a (sequence, head): a radix select of the
-//                budget-th key, then two ordered sweeps that turn flags into
-//                the list src[place] by prefix sums;
-//   k_kv_fold    one workgroup a (page, head): gathers the page's 64 tokens
-//                by that list, finds the new scale and writes new codes.
-//                Pages without a hole are left alone.
-// Read places lie behind the budget or in the workgroup's own strip, and
-// written ones in its own strip: no workgroup reads what another writes.
+// The order is that of a 33-bit key: the safe bit above the weight's bits,
+// turned so that they ascend.  Its budget-th largest value (the edge) is
+// found in three digits of 12, 11 and 10 bits, each by a histogram in LDS;
+// of the tokens at the edge the first few are kept.  Then prefix sums over
+// flags number the holes and the moved tokens.
+//
+//   k_kv_select  rows of up to 16384 tokens: one workgroup a (sequence,
+//                head), keys in registers, everything in one launch;
+//   k_kv_digit, k_kv_list  longer rows: a workgroup a piece of the row, a
+//                launch a digit and one for the lists.  Each piece stores its
+//                histogram and every piece adds up all of them, so no counter
+//                has to be cleared and none is shared;
+//   k_kv_fold    one workgroup a (page, head): gathers the page's 64 tokens,
+//                finds the new scale and writes new codes.  Pages without a
+//                hole are left alone.
+// Tokens that move lie behind the budget, and a workgroup writes its own
+// strip alone: none reads what another writes.
 #include "kv_device.h"
 
 namespace ac {
@@ -21,7 +30,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
-constexpr int kDigits = 256;  // bins of a radix pass
+constexpr int kBins1 = 4096, kBins2 = 2048, kBins3 = 1024;
 constexpr int kFoldThreads = 256;
 
 // Larger weight, larger key; -0 and +0 are one key, NaN that of +infinity.
@@ -34,12 +43,22 @@ __device__ inline uint32_t weight_key(float w) {
 struct Row {
     const float *w;
     const int32_t *pos;
-    int32_t sink;
-    int64_t border;
-    __device__ bool safe(int i) const { return pos[i] < sink || (int64_t)pos[i] >= border; }
+    int64_t sink, border;
+    __device__ bool safe(int i) const { return pos[i] < sink || pos[i] >= border; }
 };
 
-// Exclusive prefix of x over the workgroup, and the total.
+__device__ inline Row row_of(const KvEvict &a, uint32_t h, uint32_t b) {
+    const uint64_t at = ((uint64_t)b * a.c.heads + h) * a.cap;
+    return Row{a.weight + at, a.pos + at, a.sink, (int64_t)a.next_pos[b] - a.recent};
+}
+
+// Tokens of a sequence; -1 where its length is out of range.
+__device__ inline int evict_len(const KvEvict &a, uint32_t b) {
+    const int64_t n = a.c.lens[b];
+    return n < 0 || n > (int64_t)a.max_len ? -1 : (int)n;
+}
+
+// Exclusive prefix of x over the workgroup and the total (two barriers).
 __device__ inline int block_scan(int x, int *red, int *total) {
     const int incl = wave_incl_scan(x, [](int p, int q) { return p + q; });
     __syncthreads();
@@ -56,139 +75,476 @@ __device__ inline int block_scan(int x, int *red, int *total) {
     return before + incl - x;
 }
 
-// The tokens of a sequence that take part; -1 where its length or a page is
-// out of range (nothing of the sequence is touched then).
-__device__ inline int evict_len(const KvEvict &a, uint32_t b, int *bad_pages) {
-    const int64_t n = a.c.lens[b];
-    *bad_pages = 0;
-    if (n < 0 || n > (int64_t)a.max_len || n > (int64_t)a.cap) return -1;
-    return (int)n;
+// The bin that holds the need-th largest of the counted keys, and how many of
+// its own are needed.  c: this lane's counts of bins (from the top) PER * tid
+// to PER * tid + PER - 1.
+template <int PER>
+__device__ inline void find_bin(const int (&c)[PER], int need, int *red, int *out) {
+    int sum = 0, total;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) sum += c[k];
+    int before = block_scan(sum, red, &total);
+    if (before < need && need <= before + sum) {
+        bool found = false;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (!found && need <= before + c[k]) {
+                found = true;
+                out[0] = PER * kSelThreads - 1 - (PER * (int)threadIdx.x + k);
+                out[1] = need - before;
+            }
+            before += c[k];
+        }
+    }
+    __syncthreads();
 }
 
+template <int BINS>
+__device__ inline void find_in_lds(const uint32_t *hist, int need, int *red, int *out) {
+    constexpr int PER = BINS / kSelThreads;
+    int c[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) c[k] = (int)hist[BINS - 1 - (PER * (int)threadIdx.x + k)];
+    find_bin<PER>(c, need, red, out);
+}
+
+__device__ inline void clear_bins(uint32_t *hist, int n) {
+    for (int i = threadIdx.x; i < n; i += kSelThreads) hist[i] = 0;
+}
+
+// Rank among the set flags of the workgroup's tokens, in order of place, for
+// each of a lane's KPT flags; tokens lie as (wave * KPT + k) * 64 + lane.
+template <int KPT>
+__device__ inline int ordered_ranks(uint32_t flags, int (&rank)[KPT], int *red) {
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const uint64_t below = (1ull << lane) - 1;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const uint64_t m = __builtin_amdgcn_ballot_w64((flags >> k) & 1);
+        rank[k] = n + __builtin_popcountll(m & below);
+        n += __builtin_popcountll(m);
+    }
+    __syncthreads();
+    if (lane == 0) red[wave] = n;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWaves; ++w) {
+        const int v = red[w];
+        if (w < wave) before += v;
+        all += v;
+    }
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) rank[k] += before;
+    return all;
+}
+
+// What an edge decides: keep the keys above it and the first `ties` at it.
+struct Edge {
+    uint32_t safe, key;
+    int ties;
+};
+
+// The lists of one block of kSelThreads * KPT tokens from place `base` on:
+// flags of the kept ones, then the numbers of holes and moved tokens.
+// Running totals over earlier blocks go in and out.
+template <int KPT>
+__device__ inline void list_block(const KvEvict &a, uint64_t row, const Row &r, int base, int end,
+                                  const uint32_t (&key)[KPT], uint32_t safe, const Edge &edge,
+                                  int *red, int *tied, int *holes, int *moved) {
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, K = (int)a.budget;
+    uint32_t keep = 0, tie = 0, hole = 0, move = 0;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = base + (wave * KPT + k) * 64 + lane;
+        const uint32_t s = (safe >> k) & 1;
+        const bool above = s > edge.safe || (s == edge.safe && key[k] > edge.key);
+        if (i < end) {
+            keep |= (uint32_t)above << k;
+            tie |= (uint32_t)(s == edge.safe && key[k] == edge.key) << k;
+        }
+    }
+    int rank[KPT];
+    const int t = ordered_ranks<KPT>(tie, rank, red);
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+        if (((tie >> k) & 1) && *tied + rank[k] < edge.ties) keep |= 1u << k;
+    *tied += t;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = base + (wave * KPT + k) * 64 + lane;
+        if (i < end) {
+            if (i < K)
+                hole |= (~(keep >> k) & 1u) << k;
+            else
+                move |= ((keep >> k) & 1u) << k;
+        }
+    }
+    const int nh = ordered_ranks<KPT>(hole, rank, red);
+    int32_t *src = a.src + row * a.budget, *mv = a.moved + row * a.budget;
+    const uint64_t to = row * a.cap_out;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = base + (wave * KPT + k) * 64 + lane;
+        if (i < K && i < end) {
+            if ((hole >> k) & 1) {
+                src[i] = ~(*holes + rank[k]);
+            } else {
+                src[i] = i;
+                a.weight_out[to + i] = r.w[i];
+                a.pos_out[to + i] = r.pos[i];
+            }
+        }
+    }
+    *holes += nh;
+    const int nm = ordered_ranks<KPT>(move, rank, red);
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = base + (wave * KPT + k) * 64 + lane;
+        if ((move >> k) & 1) mv[*moved + rank[k]] = i;
+    }
+    *moved += nm;
+}
+
+template <int KPT>
+__device__ inline uint32_t load_keys_of(const Row &r, int base, int end, uint32_t (&key)[KPT]) {
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    uint32_t safe = 0;
+    float w[KPT];
+    int32_t p[KPT];
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        const int i = base + (wave * KPT + k) * 64 + lane;
+        w[k] = i < end ? r.w[i] : 0.0f;
+        p[k] = i < end ? r.pos[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        key[k] = weight_key(w[k]);
+        safe |= (uint32_t)(p[k] < r.sink || p[k] >= r.border) << k;
+    }
+    return safe;
+}
+
+// Copies a row that keeps everything.
+__device__ inline void copy_row(const KvEvict &a, uint64_t row, const Row &r, int from, int to, int step) {
+    for (int i = from; i < to; i += step) {
+        a.weight_out[row * a.cap_out + i] = r.w[i];
+        a.pos_out[row * a.cap_out + i] = r.pos[i];
+    }
+}
+
+template <int KPT>
 __global__ __launch_bounds__(kSelThreads) void k_kv_select(KvEvict a) {
-    __shared__ int red[kSelWaves];
-    __shared__ uint32_t hist[kDigits];
-    __shared__ uint32_t sh_prefix;
-    __shared__ int sh_need;
+    __shared__ int red[kSelWaves], found[2];
+    __shared__ uint32_t hist[kBins1];
     const uint32_t h = blockIdx.x, b = blockIdx.y;
-    const int tid = threadIdx.x, K = (int)a.budget;
+    const uint64_t row = (uint64_t)b * a.c.heads + h;
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, K = (int)a.budget;
+    const int n = evict_len(a, b);
     int bad_pages = 0;
-    int n = evict_len(a, b, &bad_pages);
-    int32_t *src = a.src + ((uint64_t)b * a.c.heads + h) * a.budget;
     if (n > K) {
         int bad = 0;
         for (int j = tid; j * kKvPage < n; j += kSelThreads) bad += page_at(a.c, b, j) == nullptr;
         block_scan(bad, red, &bad_pages);
     }
-    if (n < 0 || bad_pages) {  // src[0] = -1: the second kernel passes over the row
-        if (tid == 0) {
-            src[0] = -1;
-            if (h == 0 && a.c.n_invalid)
-                atomicAdd(a.c.n_invalid, (unsigned long long)(bad_pages ? bad_pages : 1));
-        }
-        return;
-    }
-    const uint64_t at = ((uint64_t)b * a.c.heads + h) * a.cap;
-    const uint64_t to = ((uint64_t)b * a.c.heads + h) * a.cap_out;
-    const Row r{a.weight + at, a.pos + at, a.sink, (int64_t)a.next_pos[b] - a.recent};
-    if (h == 0 && tid == 0) a.lens_out[b] = n < K ? n : K;
-    if (n <= K) {
-        if (tid == 0) src[0] = -1;
-        for (int i = tid; i < n; i += kSelThreads) {
-            a.weight_out[to + i] = r.w[i];
-            a.pos_out[to + i] = r.pos[i];
-        }
-        return;
-    }
-    // safe tokens: all kept if they fit, else the choice is among them alone
-    int mine = 0, safe_total;
-    for (int i = tid; i < n; i += kSelThreads) mine += r.safe(i);
-    block_scan(mine, red, &safe_total);
-    const bool among_safe = safe_total >= K;
     if (tid == 0) {
-        sh_prefix = 0;
-        sh_need = among_safe ? K : K - safe_total;
-    }
-    // the need-th largest key of the candidates, 8 bits a pass
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < kDigits; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t prefix = sh_prefix;
-        for (int i = tid; i < n; i += kSelThreads) {
-            if (r.safe(i) != among_safe) continue;
-            const uint32_t key = weight_key(r.w[i]);
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(key >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int need = sh_need, d = kDigits - 1;
-            while (d > 0 && (int)hist[d] < need) need -= (int)hist[d--];
-            sh_need = need;
-            sh_prefix = prefix | ((uint32_t)d << shift);
-        }
-        __syncthreads();
-    }
-    const uint32_t edge = sh_prefix;
-    const int ties = sh_need;  // of the tokens at the edge, the first `ties`
-    int tied = 0, holes = 0, moved = 0;
-    // holes in ascending order, beside the list they are filled in
-    int32_t *hole = a.src + (uint64_t)a.c.batch * a.c.heads * a.budget +
-                    ((uint64_t)b * a.c.heads + h) * a.budget;
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        bool in = i < n, safe = false, tie = false, keep = false;
-        if (in) {
-            safe = r.safe(i);
-            if (safe != among_safe) {
-                keep = safe;  // safe ones that fit, all; else no other
+        a.fold[row] = n > K && !bad_pages;
+        if (h == 0) {
+            if (n < 0 || bad_pages) {
+                if (a.c.n_invalid) atomicAdd(a.c.n_invalid, (unsigned long long)(bad_pages ? bad_pages : 1));
             } else {
-                const uint32_t key = weight_key(r.w[i]);
-                keep = key > edge;
-                tie = key == edge;
+                a.lens_out[b] = n < K ? n : K;
             }
         }
-        int total;
-        const int rank = block_scan(tie, red, &total);
-        if (tie) keep = tied + rank < ties;
-        tied += total;
-        const bool hl = in && i < K && !keep;
-        const int hrank = block_scan(hl, red, &total);
-        if (hl) hole[holes + hrank] = i;
-        holes += total;
-        if (in && i < K && keep) {
-            src[i] = i;
-            a.weight_out[to + i] = r.w[i];
-            a.pos_out[to + i] = r.pos[i];
-        }
-        const bool mv = in && i >= K && keep;
-        const int mrank = block_scan(mv, red, &total);  // its barriers also order hole[]
-        if (mv) {
-            const int p = hole[moved + mrank];
-            src[p] = i;
-            a.weight_out[to + p] = r.w[i];
-            a.pos_out[to + p] = r.pos[i];
-        }
-        moved += total;
+    }
+    if (n < 0 || bad_pages) return;
+    const Row r = row_of(a, h, b);
+    if (n <= K) {
+        copy_row(a, row, r, tid, n, kSelThreads);
+        return;
+    }
+    uint32_t key[KPT];
+    const uint32_t safe = load_keys_of<KPT>(r, 0, n, key);
+    clear_bins(hist, kBins1);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+        if ((wave * KPT + k) * 64 + lane < n) atomicAdd(&hist[(((safe >> k) & 1) << 11) | (key[k] >> 21)], 1u);
+    __syncthreads();
+    find_in_lds<kBins1>(hist, K, red, found);
+    const uint32_t d1 = (uint32_t)found[0];
+    int need = found[1];
+    Edge edge{d1 >> 11, (d1 & 2047u) << 21, 0};
+    clear_bins(hist, kBins2);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+        if ((wave * KPT + k) * 64 + lane < n && ((safe >> k) & 1) == edge.safe && ((key[k] ^ edge.key) >> 21) == 0)
+            atomicAdd(&hist[(key[k] >> 10) & 2047u], 1u);
+    __syncthreads();
+    find_in_lds<kBins2>(hist, need, red, found);
+    edge.key |= (uint32_t)found[0] << 10;
+    need = found[1];
+    clear_bins(hist, kBins3);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+        if ((wave * KPT + k) * 64 + lane < n && ((safe >> k) & 1) == edge.safe && ((key[k] ^ edge.key) >> 10) == 0)
+            atomicAdd(&hist[key[k] & 1023u], 1u);
+    __syncthreads();
+    find_in_lds<kBins3>(hist, need, red, found);
+    edge.key |= (uint32_t)found[0];
+    edge.ties = found[1];
+    int tied = 0, holes = 0, moved = 0;
+    list_block<KPT>(a, row, r, 0, n, key, safe, edge, red, &tied, &holes, &moved);
+}
+
+// ---- long rows, in pieces ----
+
+constexpr int kPieceKeys = 8;
+constexpr uint32_t kOneBlock = kSelThreads * 16;  // tokens k_kv_select holds
+constexpr uint32_t kMaxPieces = 1026;             // of at most 32768 tokens: counts fit 16 bits
+
+// Places [begin, end) of piece c: the first pieces cover the budget, the
+// others what lies behind it.
+__device__ inline void piece_range(const KvEvict &a, int c, int n, int *begin, int *end) {
+    const int K = (int)a.budget, front = (K + a.piece - 1) / a.piece;
+    const int64_t lo = c < front ? (int64_t)c * a.piece : K + (int64_t)(c - front) * a.piece;
+    const int64_t hi = lo + a.piece, stop = c < front ? K : n;
+    *begin = (int)(lo < stop ? lo : stop);
+    *end = (int)(hi < stop ? hi : stop);
+}
+
+// What the launches of a long row pass on.
+struct PieceState {
+    int32_t bad, above;  // pages that are none; keys above the edge so far
+};
+struct RowState {
+    int32_t d1, need1, d2, need2;
+};
+
+struct EvictWs {
+    PieceState *piece;
+    RowState *row;
+    uint16_t *h1, *h2, *h3;
+};
+
+__host__ __device__ inline EvictWs long_ws(const KvEvict &a) {
+    const uint64_t rows = (uint64_t)a.c.batch * a.c.heads, np = rows * a.pieces;
+    EvictWs w;
+    w.row = reinterpret_cast<RowState *>(a.rest);
+    w.piece = reinterpret_cast<PieceState *>(w.row + rows);
+    w.h1 = reinterpret_cast<uint16_t *>(w.piece + np);
+    w.h2 = w.h1 + np * kBins1;
+    w.h3 = w.h2 + np * kBins2;
+    return w;
+}
+
+// Adds up the pieces' counts of this lane's bins, from the top.
+template <int BINS>
+__device__ inline void sum_bins(const uint16_t *h, int pieces, int (&c)[BINS / kSelThreads]) {
+    constexpr int PER = BINS / kSelThreads;
+    const int first = BINS - PER * ((int)threadIdx.x + 1);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) c[k] = 0;
+#pragma unroll 4
+    for (int p = 0; p < pieces; ++p) {
+        uint16_t v[PER];
+        __builtin_memcpy(v, __builtin_assume_aligned(h + (uint64_t)p * BINS + first, PER * 2), PER * 2);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) c[PER - 1 - k] += v[k];
     }
 }
 
-template <int CODES>
+__device__ inline bool row_is_bad(const KvEvict &a, const EvictWs &w, uint64_t row, int *red) {
+    int bad = 0, total;
+    for (int p = threadIdx.x; p < (int)a.pieces; p += kSelThreads) bad += w.piece[row * a.pieces + p].bad;
+    block_scan(bad, red, &total);
+    return total != 0;
+}
+
+// One digit of the edge: DIGIT 1 counts the first, 2 and 3 find the digit
+// before from the pieces' counts and count the next.
+template <int DIGIT>
+__global__ __launch_bounds__(kSelThreads) void k_kv_digit(KvEvict a) {
+    __shared__ int red[kSelWaves], found[2];
+    __shared__ uint32_t hist[kBins1];
+    const uint32_t c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const uint64_t row = (uint64_t)b * a.c.heads + h, at = row * a.pieces;
+    const int tid = threadIdx.x, K = (int)a.budget;
+    const int n = evict_len(a, b);
+    if (n <= K) return;
+    const EvictWs w = long_ws(a);
+    const Row r = row_of(a, h, b);
+    int begin, end;
+    piece_range(a, (int)c, n, &begin, &end);
+    Edge edge{0, 0, 0};
+    if constexpr (DIGIT == 1) {
+        int bad = 0, total;
+        // pages that begin in the piece (pieces and the budget are whole pages)
+        for (int j = begin / kKvPage + tid; j * kKvPage < end; j += kSelThreads)
+            bad += page_at(a.c, b, j) == nullptr;
+        block_scan(bad, red, &total);
+        if (tid == 0) w.piece[at + c] = PieceState{total, 0};
+    } else {
+        if (row_is_bad(a, w, row, red)) return;
+        int above = 0;
+        if constexpr (DIGIT == 2) {
+            int v[kBins1 / kSelThreads];
+            sum_bins<kBins1>(w.h1 + at * kBins1, (int)a.pieces, v);
+            find_bin(v, K, red, found);
+            for (int i = found[0] + 1 + tid; i < kBins1; i += kSelThreads) above += w.h1[(at + c) * kBins1 + i];
+            if (c == 0 && tid == 0) {
+                w.row[row].d1 = found[0];
+                w.row[row].need1 = found[1];
+            }
+            edge.safe = (uint32_t)found[0] >> 11;
+            edge.key = ((uint32_t)found[0] & 2047u) << 21;
+        } else {
+            const RowState s = w.row[row];
+            int v[kBins2 / kSelThreads];
+            sum_bins<kBins2>(w.h2 + at * kBins2, (int)a.pieces, v);
+            find_bin(v, s.need1, red, found);
+            for (int i = found[0] + 1 + tid; i < kBins2; i += kSelThreads) above += w.h2[(at + c) * kBins2 + i];
+            if (c == 0 && tid == 0) {
+                w.row[row].d2 = found[0];
+                w.row[row].need2 = found[1];
+            }
+            edge.safe = (uint32_t)s.d1 >> 11;
+            edge.key = ((uint32_t)s.d1 & 2047u) << 21 | (uint32_t)found[0] << 10;
+        }
+        int total;
+        block_scan(above, red, &total);
+        if (tid == 0) w.piece[at + c].above += total;
+    }
+    constexpr int kBins = DIGIT == 1 ? kBins1 : DIGIT == 2 ? kBins2 : kBins3;
+    clear_bins(hist, kBins);
+    __syncthreads();
+    for (int base = begin; base < end; base += kSelThreads * kPieceKeys) {
+        uint32_t key[kPieceKeys];
+        const uint32_t safe = load_keys_of<kPieceKeys>(r, base, end, key);
+#pragma unroll
+        for (int k = 0; k < kPieceKeys; ++k) {
+            if (base + (tid / 64 * kPieceKeys + k) * 64 + tid % 64 >= end) continue;
+            const uint32_t s = (safe >> k) & 1;
+            if constexpr (DIGIT == 1) {
+                atomicAdd(&hist[(s << 11) | (key[k] >> 21)], 1u);
+            } else if constexpr (DIGIT == 2) {
+                if (s == edge.safe && ((key[k] ^ edge.key) >> 21) == 0) atomicAdd(&hist[(key[k] >> 10) & 2047u], 1u);
+            } else {
+                if (s == edge.safe && ((key[k] ^ edge.key) >> 10) == 0) atomicAdd(&hist[key[k] & 1023u], 1u);
+            }
+        }
+    }
+    __syncthreads();
+    uint16_t *out = DIGIT == 1 ? w.h1 : DIGIT == 2 ? w.h2 : w.h3;
+    uint32_t *out2 = reinterpret_cast<uint32_t *>(out + (at + c) * kBins);
+    for (int i = tid; i < kBins / 2; i += kSelThreads) out2[i] = hist[2 * i] | (hist[2 * i + 1] << 16);
+}
+
+// The last digit, then a piece's part of the lists.
+__global__ __launch_bounds__(kSelThreads) void k_kv_list(KvEvict a) {
+    __shared__ int red[kSelWaves], found[2];
+    __shared__ int kept_before[2], ties_before, above_in[kMaxPieces];
+    const uint32_t c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const uint64_t row = (uint64_t)b * a.c.heads + h, at = row * a.pieces;
+    const int tid = threadIdx.x, K = (int)a.budget;
+    const int n = evict_len(a, b);
+    const EvictWs w = long_ws(a);
+    const bool bad = n > K && row_is_bad(a, w, row, red);
+    if (c == 0) {
+        if (tid == 0) {
+            a.fold[row] = n > K && !bad;
+            if (h == 0 && n >= 0 && !bad) a.lens_out[b] = n < K ? n : K;
+        }
+        if (h == 0 && a.c.n_invalid) {
+            if (n < 0 && tid == 0) atomicAdd(a.c.n_invalid, 1ull);
+            if (bad)
+                for (int p = tid; p < (int)a.pieces; p += kSelThreads)
+                    if (w.piece[at + p].bad) atomicAdd(a.c.n_invalid, (unsigned long long)w.piece[at + p].bad);
+        }
+    }
+    if (n < 0 || bad) return;
+    const Row r = row_of(a, h, b);
+    if (n <= K) {
+        copy_row(a, row, r, (int)c * kSelThreads + tid, n, (int)a.pieces * kSelThreads);
+        return;
+    }
+    const RowState s = w.row[row];
+    int v[1];
+    sum_bins<kBins3>(w.h3 + at * kBins3, (int)a.pieces, v);
+    find_bin(v, s.need2, red, found);
+    const int d3 = found[0];
+    const Edge edge{(uint32_t)s.d1 >> 11, ((uint32_t)s.d1 & 2047u) << 21 | (uint32_t)s.d2 << 10 | (uint32_t)d3, found[1]};
+    // what earlier pieces keep: keys above the edge, and of the ties the
+    // first; `front` pieces give holes, the others moved tokens
+    const int front = (K + a.piece - 1) / a.piece;
+    for (int p = tid / 64; p < (int)c; p += kSelWaves) {
+        int above = 0;
+        for (int i = d3 + 1 + tid % 64; i < kBins3; i += 64) above += w.h3[(at + p) * kBins3 + i];
+        above = wave_reduce(above, [](int x, int y) { return x + y; });
+        if (tid % 64 == 0) above_in[p] = w.piece[at + p].above + above;
+    }
+    __syncthreads();
+    if (tid < 64) {
+        int tied = 0, kept[2] = {0, 0};
+        // one wave, a piece a lane; ties in order through a prefix
+        for (int p0 = 0; p0 < (int)c; p0 += 64) {
+            const int p = p0 + tid;
+            int above = 0, ties = 0;
+            if (p < (int)c) {
+                above = above_in[p];
+                ties = w.h3[(at + p) * kBins3 + d3];
+            }
+            const int incl = wave_incl_scan(ties, [](int x, int y) { return x + y; });
+            const int before = tied + incl - ties, left = edge.ties > before ? edge.ties - before : 0;
+            const int k = p < (int)c ? above + (ties < left ? ties : left) : 0;
+            kept[0] += wave_reduce(p < front ? k : 0, [](int x, int y) { return x + y; });
+            kept[1] += wave_reduce(p >= front ? k : 0, [](int x, int y) { return x + y; });
+            tied += read_lane<63>(incl);
+        }
+        if (tid == 0) {
+            ties_before = tied;
+            kept_before[0] = kept[0];
+            kept_before[1] = kept[1];
+        }
+    }
+    __syncthreads();
+    int begin, end, tied = ties_before;
+    piece_range(a, (int)c, n, &begin, &end);
+    int holes = (int)c < front ? begin - kept_before[0] : 0, moved = kept_before[1];
+    for (int base = begin; base < end; base += kSelThreads * kPieceKeys) {
+        uint32_t key[kPieceKeys];
+        const uint32_t safe = load_keys_of<kPieceKeys>(r, base, end, key);
+        list_block<kPieceKeys>(a, row, r, base, end, key, safe, edge, red, &tied, &holes, &moved);
+    }
+}
+
+template <int D, int CODES>
 __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
-    __shared__ const uint8_t *from[kKvPage];
+    __shared__ const uint8_t *from[kKvPage];  // a token's first value code
+    __shared__ int place[kKvPage];
     __shared__ float scale[2][kKvPage];
     __shared__ float red[2][kFoldThreads / 64];
     const uint32_t j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const uint64_t row = (uint64_t)b * a.c.heads + h;
     const int tid = threadIdx.x, lane = tid % 64;
-    const int D = (int)a.c.dim;
-    const int32_t *src = a.src + ((uint64_t)b * a.c.heads + h) * a.budget;
-    if (src[0] < 0) return;
-    const int32_t s = src[j * kKvPage + lane];
-    if (__builtin_amdgcn_ballot_w64(s != (int32_t)(j * kKvPage + lane)) == 0) return;
+    if (!a.fold[row]) return;
+    const int own = (int)(j * kKvPage) + lane;
+    int s = a.src[row * a.budget + own];
+    if (__builtin_amdgcn_ballot_w64(s != own) == 0) return;
     if (tid < kKvPage) {
+        if (s < 0) {
+            s = a.moved[row * a.budget + ~s];
+            a.weight_out[row * a.cap_out + own] = a.weight[row * a.cap + s];
+            a.pos_out[row * a.cap_out + own] = a.pos[row * a.cap + s];
+        }
         uint8_t *page = page_at(a.c, b, (uint64_t)s / kKvPage);
         const float *sc = page_scales(a.c, page, h);
-        from[tid] = page + (uint64_t)h * 2 * kKvPage * D;
+        place[tid] = s % kKvPage;
+        from[tid] = page + (uint64_t)h * 2 * kKvPage * D + kKvPage * D + s % kKvPage;
         scale[0][tid] = sc[0];
         scale[1][tid] = sc[1];
     }
@@ -196,43 +552,40 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
     uint8_t *page = page_at(a.c, b, j);
     float *sc = page_scales(a.c, page, h);
     uint8_t *kc = page + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
-    // keys: a dword is 4 dimensions of a token; values: 4 tokens of a dimension
-    constexpr int kMax = kKvPage * (int)kKvMaxDim / 4 / kFoldThreads;  // 16 of each
-    uint32_t kw[kMax], vw[kMax];
-    const int per = D / 4, items = kKvPage * D / 4;
+    // keys: 8 dimensions of a token a lane; values: 4 tokens of a dimension,
+    // a lane's tokens the same for all of its dimensions
+    constexpr int kK = D / 32, kV = D / 16, kPer = D / 8;
+    u32x2 kw[kK];
+    uint8_t vb[kV][4];
+    const int t0 = tid % 16 * 4, dv = tid / 16;
+#pragma unroll
+    for (int i = 0; i < kK; ++i) {
+        const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
+        kw[i] = *reinterpret_cast<const u32x2 *>(from[t] - kKvPage * D + place[t] * (D - 1) + d);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint8_t *p = from[t0 + e] + dv * kKvPage;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) vb[i][e] = p[i * 16 * kKvPage];
+    }
     float km = 0.0f, vm = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kMax; ++i) {
-        const int item = tid + i * kFoldThreads;
-        if (item < items) {
-            const int t = item / per, d = item % per * 4;
-            const int place = src[j * kKvPage + t] % kKvPage;
-            kw[i] = *reinterpret_cast<const uint32_t *>(from[t] + place * D + d);
-            const int dv = item / (kKvPage / 4), t0 = item % (kKvPage / 4) * 4;
-            vw[i] = 0;
+    for (int i = 0; i < kK; ++i) {
+        const float f = scale[0][(tid + i * kFoldThreads) / kPer];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int pl = src[j * kKvPage + t0 + e] % kKvPage;
-                vw[i] |= (uint32_t)from[t0 + e][kKvPage * D + dv * kKvPage + pl] << (8 * e);
-            }
+        for (int x = 0; x < 2; ++x) {
+            km = fmaxf(km, finite_abs(code_value<CODES, 0>(kw[i][x]) * f));
+            km = fmaxf(km, finite_abs(code_value<CODES, 1>(kw[i][x]) * f));
+            km = fmaxf(km, finite_abs(code_value<CODES, 2>(kw[i][x]) * f));
+            km = fmaxf(km, finite_abs(code_value<CODES, 3>(kw[i][x]) * f));
         }
     }
+    const float g[4] = {scale[1][t0], scale[1][t0 + 1], scale[1][t0 + 2], scale[1][t0 + 3]};
 #pragma unroll
-    for (int i = 0; i < kMax; ++i) {
-        const int item = tid + i * kFoldThreads;
-        if (item < items) {
-            const float f = scale[0][item / per];
-            const float *g = &scale[1][item % (kKvPage / 4) * 4];
-            km = fmaxf(km, finite_abs(code_value<CODES, 0>(kw[i]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 1>(kw[i]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 2>(kw[i]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 3>(kw[i]) * f));
-            vm = fmaxf(vm, finite_abs(code_value<CODES, 0>(vw[i]) * g[0]));
-            vm = fmaxf(vm, finite_abs(code_value<CODES, 1>(vw[i]) * g[1]));
-            vm = fmaxf(vm, finite_abs(code_value<CODES, 2>(vw[i]) * g[2]));
-            vm = fmaxf(vm, finite_abs(code_value<CODES, 3>(vw[i]) * g[3]));
-        }
-    }
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vm = fmaxf(vm, finite_abs(code_value<CODES, 0>(vb[i][e]) * g[e]));
     km = wave_max0(km);
     vm = wave_max0(vm);
     if (lane == 0) {
@@ -245,33 +598,79 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
     const int ke = scale_exp<CODES>(km), ve = scale_exp<CODES>(vm);
     const float ki = pow2(-ke), vi = pow2(-ve);
 #pragma unroll
-    for (int i = 0; i < kMax; ++i) {
-        const int item = tid + i * kFoldThreads;
-        if (item < items) {
-            const int t = item / per, d = item % per * 4;
-            *reinterpret_cast<uint32_t *>(kc + t * D + d) = requant4<CODES>(kw[i], scale[0][t] * ki);
-            const int dv = item / (kKvPage / 4), t0 = item % (kKvPage / 4) * 4;
-            const float *g = &scale[1][t0];
-            *reinterpret_cast<uint32_t *>(vc + dv * kKvPage + t0) = to_codes4<CODES>(
-                code_value<CODES, 0>(vw[i]) * (g[0] * vi), code_value<CODES, 1>(vw[i]) * (g[1] * vi),
-                code_value<CODES, 2>(vw[i]) * (g[2] * vi), code_value<CODES, 3>(vw[i]) * (g[3] * vi));
-        }
+    for (int i = 0; i < kK; ++i) {
+        const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
+        const float f = scale[0][t] * ki;
+        u32x2 w;
+        w[0] = requant4<CODES>(kw[i][0], f);
+        w[1] = requant4<CODES>(kw[i][1], f);
+        *reinterpret_cast<u32x2 *>(kc + t * D + d) = w;
     }
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+        *reinterpret_cast<uint32_t *>(vc + (dv + i * 16) * kKvPage + t0) = to_codes4<CODES>(
+            code_value<CODES, 0>(vb[i][0]) * (g[0] * vi), code_value<CODES, 0>(vb[i][1]) * (g[1] * vi),
+            code_value<CODES, 0>(vb[i][2]) * (g[2] * vi), code_value<CODES, 0>(vb[i][3]) * (g[3] * vi));
     if (tid == 0) {
         sc[0] = pow2(ke);
         sc[1] = pow2(ve);
     }
 }
 
-}  // namespace
-
-hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s) {
-    hipLaunchKernelGGL(k_kv_select, dim3(a.c.heads, a.c.batch), dim3(kSelThreads), 0, s, a);
+template <int D>
+void fold_go(const KvEvict &a, int codes, hipStream_t s) {
     const dim3 grid(a.budget / kKvPage, a.c.heads, a.c.batch);
     if (codes == kE4m3)
-        hipLaunchKernelGGL((k_kv_fold<kE4m3>), grid, dim3(kFoldThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_fold<D, kE4m3>), grid, dim3(kFoldThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((k_kv_fold<kInt8>), grid, dim3(kFoldThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_fold<D, kInt8>), grid, dim3(kFoldThreads), 0, s, a);
+}
+
+}  // namespace
+
+KvEvictPlan kv_evict_plan(uint32_t batch, uint32_t heads, uint32_t budget, uint32_t max_len) {
+    KvEvictPlan p{};
+    const uint64_t rows = (uint64_t)batch * heads;
+    p.list_bytes = rows * budget * 4;
+    p.fold_bytes = (rows * 4 + 255) / 256 * 256;
+    if (max_len > kOneBlock) {
+        const uint32_t behind = max_len > budget ? max_len - budget : 0;
+        p.piece = kSelThreads * kPieceKeys;
+        for (;;) {
+            p.pieces = (budget + p.piece - 1) / p.piece + (behind + p.piece - 1) / p.piece;
+            if (p.pieces <= kMaxPieces) break;
+            p.piece *= 2;
+        }
+        p.rest_bytes = rows * sizeof(RowState) +
+                       rows * p.pieces * (sizeof(PieceState) + 2 * (kBins1 + kBins2 + kBins3));
+    }
+    p.total = 2 * p.list_bytes + p.fold_bytes + p.rest_bytes;
+    return p;
+}
+
+hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s) {
+    if (a.max_len <= kOneBlock) {
+        const dim3 grid(a.c.heads, a.c.batch);
+        if (a.max_len <= kOneBlock / 2)
+            hipLaunchKernelGGL((k_kv_select<8>), grid, dim3(kSelThreads), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_kv_select<16>), grid, dim3(kSelThreads), 0, s, a);
+    } else {
+        const dim3 grid(a.pieces, a.c.heads, a.c.batch);
+        hipLaunchKernelGGL((k_kv_digit<1>), grid, dim3(kSelThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_digit<2>), grid, dim3(kSelThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_digit<3>), grid, dim3(kSelThreads), 0, s, a);
+        hipLaunchKernelGGL(k_kv_list, grid, dim3(kSelThreads), 0, s, a);
+    }
+    if (a.max_len <= a.budget) return hipGetLastError();  // nothing can move
+    switch (a.c.dim) {
+        case 64: fold_go<64>(a, codes, s); break;
+        case 96: fold_go<96>(a, codes, s); break;
+        case 128: fold_go<128>(a, codes, s); break;
+        case 192: fold_go<192>(a, codes, s); break;
+        case 256: fold_go<256>(a, codes, s); break;
+        default: return hipErrorInvalidValue;
+    }
     return hipGetLastError();
 }
 

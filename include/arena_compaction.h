@@ -599,8 +599,8 @@ int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_
  * a sequence of at most budget tokens is copied there as it is. */
 typedef struct defrag_kv_evict_args {
     const defrag_kv_cache *cache;
-    uint32_t budget;                 /* a multiple of 64, not 0              */
-    uint32_t max_len;                /* no length exceeds it                 */
+    uint32_t budget;                 /* a multiple of 64, not 0, <= 2^25     */
+    uint32_t max_len;                /* no length exceeds it, <= 2^25        */
     int32_t sink, recent;            /* recent is not negative               */
     const int32_t *next_pos_dev;     /* batch: position of the next token    */
     const float *weight_dev;         /* batch x heads x weight_stride        */

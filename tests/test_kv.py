@@ -83,7 +83,7 @@ def test_attend_refusals(fault):
 
 
 @pytest.mark.parametrize("fault", CACHE_FAULTS + [
-    dict(budget=0), dict(budget=100), dict(budget=0xFFFFFFC0), dict(max_len=1025), dict(weight_stride=1000),
+    dict(budget=0), dict(budget=100), dict(budget=0xFFFFFFC0), dict(budget=(1 << 25) + 64), dict(max_len=1025), dict(weight_stride=1000),
     dict(weight_out_stride=127), dict(recent=-1), dict(pos_dev=None), dict(next_pos_dev=None),
     dict(weight_out_dev=None), dict(lens_out_dev=0x90002)])
 def test_evict_refusals(fault):

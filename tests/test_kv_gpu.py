@@ -404,6 +404,37 @@ def test_evict_long(ac):
         check_evict(ac, c, [n], budget, w, pos, sink=4, recent=32, next_pos=[n + 11])
 
 
+@pytest.mark.parametrize("n,budget,ties", [(16385, 64, False), (20000, 8256, True), (40007, 30016, False),
+                                           (70000, 192, True)])
+def test_evict_longer_rows(ac, n, budget, ties):
+    """Rows that several workgroups share, beside shorter ones."""
+    lens = [n, 100, budget, min(n, budget + 1), n - 4321]
+    c = Cache([-(-x // PAGE) for x in lens], 1, 64, INT8)
+    gen = torch.Generator().manual_seed(44)
+    for b in range(len(lens)):
+        for j in range(-(-lens[b] // PAGE)):
+            k, v, sc = c.head(int(c.pages[b, j]), 0)
+            for x in (k, v):
+                x.copy_(torch.randint(-127, 128, x.shape, generator=gen).to(torch.int8))
+            sc.copy_(2.0 ** torch.randint(-3, 3, (2,), generator=gen))
+    w, pos = plane(5, 1, n, 45, ties=ties)
+    check_evict(ac, c, lens, budget, w, pos, sink=4, recent=32 if ties else budget * 3)
+
+
+def test_evict_longer_rows_bad_pages(ac):
+    n = 20000
+    c = Cache([-(-n // PAGE), 1], 2, 64, INT8)
+    c.fill_random([64, 60], 46)
+    c.pages[0, 5], c.pages[0, 200] = -1, c.arena.numel()
+    w, pos = plane(2, 2, n, 47)
+    arena, bad = c.arena.cuda(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    wo, po = torch.zeros(2, 2, 64, device="cuda"), torch.zeros(2, 2, 64, dtype=torch.int32, device="cuda")
+    lo = torch.full((2,), 77, dtype=torch.int32, device="cuda")
+    ac.defrag_kv_evict(arena, c.pages.cuda(), ints([n, 60]), 64, w.cuda(), pos.cuda(), wo, po, lo, 64, INT8, n_invalid=bad)
+    assert int(bad) == 2 and lo.tolist() == [77, 60] and (wo[0] == 0).all() and torch.equal(wo[1, :, :60].cpu(), w[1, :, :60])
+    same(c, arena)
+
+
 def test_evict_leaves_bad_sequences_alone(ac):
     c = Cache([3, 3, 3], 2, 64, INT8, stride=3)
     c.fill_random([190, 190, 190], 41)
