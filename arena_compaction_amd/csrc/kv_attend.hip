@@ -58,7 +58,7 @@ __device__ inline int block_pages(const KvAttend &a, const Seq &s, int rb) {
 }
 
 template <int D, int CODES, int DTYPE, int R>
-__global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
+__global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_attend(KvAttend a) {
     constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 16 * R, kJoin = 4;
     __shared__ f32x4 sm_o[kWaves][R * kJoin * 64];
     __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
     const int active = pages > per ? (pages + per - 1) / per : 1;
     if (split >= active) return;
     const int p_lo = split * per, p_hi = p_lo + per < pages ? p_lo + per : pages;
-    const bool counts = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows && lane == 0;
+    const bool counts = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows && lane == 0;  // once a page
 
     // queries, and how many tokens each row sees
     u32x4 q[R][kSteps];
@@ -105,31 +105,42 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
         for (int dt = 0; dt < kTiles; ++dt) o[rt][dt] = f32x4{0, 0, 0, 0};
     }
 
+    // this wave's pages, every fourth: lane i keeps the i-th one's offset and
+    // scales, so that the loop waits for neither
+    const int np = p_hi - p_lo > wave ? (p_hi - p_lo - wave + kWaves - 1) / kWaves : 0;
+    const uint64_t off = lane < np ? page_offset(a.c, b, p_lo + wave + kWaves * lane) : kNoPage;
+    const uint64_t good = __builtin_amdgcn_ballot_w64(off != kNoPage);
+    f32x2 scales = {0, 0};
+    if (off != kNoPage) scales = *reinterpret_cast<const f32x2 *>(page_scales(a.c, a.c.arena + off, h));
+    if (counts && np) {
+        const int none = np - __builtin_popcountll(good);
+        if (none) atomicAdd(a.c.n_invalid, (unsigned long long)none);
+    }
+    const uint8_t *strips = a.c.arena + (uint64_t)h * 2 * kKvPage * D;
     uint32_t kraw[4][D / 16];
     u32x4 vraw[kTiles];
-    auto load_values = [&](const uint8_t *strip) {
+    auto get_keys = [&](int i) { load_keys<D>(strips + lane_u64(off, i), lane, kraw); };
+    auto get_values = [&](int i) {
+        const uint8_t *from = strips + lane_u64(off, i) + kKvPage * D + n * kKvPage + g * 16;
 #pragma unroll
-        for (int dt = 0; dt < kTiles; ++dt)
-            vraw[dt] = *reinterpret_cast<const u32x4 *>(strip + kKvPage * D + (dt * 16 + n) * kKvPage + g * 16);
+        for (int dt = 0; dt < kTiles; ++dt) vraw[dt] = *reinterpret_cast<const u32x4 *>(from + dt * 16 * kKvPage);
     };
-    auto strip_of = [&](const uint8_t *page) { return page + (uint64_t)h * 2 * kKvPage * D; };
-    int p = p_lo + wave;
-    uint8_t *page = p < p_hi ? wave_uniform(page_at(a.c, b, p)) : nullptr;
-    if (page) load_keys<D>(strip_of(page), lane, kraw);
-    for (; p < p_hi; p += kWaves) {
-        uint8_t *next = p + kWaves < p_hi ? wave_uniform(page_at(a.c, b, p + kWaves)) : nullptr;
-        if (!page) {
-            if (counts) atomicAdd(a.c.n_invalid, 1ull);
-            page = next;
-            if (page) load_keys<D>(strip_of(page), lane, kraw);
-            continue;
-        }
-        const float *sc = page_scales(a.c, page, h);
-        const float f = a.scale * kLog2e * sc[0];
-        int ei = exp_of_pow2(sc[1]);
+    // positions of the set bits of `good` are the pages that are there
+    uint64_t todo = good;
+    uint32_t no_numbers = 0;
+    if (todo) {
+        get_keys(__builtin_ctzll(todo));
+        get_values(__builtin_ctzll(todo));
+    }
+    while (todo) {
+        const int i = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const int next = todo ? __builtin_ctzll(todo) : -1;
+        const int base = (p_lo + wave + kWaves * i) * kKvPage;
+        const float f = a.scale * kLog2e * lane_f32(scales[0], i);
+        int ei = exp_of_pow2(lane_f32(scales[1], i));
         ei = ei < -100 ? -100 : ei;
         const float ev = (float)ei, un = pow2(-ei);
-        load_values(strip_of(page));
         f32x4 w[R][4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
@@ -142,8 +153,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
                 for (int rt = 0; rt < R; ++rt) w[rt][tt] = mfma16<DTYPE>(kk, q[rt][st], w[rt][tt]);
             }
         }
-        if (next) load_keys<D>(strip_of(next), lane, kraw);
-        const int base = p * kKvPage;
+        if (next >= 0) get_keys(next);
         const bool edge = base + kKvPage > see_least;
         u32x4 pw[R][2];
 #pragma unroll
@@ -160,8 +170,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
                     top = fmaxf(top, t);
                 }
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = across_groups(top, [](float x, float y) { return fmaxf(x, y); });
             const float mn = fmaxf(m[rt], top - kLift), ms = mn == KV_NEG_INF ? 0.0f : mn;
             const float fade = __builtin_amdgcn_exp2f(m[rt] - ms);
             m[rt] = mn;
@@ -196,40 +205,17 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
         }
         if constexpr (CODES == kE4m3) {
             // a value that is no number must not reach rows that do not see
-            // its token (their weight is 0, and 0 x NaN is NaN)
-            uint32_t any = 0;
+            // its token (their weight is 0, and 0 x NaN is NaN): left out
+            // here, it is put in below for the rows that see it
             if (edge) {
 #pragma unroll
                 for (int dt = 0; dt < kTiles; ++dt)
-                    any |= nan_codes(vraw[dt][0]) | nan_codes(vraw[dt][1]) | nan_codes(vraw[dt][2]) |
-                           nan_codes(vraw[dt][3]);
-            }
-            if (__builtin_amdgcn_ballot_w64(any != 0)) {
 #pragma unroll
-                for (int rt = 0; rt < R; ++rt) {
-                    // whether the row sees each token, x whether its value is NaN
-                    const int see = lim[rt] - base - g * 16;
-                    u32x4 sees[2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sees[i / 4][i % 4] = (2 * i < see ? 0x3C00u : 0u) | (2 * i + 1 < see ? 0x3C000000u : 0u);
-#pragma unroll
-                    for (int dt = 0; dt < kTiles; ++dt) {
-                        uint32_t one[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) one[x] = (nan_codes(vraw[dt][x]) >> 7) * 0x38u;
-                        f32x4 hit = {0, 0, 0, 0};
-                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[0], one[1]), sees[0], hit);
-                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[2], one[3]), sees[1], hit);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (hit[i] > 0.0f) o[rt][dt][i] = __builtin_nanf("");
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t no = nan_codes(vraw[dt][x]);
+                        vraw[dt][x] &= ~((no >> 7) * 255u);
+                        no_numbers |= no;
                     }
-                }
-#pragma unroll
-                for (int dt = 0; dt < kTiles; ++dt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) vraw[dt][x] &= ~((nan_codes(vraw[dt][x]) >> 7) * 255u);
             }
         }
 #pragma unroll
@@ -242,15 +228,44 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
                 o[rt][dt] = mfma16<kFp16>(v1, pw[rt][1], o[rt][dt]);
             }
         }
-        page = next;
+        if (next >= 0) get_values(next);
+    }
+    if constexpr (CODES == kE4m3) {
+        if (__builtin_amdgcn_ballot_w64(no_numbers != 0)) {
+            // sums over tokens of (the row sees it) x (its value is NaN)
+            for (todo = good; todo; todo &= todo - 1) {
+                const int i = __builtin_ctzll(todo), base = (p_lo + wave + kWaves * i) * kKvPage;
+                if (base + kKvPage <= see_least) continue;
+                const uint8_t *from = strips + lane_u64(off, i) + kKvPage * D + n * kKvPage + g * 16;
+#pragma unroll
+                for (int dt = 0; dt < kTiles; ++dt) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(from + dt * 16 * kKvPage);
+                    uint32_t one[4];  // 0x38 is the code of 1
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) one[x] = (nan_codes(v[x]) >> 7) * 0x38u;
+#pragma unroll
+                    for (int rt = 0; rt < R; ++rt) {
+                        const int see = lim[rt] - base - g * 16;
+                        u32x4 sees[2];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            sees[x / 4][x % 4] = (2 * x < see ? 0x3C00u : 0u) | (2 * x + 1 < see ? 0x3C000000u : 0u);
+                        f32x4 hit = {0, 0, 0, 0};
+                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[0], one[1]), sees[0], hit);
+                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[2], one[3]), sees[1], hit);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (hit[x] > 0.0f) o[rt][dt][x] = __builtin_nanf("");
+                    }
+                }
+            }
+        }
     }
 
     // join the four waves
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
-        float sum = l[rt];
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
+        const float sum = across_groups(l[rt], [](float x, float y) { return x + y; });
         if (g == 0) {
             sm_m[wave][rt * 16 + n] = m[rt];
             sm_l[wave][rt * 16 + n] = sum;
@@ -315,14 +330,17 @@ __global__ __launch_bounds__(kThreads) void k_kv_attend(KvAttend a) {
     }
 }
 
-// Joins the parts of rows whose cache was split: one wave a row and head.
+// Joins the parts of rows whose cache was split: one workgroup a row and
+// head.  Each wave takes every fourth part, 64 of them at a time with a
+// part's maximum and sum in a lane, so that all loads are under way at once.
 template <int DTYPE>
 __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttend a) {
+    constexpr int kMost = (int)kKvMaxDim / 64;
+    __shared__ float sm_v[kWaves][kKvMaxDim], sm_m[kWaves], sm_l[kWaves];
     const uint32_t b = blockIdx.y, D = a.c.dim;
-    const int lane = threadIdx.x % 64, G = (int)a.group;
+    const int wave = wave_uniform(threadIdx.x / 64), lane = threadIdx.x % 64, G = (int)a.group;
     const uint64_t heads = (uint64_t)a.c.heads * G, all = a.tokens * heads;
-    const uint64_t unit = (uint64_t)blockIdx.x * kWaves + threadIdx.x / 64;
-    const uint64_t t = unit / heads, hq = unit % heads;
+    const uint64_t t = blockIdx.x / heads, hq = blockIdx.x % heads;
     bool bad;
     const Seq s = sequence(a, b, &bad);
     if (t >= (uint64_t)s.count) return;
@@ -331,27 +349,59 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttend a) {
     if (active <= 1) return;
     const uint64_t row = (s.first + t) * heads + hq;
     const float *ml = a.part + (uint64_t)a.splits * all * D + row * 2;
-    float top = KV_NEG_INF;
-    for (int k = 0; k < active; ++k) top = fmaxf(top, ml[k * all * 2]);
-    const float ts = top == KV_NEG_INF ? 0.0f : top;
-    float sum = 0.0f, v[kKvMaxDim / 64] = {};
-    for (int k = 0; k < active; ++k) {
-        const float fade = __builtin_amdgcn_exp2f(ml[k * all * 2] - ts);
-        sum += ml[k * all * 2 + 1] * fade;
-        const float *src = a.part + (k * all + row) * D;
+    float top = KV_NEG_INF, sum = 0.0f, v[kMost] = {};
+    for (int k0 = wave; k0 < active; k0 += kWaves * 64) {
+        const int mine = k0 + lane * kWaves;
+        f32x2 x = {KV_NEG_INF, 0.0f};
+        if (mine < active) x = *reinterpret_cast<const f32x2 *>(ml + mine * all * 2);
+        const float m = x[0], l = x[1];
+        const float now = fmaxf(top, wave_reduce(m, [](float p, float q) { return fmaxf(p, q); }));
+        const float ts = now == KV_NEG_INF ? 0.0f : now;
+        const float fade = __builtin_amdgcn_exp2f(m - ts), old = __builtin_amdgcn_exp2f(top - ts);
+        top = now;
+        sum = sum * old + wave_reduce(l * fade, [](float p, float q) { return p + q; });
 #pragma unroll
-        for (int i = 0; i < (int)kKvMaxDim / 64; ++i) {
-            const uint32_t d = lane + 64 * i;
-            if (d < D) v[i] += src[d] * fade;
+        for (int i = 0; i < kMost; ++i) v[i] *= old;
+        const int n = (active - k0 + kWaves - 1) / kWaves < 64 ? (active - k0 + kWaves - 1) / kWaves : 64;
+        const float *src = a.part + (k0 * all + row) * D;
+        for (int k = 0; k < n; k += 8) {
+            float x[8][kMost];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float *p = src + (uint64_t)(k + u < n ? k + u : n - 1) * kWaves * all * D;
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) x[u][i] = lane + 64 * i < (int)D ? p[lane + 64 * i] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float w = k + u < n ? lane_f32(fade, k + u < n ? k + u : 0) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < kMost; ++i)
+                    if (k + u < n) v[i] += x[u][i] * w;
+            }
         }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < (int)kKvMaxDim / 64; ++i) {
-        const uint32_t d = lane + 64 * i;
-        if (d < D) a.out[row * D + d] = (uint16_t)pack2<DTYPE>(v[i] * inv, 0.0f);
-    }
     if (lane == 0) {
+        sm_m[wave] = top;
+        sm_l[wave] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) sm_v[wave][lane + 64 * i] = v[i];
+    __syncthreads();
+    top = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    const float ts = top == KV_NEG_INF ? 0.0f : top;
+    float fade[kWaves], out = 0.0f;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+        fade[k] = __builtin_amdgcn_exp2f(sm_m[k] - ts);
+        sum += sm_l[k] * fade[k];
+    }
+    const uint32_t d = threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) out += sm_v[k][d] * fade[k];
+    if (d < D) a.out[row * D + d] = (uint16_t)pack2<DTYPE>(sum == 0.0f ? 0.0f : out / sum, 0.0f);
+    if (d == 0) {
         const float l2 = sum == 0.0f ? KV_NEG_INF : ts + log2f(sum);
         if (a.lse) a.lse[row] = l2 * kLn2;
         if (a.lse2) a.lse2[row] = l2;
@@ -373,11 +423,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_weigh(KvAttend a) {
     const Seq s = sequence(a, b, &bad);
     const int p = blockIdx.x, base = p * kKvPage;
     if (base >= s.len || s.count == 0) return;
-    uint8_t *page = wave_uniform(page_at(a.c, b, p));
-    if (!page) return;
+    const uint64_t off = wave_uniform(page_offset(a.c, b, p));
+    if (off == kNoPage) return;
     uint32_t kraw[4][D / 16];
-    load_keys<D>(page + (uint64_t)h * 2 * kKvPage * D, lane, kraw);
-    const float f = a.scale * kLog2e * page_scales(a.c, page, h)[0];
+    load_keys<D>(a.c.arena + off + (uint64_t)h * 2 * kKvPage * D, lane, kraw);
+    const float f = a.scale * kLog2e * page_scales(a.c, a.c.arena + off, h)[0];
     u32x4 kk[4][kSteps];
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
@@ -428,14 +478,14 @@ __global__ __launch_bounds__(kThreads) void k_kv_weigh(KvAttend a) {
 template <int D, int CODES, int DTYPE>
 void attend_go(const KvAttend &a, hipStream_t s) {
     const dim3 grid(a.splits * a.row_blocks, a.c.heads, a.c.batch);
-    if (a.rows == 16)
-        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1>), grid, dim3(kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2>), grid, dim3(kThreads), 0, s, a);
+    if constexpr (D <= 128) {
+        if (a.rows == 32)
+            hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2>), grid, dim3(kThreads), 0, s, a);
+    }
+    if (a.rows == 16) hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1>), grid, dim3(kThreads), 0, s, a);
     if (a.splits > 1) {
-        const uint64_t units = (uint64_t)a.max_new * a.c.heads * a.group;
-        hipLaunchKernelGGL((k_kv_join<DTYPE>), dim3((uint32_t)((units + kWaves - 1) / kWaves), a.c.batch),
-                           dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_join<DTYPE>), dim3(a.max_new * a.c.heads * a.group, a.c.batch), dim3(kThreads), 0,
+                           s, a);
     }
     if (a.weight)
         hipLaunchKernelGGL((k_kv_weigh<D, CODES, DTYPE>),
@@ -465,15 +515,20 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
                             uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
     KvAttendPlan p{};
     const uint64_t rows = (uint64_t)max_new * group;
-    p.rows = rows <= 16 ? 16 : 32;
+    // 32 rows a wave share the codes brought to 16 bits; above 128 dimensions
+    // their sums would leave no registers to load ahead
+    p.rows = rows <= 16 || dim > 128 ? 16 : 32;
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    // enough workgroups for 4 on each of 256 compute units, and a page for
-    // each of a workgroup's waves
-    uint64_t splits = units ? (1024 + units - 1) / units : 1;
+    // two workgroups for each of 256 compute units, and a page for each of a
+    // workgroup's waves (four a unit: long 111 us instead of 104, draft 55
+    // instead of 48, batch 72 instead of 61, scored 54 instead of 61)
+    constexpr uint64_t kTarget = 512;
+    uint64_t splits = units ? (kTarget + units - 1) / units : 1;
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
+    if (per > 64 * kWaves) per = 64 * kWaves;  // a lane keeps the offset of each page of its wave
     p.per_split = (uint32_t)per;
     p.splits = (uint32_t)((pages + per - 1) / per);
     if (p.splits < 1) p.splits = 1;

@@ -106,14 +106,29 @@ __device__ inline uint32_t requant4(uint32_t w, float f) {
                             code_value<CODES, 2>(w) * f, code_value<CODES, 3>(w) * f);
 }
 
-// The first byte of a page, or null where the table's entry is none: outside
-// the arena, or not on the arena's 32-byte grid.
-__device__ inline uint8_t *page_at(const KvCache &c, uint32_t b, uint64_t j) {
+constexpr uint64_t kNoPage = ~0ull;
+
+// A page's offset, or kNoPage where the table's entry is none: outside the
+// arena, or not on the arena's 32-byte grid.
+__device__ inline uint64_t page_offset(const KvCache &c, uint32_t b, uint64_t j) {
     const int64_t off = c.pages[(uint64_t)b * c.stride + j];
     const uint64_t need = kv_page_bytes(c.heads, c.dim);
-    if (off < 0 || (off & 31) || need > c.arena_bytes || (uint64_t)off > c.arena_bytes - need)
-        return nullptr;
-    return c.arena + off;
+    const bool bad = off < 0 || (off & 31) || need > c.arena_bytes || (uint64_t)off > c.arena_bytes - need;
+    return bad ? kNoPage : (uint64_t)off;
+}
+
+__device__ inline uint8_t *page_at(const KvCache &c, uint32_t b, uint64_t j) {
+    const uint64_t off = page_offset(c, b, j);
+    return off == kNoPage ? nullptr : c.arena + off;
+}
+
+// What lane i (the same i in every lane) holds, in scalar registers.
+__device__ inline uint64_t lane_u64(uint64_t x, int i) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, i) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), i) << 32;
+}
+__device__ inline float lane_f32(float x, int i) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
 }
 
 __device__ inline float *page_scales(const KvCache &c, uint8_t *page, uint32_t h) {
@@ -139,6 +154,21 @@ __device__ inline void new_tokens(const int32_t *starts, uint64_t tokens, uint32
 // The top bit of each of four e4m3 codes that is a NaN (0x7F or 0xFF).
 __device__ inline uint32_t nan_codes(uint32_t w) {
     return ~(((w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;
+}
+
+// op over the four lanes that share lane % 16, in each of them.  The swaps
+// exchange rows of 16 (halves of 32) lanes of two registers: of a value with
+// itself, the results are the one row (half) and the other, in both.
+template <typename Op>
+__device__ inline float across_groups(float x, Op op) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t p0 = p[0], p1 = p[1];
+    const float y = op(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1));
+    const uint32_t v = __builtin_bit_cast(uint32_t, y);
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    return op(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
 }
 
 // Largest of the wave's values (each at least 0), in every lane.
