@@ -23,6 +23,7 @@ namespace ac {
 constexpr int kKvPage = 64;       // tokens of a page
 constexpr int kKvExpMin = -64;    // least exponent of a scale
 constexpr uint32_t kKvMaxDim = 256;
+constexpr uint32_t kKvPromptRows = 128;  // query rows of a workgroup over a prompt
 
 inline __host__ __device__ uint64_t kv_page_bytes(uint32_t heads, uint32_t dim) {
     return (uint64_t)heads * (2ull * kKvPage * dim + 8);
@@ -71,8 +72,9 @@ struct KvAttend {
     uint32_t rows;               // query rows of a workgroup
     uint32_t row_blocks;
     float *part;     // [splits][tokens * heads * group][dim + 2]
-    float *scores;   // [batch][heads][pages][row_blocks * rows][64]
-    float *lse2;     // [tokens * heads * group], base-2 log of the sums
+    float *scores;   // [batch][heads][score_pages][score_rows][64], or null
+    uint32_t score_pages, score_rows;
+    float2 *sums;    // [tokens * heads * group]: m and 1 / sum of 2^(t - m), or null
 };
 
 struct KvEvict {
@@ -103,8 +105,8 @@ struct KvEvictPlan {
 KvEvictPlan kv_evict_plan(uint32_t batch, uint32_t heads, uint32_t budget, uint32_t max_len);
 
 struct KvAttendPlan {
-    uint32_t rows, row_blocks, splits, per_split;
-    uint64_t part_bytes, score_bytes, lse_bytes, total;
+    uint32_t rows, row_blocks, splits, per_split, score_rows;
+    uint64_t part_bytes, score_bytes, sum_bytes, total;
 };
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
@@ -113,6 +115,8 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
 // codes: 0 e4m3, 1 int8; dtype: 0 bfloat16, 1 float16
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_prompt(const KvAttend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_weigh(const KvAttend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s);
 hipError_t launch_kv_zero(uint64_t *p, hipStream_t s);
 

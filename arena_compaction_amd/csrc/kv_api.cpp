@@ -154,7 +154,7 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     const defrag_kv_cache *c = a->cache;
     const KvAttendPlan p = plan_of(a);
     if (a->tokens) {
-        if ((uint64_t)p.splits * p.row_blocks > kMaxGrid ||
+        if ((uint64_t)p.splits * p.row_blocks * c->batch * c->heads > kMaxGrid ||
             (uint64_t)a->max_new * c->heads * a->group > kMaxGrid)
             return DEFRAG_EINVAL;
         rc = check_ws(ws_dev, ws_bytes, p.total);
@@ -184,8 +184,10 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     k.rows = p.rows;
     k.row_blocks = p.row_blocks;
     k.part = reinterpret_cast<float *>(ws);
-    k.scores = reinterpret_cast<float *>(ws + p.part_bytes);
-    k.lse2 = p.lse_bytes ? reinterpret_cast<float *>(ws + p.part_bytes + p.score_bytes) : nullptr;
+    k.scores = p.score_bytes ? reinterpret_cast<float *>(ws + p.part_bytes) : nullptr;
+    k.score_pages = (a->max_len + kKvPage - 1) / kKvPage;
+    k.score_rows = p.score_rows;
+    k.sums = p.sum_bytes ? reinterpret_cast<float2 *>(ws + p.part_bytes + p.score_bytes) : nullptr;
     return launch_kv_attend(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
 }
 

@@ -9,8 +9,8 @@
 // Everything runs in powers of two, t_rj = log2(e) * s_rj + log2(ev): with
 // the value scale inside the exponent, w_rj = 2^(t_rj - m) multiplies value
 // codes of any page, and sum_j w_rj / ev is the softmax's sum, one factor a
-// page.  m is the running maximum of t less 14: float16 weights then reach
-// down to 2^-38 of the largest before they lose their last bit.
+// page.  m lies 13 to 15 below the running maximum of t: float16 weights then
+// reach down to 2^-37 of the largest before they lose their last bit.
 //
 // A wave takes whole pages, one at a time, with its own running maximum and
 // sums; a page's key codes are loaded while the page before is summed, its
@@ -20,42 +20,10 @@
 // the weights are the next product's operand where they are.  Four waves
 // share a workgroup's rows and join through LDS; workgroups split a long
 // cache and k_kv_join joins their parts.
-#include "kv_mfma.h"
+#include "kv_rows.h"
 
 namespace ac {
 namespace {
-
-constexpr int kThreads = 256, kWaves = 4;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kLift = 14.0f;
-#define KV_NEG_INF (-__builtin_inff())
-
-// Place of a call's sequence b: its new tokens, and how many tokens it holds.
-struct Seq {
-    uint64_t first;
-    int count, len, had;
-};
-
-__device__ inline Seq sequence(const KvAttend &a, uint32_t b, bool *bad) {
-    Seq s;
-    new_tokens(a.starts, a.tokens, a.max_new, b, &s.first, &s.count, bad);
-    s.len = a.c.lens[b];
-    if (s.len < 0 || (uint32_t)s.len > a.max_len) {  // as a sequence that holds nothing
-        *bad = true;
-        s.len = 0;
-    }
-    s.had = s.len - s.count;
-    return s;
-}
-
-// Pages that the rows of block rb may see (its last row sees most).
-__device__ inline int block_pages(const KvAttend &a, const Seq &s, int rb) {
-    const int rows = s.count * (int)a.group;
-    int last = (rb + 1) * (int)a.rows;
-    last = (last < rows ? last : rows) - 1;
-    const int see = s.had + last / (int)a.group + 1;
-    return see > 0 ? (see + kKvPage - 1) / kKvPage : 0;
-}
 
 template <int D, int CODES, int DTYPE, int R>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_attend(KvAttend a) {
@@ -78,29 +46,15 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
     const int p_lo = split * per, p_hi = p_lo + per < pages ? p_lo + per : pages;
     const bool counts = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows && lane == 0;  // once a page
 
-    // queries, and how many tokens each row sees
     u32x4 q[R][kSteps];
     int lim[R];
+    load_rows<D, R>(a, s, h, rb * kRows, lane, q, lim);
     const int see_least = s.had + rb * kRows / G + 1;  // of the block's first row
-#pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        const int r = rb * kRows + rt * 16 + n;
-        const bool real = r < rows;
-        const int t = real ? r / G : 0, hg = real ? r % G : 0;
-        lim[rt] = real ? s.had + t + 1 : 0;
-        const uint16_t *p = a.q + (int64_t)(s.first + t) * a.q_row + (int64_t)(h * G + hg) * a.q_head;
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            q[rt][st] = u32x4{0, 0, 0, 0};
-            if (real) q[rt][st] = load_q8(p + dim_of<D>(st, g), a.vec_q);
-        }
-    }
     f32x4 o[R][kTiles];
-    float m[R], l[R];
+    Soft soft[R];
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
-        m[rt] = KV_NEG_INF;
-        l[rt] = 0.0f;
+        soft[rt] = Soft{KV_NEG_INF, 0.0f};
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt) o[rt][dt] = f32x4{0, 0, 0, 0};
     }
@@ -138,9 +92,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
         const int next = todo ? __builtin_ctzll(todo) : -1;
         const int base = (p_lo + wave + kWaves * i) * kKvPage;
         const float f = a.scale * kLog2e * lane_f32(scales[0], i);
-        int ei = exp_of_pow2(lane_f32(scales[1], i));
-        ei = ei < -100 ? -100 : ei;
-        const float ev = (float)ei, un = pow2(-ei);
+        const int ei = value_exp(lane_f32(scales[1], i));
         f32x4 w[R][4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
@@ -154,54 +106,38 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
             }
         }
         if (next >= 0) get_keys(next);
+        if (a.scores) {
+            float *to = a.scores + ((uint64_t)b * a.c.heads + h) * a.score_pages * a.score_rows * kKvPage;
+            to += (uint64_t)(p_lo + wave + kWaves * i) * a.score_rows * kKvPage;
+#pragma unroll
+            for (int rt = 0; rt < R; ++rt) {
+                const int r = rb * kRows + rt * 16 + n;
+                if (r < rows) {
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt)
+                        *reinterpret_cast<f32x4 *>(to + r * kKvPage + g * 16 + tt * 4) = w[rt][tt] * f;
+                }
+            }
+        }
         const bool edge = base + kKvPage > see_least;
         u32x4 pw[R][2];
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
-            float top = KV_NEG_INF;
-            const int see = lim[rt] - base - g * 16;
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float t = __builtin_fmaf(w[rt][tt][i], f, ev);
-                    if (edge && tt * 4 + i >= see) t = KV_NEG_INF;
-                    w[rt][tt][i] = t;
-                    top = fmaxf(top, t);
-                }
-            }
-            top = across_groups(top, [](float x, float y) { return fmaxf(x, y); });
-            const float mn = fmaxf(m[rt], top - kLift), ms = mn == KV_NEG_INF ? 0.0f : mn;
-            const float fade = __builtin_amdgcn_exp2f(m[rt] - ms);
-            m[rt] = mn;
-            float sum = 0.0f;
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[rt][tt][i] = __builtin_amdgcn_exp2f(w[rt][tt][i] - ms);
-                    sum += w[rt][tt][i];
-                }
-                pw[rt][tt / 2][tt % 2 * 2] = pack2<kFp16>(w[rt][tt][0], w[rt][tt][1]);
-                pw[rt][tt / 2][tt % 2 * 2 + 1] = pack2<kFp16>(w[rt][tt][2], w[rt][tt][3]);
-            }
-            l[rt] = l[rt] * fade + sum * un;
+            const float fade = soft_page(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
+            pack_weights(w[rt], pw[rt]);
             if (__builtin_amdgcn_ballot_w64(fade != 1.0f)) {
 #pragma unroll
                 for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[rt][dt][i] *= fade;
+                    for (int x = 0; x < 4; ++x) o[rt][dt][x] *= fade;
             }
         }
-        if (base + kKvPage > s.len) {  // places behind the last token may hold no numbers
-            const int there = s.len - base - g * 16;
+        if (base + kKvPage > s.len) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int k = there - 4 * x;
-                const uint32_t mask = k >= 4 ? ~0u : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+            for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
-                for (int dt = 0; dt < kTiles; ++dt) vraw[dt][x] &= mask;
-            }
+                for (int x = 0; x < 4; ++x)
+                    vraw[dt][x] = only_there(vraw[dt][x], s.len - base - g * 16 - 4 * x);
         }
         if constexpr (CODES == kE4m3) {
             // a value that is no number must not reach rows that do not see
@@ -232,32 +168,13 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
     }
     if constexpr (CODES == kE4m3) {
         if (__builtin_amdgcn_ballot_w64(no_numbers != 0)) {
-            // sums over tokens of (the row sees it) x (its value is NaN)
             for (todo = good; todo; todo &= todo - 1) {
                 const int i = __builtin_ctzll(todo), base = (p_lo + wave + kWaves * i) * kKvPage;
                 if (base + kKvPage <= see_least) continue;
-                const uint8_t *from = strips + lane_u64(off, i) + kKvPage * D + n * kKvPage + g * 16;
+                int see[R];
 #pragma unroll
-                for (int dt = 0; dt < kTiles; ++dt) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(from + dt * 16 * kKvPage);
-                    uint32_t one[4];  // 0x38 is the code of 1
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) one[x] = (nan_codes(v[x]) >> 7) * 0x38u;
-#pragma unroll
-                    for (int rt = 0; rt < R; ++rt) {
-                        const int see = lim[rt] - base - g * 16;
-                        u32x4 sees[2];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            sees[x / 4][x % 4] = (2 * x < see ? 0x3C00u : 0u) | (2 * x + 1 < see ? 0x3C000000u : 0u);
-                        f32x4 hit = {0, 0, 0, 0};
-                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[0], one[1]), sees[0], hit);
-                        hit = mfma16<kFp16>(widen8<kE4m3, kFp16>(one[2], one[3]), sees[1], hit);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (hit[x] > 0.0f) o[rt][dt][x] = __builtin_nanf("");
-                    }
-                }
+                for (int rt = 0; rt < R; ++rt) see[rt] = lim[rt] - base - g * 16;
+                put_nan<D, R>(strips + lane_u64(off, i) + kKvPage * D + n * kKvPage + g * 16, see, o);
             }
         }
     }
@@ -265,9 +182,9 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
     // join the four waves
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
-        const float sum = across_groups(l[rt], [](float x, float y) { return x + y; });
+        const float sum = across_groups(soft[rt].l, [](float x, float y) { return x + y; });
         if (g == 0) {
-            sm_m[wave][rt * 16 + n] = m[rt];
+            sm_m[wave][rt * 16 + n] = soft[rt].m;
             sm_l[wave][rt * 16 + n] = sum;
         }
     }
@@ -278,7 +195,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
         const int x = rt * 16 + n;
         float top = fmaxf(fmaxf(sm_m[0][x], sm_m[1][x]), fmaxf(sm_m[2][x], sm_m[3][x]));
         if (top == KV_NEG_INF) top = 0.0f;
-        const float fade = __builtin_amdgcn_exp2f(m[rt] - top);
+        const float fade = __builtin_amdgcn_exp2f(soft[rt].m - top);
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
@@ -313,11 +230,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
                 w[0] = pack2<DTYPE>(v[0] * inv, v[1] * inv);
                 w[1] = pack2<DTYPE>(v[2] * inv, v[3] * inv);
                 *reinterpret_cast<u32x2 *>(a.out + row * D + d) = w;
-                if (d == 0) {
-                    const float l2 = sum == 0.0f ? KV_NEG_INF : ts + log2f(sum);
-                    if (a.lse) a.lse[row] = l2 * kLn2;
-                    if (a.lse2) a.lse2[row] = l2;
-                }
+                if (d == 0) put_sum(a, row, ts, sum);
             } else {
                 *reinterpret_cast<f32x4 *>(a.part + ((uint64_t)split * all + row) * D + d) = v;
                 if (d == 0) {
@@ -401,78 +314,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttend a) {
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) out += sm_v[k][d] * fade[k];
     if (d < D) a.out[row * D + d] = (uint16_t)pack2<DTYPE>(sum == 0.0f ? 0.0f : out / sum, 0.0f);
-    if (d == 0) {
-        const float l2 = sum == 0.0f ? KV_NEG_INF : ts + log2f(sum);
-        if (a.lse) a.lse[row] = l2 * kLn2;
-        if (a.lse2) a.lse2[row] = l2;
-    }
-}
-
-// The weight every cached token receives.  It needs each row's whole sum, so
-// it makes the scores again: one workgroup a (page, head) holds the page's
-// keys and goes over all the rows that see it, the waves taking 16 rows at a
-// time in turn; sums run in one order whatever else runs.
-template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(kThreads) void k_kv_weigh(KvAttend a) {
-    constexpr int kSteps = D / 32;
-    __shared__ float sm[kWaves][kKvPage];
-    const uint32_t h = blockIdx.y, b = blockIdx.z;
-    const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
-    const int n = lane % 16, g = lane / 16, G = (int)a.group;
-    bool bad;
-    const Seq s = sequence(a, b, &bad);
-    const int p = blockIdx.x, base = p * kKvPage;
-    if (base >= s.len || s.count == 0) return;
-    const uint64_t off = wave_uniform(page_offset(a.c, b, p));
-    if (off == kNoPage) return;
-    uint32_t kraw[4][D / 16];
-    load_keys<D>(a.c.arena + off + (uint64_t)h * 2 * kKvPage * D, lane, kraw);
-    const float f = a.scale * kLog2e * page_scales(a.c, a.c.arena + off, h)[0];
-    u32x4 kk[4][kSteps];
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st)
-            kk[tt][st] = widen8<CODES, DTYPE>(kraw[tt][2 * st], kraw[tt][2 * st + 1]);
-    float acc[16] = {};
-    const int rows = s.count * G;
-    const int from = base > s.had ? (base - s.had) * G / 16 : 0;  // earlier rows see nothing here
-    const uint64_t heads = (uint64_t)a.c.heads * G;
-    for (int x = from + wave; x * 16 < rows; x += kWaves) {
-        const int r = x * 16 + n;
-        const bool real = r < rows;
-        const int t = real ? r / G : 0, hg = real ? r % G : 0;
-        const int see = real ? s.had + t + 1 - base - g * 16 : 0;
-        const float l2 = real ? a.lse2[(s.first + t) * heads + (uint64_t)h * G + hg] : 0.0f;
-        const uint16_t *qp = a.q + (int64_t)(s.first + t) * a.q_row + (int64_t)(h * G + hg) * a.q_head;
-        u32x4 q[kSteps];
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) q[st] = load_q8(qp + dim_of<D>(st, g), a.vec_q);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            f32x4 w = {0, 0, 0, 0};
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) w = mfma16<DTYPE>(kk[tt][st], q[st], w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], f, -l2));
-                acc[tt * 4 + i] += tt * 4 + i < see ? e : 0.0f;
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float v = acc[i];
-        v += dpp_move<kDppQuadSwap1>(v);
-        v += dpp_move<kDppQuadSwap2>(v);
-        v += dpp_move<kDppRowHalfMirror>(v);
-        v += dpp_move<kDppRowMirror>(v);
-        if (n == 0) sm[wave][g * 16 + i] = v;
-    }
-    __syncthreads();
-    if (tid < kKvPage && base + tid < s.len && (uint64_t)(base + tid) < a.cap)
-        a.weight[((uint64_t)b * a.c.heads + h) * a.cap + base + tid] +=
-            sm[0][tid] + sm[1][tid] + sm[2][tid] + sm[3][tid];
+    if (d == 0) put_sum(a, row, ts, sum);
 }
 
 template <int D, int CODES, int DTYPE>
@@ -483,14 +325,6 @@ void attend_go(const KvAttend &a, hipStream_t s) {
             hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2>), grid, dim3(kThreads), 0, s, a);
     }
     if (a.rows == 16) hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1>), grid, dim3(kThreads), 0, s, a);
-    if (a.splits > 1) {
-        hipLaunchKernelGGL((k_kv_join<DTYPE>), dim3(a.max_new * a.c.heads * a.group, a.c.batch), dim3(kThreads), 0,
-                           s, a);
-    }
-    if (a.weight)
-        hipLaunchKernelGGL((k_kv_weigh<D, CODES, DTYPE>),
-                           dim3((a.max_len + kKvPage - 1) / kKvPage, a.c.heads, a.c.batch),
-                           dim3(kThreads), 0, s, a);
 }
 
 template <int D, int CODES>
@@ -511,43 +345,67 @@ void attend_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 
 }  // namespace
 
+// Rows up to which a wave takes all rows and its own pages; above, the rows of
+// a workgroup share a page brought to 16 bits once, in LDS.
+constexpr uint64_t kFewRows = 32;
+constexpr uint64_t kTarget = 512;
+
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
                             uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
     KvAttendPlan p{};
     const uint64_t rows = (uint64_t)max_new * group;
     // 32 rows a wave share the codes brought to 16 bits; above 128 dimensions
     // their sums would leave no registers to load ahead
-    p.rows = rows <= 16 || dim > 128 ? 16 : 32;
+    p.rows = rows > kFewRows ? kKvPromptRows : rows <= 16 || dim > 128 ? 16 : 32;
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
     // two workgroups for each of 256 compute units, and a page for each of a
     // workgroup's waves (four a unit: long 111 us instead of 104, draft 55
     // instead of 48, batch 72 instead of 61, scored 54 instead of 61)
-    constexpr uint64_t kTarget = 512;
     uint64_t splits = units ? (kTarget + units - 1) / units : 1;
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
-    if (per > 64 * kWaves) per = 64 * kWaves;  // a lane keeps the offset of each page of its wave
+    // a lane keeps the offset of each page of its wave
+    if (p.rows != kKvPromptRows && per > 64 * kWaves) per = 64 * kWaves;
     p.per_split = (uint32_t)per;
     p.splits = (uint32_t)((pages + per - 1) / per);
     if (p.splits < 1) p.splits = 1;
     const uint64_t all = tokens * heads * group;
     p.part_bytes = p.splits > 1 ? (p.splits * all * (dim + 2) * 4 + 255) / 256 * 256 : 0;
-    p.lse_bytes = scored ? (all * 4 + 255) / 256 * 256 : 0;
-    p.total = p.part_bytes + p.score_bytes + p.lse_bytes;
+    // one row block keeps its scores for the weights (a write and a read of 4
+    // bytes a row and token) where that is less than reading the keys again
+    if (scored && p.row_blocks == 1 && rows * 8 <= dim) {
+        p.score_rows = (uint32_t)rows;
+        p.score_bytes = (uint64_t)batch * heads * pages * rows * kKvPage * 4;
+    }
+    p.sum_bytes = scored ? (all * 8 + 255) / 256 * 256 : 0;
+    p.total = p.part_bytes + p.score_bytes + p.sum_bytes;
     return p;
 }
 
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s) {
-    switch (a.c.dim) {
-        case 64: attend_codes<64>(a, codes, dtype, s); break;
-        case 96: attend_codes<96>(a, codes, dtype, s); break;
-        case 128: attend_codes<128>(a, codes, dtype, s); break;
-        case 192: attend_codes<192>(a, codes, dtype, s); break;
-        case 256: attend_codes<256>(a, codes, dtype, s); break;
-        default: return hipErrorInvalidValue;
+    if (a.rows == kKvPromptRows) {
+        const hipError_t e = launch_kv_prompt(a, codes, dtype, s);
+        if (e != hipSuccess) return e;
+    } else {
+        switch (a.c.dim) {
+            case 64: attend_codes<64>(a, codes, dtype, s); break;
+            case 96: attend_codes<96>(a, codes, dtype, s); break;
+            case 128: attend_codes<128>(a, codes, dtype, s); break;
+            case 192: attend_codes<192>(a, codes, dtype, s); break;
+            case 256: attend_codes<256>(a, codes, dtype, s); break;
+            default: return hipErrorInvalidValue;
+        }
     }
+    if (a.splits > 1) {
+        const dim3 grid(a.max_new * a.c.heads * a.group, a.c.batch);
+        if (dtype == kBf16)
+            hipLaunchKernelGGL((k_kv_join<kBf16>), grid, dim3(kThreads), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_kv_join<kFp16>), grid, dim3(kThreads), 0, s, a);
+    }
+    if (a.weight) return launch_kv_weigh(a, codes, dtype, s);
     return hipGetLastError();
 }
 
