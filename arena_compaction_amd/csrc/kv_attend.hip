@@ -25,7 +25,8 @@
 namespace ac {
 namespace {
 
-template <int D, int CODES, int DTYPE, int R>
+// KEEP: scores are kept for the weights.
+template <int D, int CODES, int DTYPE, int R, bool KEEP>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_attend(KvAttend a) {
     constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 16 * R, kJoin = 4;
     __shared__ f32x4 sm_o[kWaves][R * kJoin * 64];
@@ -86,10 +87,14 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
         get_keys(__builtin_ctzll(todo));
         get_values(__builtin_ctzll(todo));
     }
+    arrived(scales[0]);
+    arrived(scales[1]);
     while (todo) {
         const int i = __builtin_ctzll(todo);
         todo &= todo - 1;
-        const int next = todo ? __builtin_ctzll(todo) : -1;
+        // the last page is loaded once more: loads under a condition would be
+        // waited for as if they had not been issued, all of them at once
+        const int next = todo ? __builtin_ctzll(todo) : i;
         const int base = (p_lo + wave + kWaves * i) * kKvPage;
         const float f = a.scale * kLog2e * lane_f32(scales[0], i);
         const int ei = value_exp(lane_f32(scales[1], i));
@@ -105,8 +110,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
                 for (int rt = 0; rt < R; ++rt) w[rt][tt] = mfma16<DTYPE>(kk, q[rt][st], w[rt][tt]);
             }
         }
-        if (next >= 0) get_keys(next);
-        if (a.scores) {
+        get_keys(next);
+        if constexpr (KEEP) {
             float *to = a.scores + ((uint64_t)b * a.c.heads + h) * a.score_pages * a.score_rows * kKvPage;
             to += (uint64_t)(p_lo + wave + kWaves * i) * a.score_rows * kKvPage;
 #pragma unroll
@@ -164,7 +169,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
                 o[rt][dt] = mfma16<kFp16>(v1, pw[rt][1], o[rt][dt]);
             }
         }
-        if (next >= 0) get_values(next);
+        get_values(next);
     }
     if constexpr (CODES == kE4m3) {
         if (__builtin_amdgcn_ballot_w64(no_numbers != 0)) {
@@ -322,9 +327,12 @@ void attend_go(const KvAttend &a, hipStream_t s) {
     const dim3 grid(a.splits * a.row_blocks, a.c.heads, a.c.batch);
     if constexpr (D <= 128) {
         if (a.rows == 32)
-            hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 2, false>), grid, dim3(kThreads), 0, s, a);
     }
-    if (a.rows == 16) hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1>), grid, dim3(kThreads), 0, s, a);
+    if (a.rows == 16 && a.scores)
+        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1, true>), grid, dim3(kThreads), 0, s, a);
+    else if (a.rows == 16)
+        hipLaunchKernelGGL((k_kv_attend<D, CODES, DTYPE, 1, false>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <int D, int CODES>
@@ -375,7 +383,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     p.part_bytes = p.splits > 1 ? (p.splits * all * (dim + 2) * 4 + 255) / 256 * 256 : 0;
     // one row block keeps its scores for the weights (a write and a read of 4
     // bytes a row and token) where that is less than reading the keys again
-    if (scored && p.row_blocks == 1 && rows * 8 <= dim) {
+    if (scored && rows <= 16 && rows * 8 <= dim) {
         p.score_rows = (uint32_t)rows;
         p.score_bytes = (uint64_t)batch * heads * pages * rows * kKvPage * 4;
     }

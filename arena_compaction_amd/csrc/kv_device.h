@@ -127,6 +127,12 @@ __device__ inline uint64_t lane_u64(uint64_t x, int i) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, i) |
            (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), i) << 32;
 }
+// Waits here for a loaded value (and not at its first use, inside a loop that
+// has younger loads under way).
+template <typename T>
+__device__ inline void arrived(T x) {
+    asm volatile("" ::"v"(x));
+}
 __device__ inline float lane_f32(float x, int i) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
 }

@@ -120,6 +120,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_kv_prompt(KvAtte
             }
             if (nan) sm_nan = 1;
         };
+        arrived(scales[0]);
+        arrived(scales[1]);
         uint64_t todo = good;
         int cur = 0;
         if (todo) {

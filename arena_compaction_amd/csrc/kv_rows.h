@@ -61,12 +61,18 @@ __device__ inline float soft_page(Soft &s, f32x4 (&w)[4], float f, int ei, bool 
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float t = __builtin_fmaf(w[tt][i], f, c);
-            if (edge && tt * 4 + i >= see) t = KV_NEG_INF;
-            w[tt][i] = t;
-            top = fmaxf(top, t);
-        }
+        for (int i = 0; i < 4; ++i) w[tt][i] = __builtin_fmaf(w[tt][i], f, c);
+    if (__builtin_expect(edge, 0)) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tt * 4 + i >= see) w[tt][i] = KV_NEG_INF;
+    }
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, w[tt][i]);
     float fade = 1.0f;
     if (__builtin_amdgcn_ballot_w64(top > (first ? KV_NEG_INF : kRoom))) {
         top = across_groups(top, [](float x, float y) { return fmaxf(x, y); });
