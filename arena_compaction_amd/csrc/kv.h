@@ -72,7 +72,7 @@ struct KvAttend {
     uint32_t rows;               // query rows of a workgroup
     uint32_t row_blocks;
     float *part;     // [splits][tokens * heads * group][dim + 2]
-    float *scores;   // [batch][heads][score_pages][score_rows][64], or null
+    float *scores;   // [batch][heads][score_pages][tile 4][group 4][score_rows][4], or null
     uint32_t score_pages, score_rows;
     float2 *sums;    // [tokens * heads * group]: m and 1 / sum of 2^(t - m), or null
 };
@@ -116,6 +116,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_prompt(const KvAttend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_finish(const KvAttend &a, int dtype, hipStream_t s);
 hipError_t launch_kv_weigh(const KvAttend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s);
 hipError_t launch_kv_zero(uint64_t *p, hipStream_t s);

@@ -155,7 +155,8 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     const KvAttendPlan p = plan_of(a);
     if (a->tokens) {
         if ((uint64_t)p.splits * p.row_blocks * c->batch * c->heads > kMaxGrid ||
-            (uint64_t)a->max_new * c->heads * a->group > kMaxGrid)
+            (uint64_t)a->max_new * c->heads * a->group +
+                    (a->weight_dev ? (a->max_len / 256 + 1ull) * c->heads : 0) > kMaxGrid)
             return DEFRAG_EINVAL;
         rc = check_ws(ws_dev, ws_bytes, p.total);
         if (rc) return rc;

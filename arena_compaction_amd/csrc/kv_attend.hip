@@ -19,7 +19,7 @@
 // one row: the maximum needs two steps across lanes, the rescaling none, and
 // the weights are the next product's operand where they are.  Four waves
 // share a workgroup's rows and join through LDS; workgroups split a long
-// cache and k_kv_join joins their parts.
+// cache and k_kv_finish joins their parts.
 #include "kv_rows.h"
 
 namespace ac {
@@ -114,14 +114,10 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
         if constexpr (KEEP) {
             float *to = a.scores + ((uint64_t)b * a.c.heads + h) * a.score_pages * a.score_rows * kKvPage;
             to += (uint64_t)(p_lo + wave + kWaves * i) * a.score_rows * kKvPage;
+            if (n < rows) {  // one row block of one tile
 #pragma unroll
-            for (int rt = 0; rt < R; ++rt) {
-                const int r = rb * kRows + rt * 16 + n;
-                if (r < rows) {
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt)
-                        *reinterpret_cast<f32x4 *>(to + r * kKvPage + g * 16 + tt * 4) = w[rt][tt] * f;
-                }
+                for (int tt = 0; tt < 4; ++tt)
+                    *reinterpret_cast<f32x4 *>(to + ((tt * 4 + g) * (int)a.score_rows + n) * 4) = w[0][tt] * f;
             }
         }
         const bool edge = base + kKvPage > see_least;
@@ -248,80 +244,6 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
     }
 }
 
-// Joins the parts of rows whose cache was split: one workgroup a row and
-// head.  Each wave takes every fourth part, 64 of them at a time with a
-// part's maximum and sum in a lane, so that all loads are under way at once.
-template <int DTYPE>
-__global__ __launch_bounds__(kThreads) void k_kv_join(KvAttend a) {
-    constexpr int kMost = (int)kKvMaxDim / 64;
-    __shared__ float sm_v[kWaves][kKvMaxDim], sm_m[kWaves], sm_l[kWaves];
-    const uint32_t b = blockIdx.y, D = a.c.dim;
-    const int wave = wave_uniform(threadIdx.x / 64), lane = threadIdx.x % 64, G = (int)a.group;
-    const uint64_t heads = (uint64_t)a.c.heads * G, all = a.tokens * heads;
-    const uint64_t t = blockIdx.x / heads, hq = blockIdx.x % heads;
-    bool bad;
-    const Seq s = sequence(a, b, &bad);
-    if (t >= (uint64_t)s.count) return;
-    const int pages = block_pages(a, s, (int)((t * G + hq % G) / a.rows));
-    const int active = (pages + (int)a.per_split - 1) / (int)a.per_split;
-    if (active <= 1) return;
-    const uint64_t row = (s.first + t) * heads + hq;
-    const float *ml = a.part + (uint64_t)a.splits * all * D + row * 2;
-    float top = KV_NEG_INF, sum = 0.0f, v[kMost] = {};
-    for (int k0 = wave; k0 < active; k0 += kWaves * 64) {
-        const int mine = k0 + lane * kWaves;
-        f32x2 x = {KV_NEG_INF, 0.0f};
-        if (mine < active) x = *reinterpret_cast<const f32x2 *>(ml + mine * all * 2);
-        const float m = x[0], l = x[1];
-        const float now = fmaxf(top, wave_reduce(m, [](float p, float q) { return fmaxf(p, q); }));
-        const float ts = now == KV_NEG_INF ? 0.0f : now;
-        const float fade = __builtin_amdgcn_exp2f(m - ts), old = __builtin_amdgcn_exp2f(top - ts);
-        top = now;
-        sum = sum * old + wave_reduce(l * fade, [](float p, float q) { return p + q; });
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) v[i] *= old;
-        const int n = (active - k0 + kWaves - 1) / kWaves < 64 ? (active - k0 + kWaves - 1) / kWaves : 64;
-        const float *src = a.part + (k0 * all + row) * D;
-        for (int k = 0; k < n; k += 8) {
-            float x[8][kMost];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float *p = src + (uint64_t)(k + u < n ? k + u : n - 1) * kWaves * all * D;
-#pragma unroll
-                for (int i = 0; i < kMost; ++i) x[u][i] = lane + 64 * i < (int)D ? p[lane + 64 * i] : 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float w = k + u < n ? lane_f32(fade, k + u < n ? k + u : 0) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < kMost; ++i)
-                    if (k + u < n) v[i] += x[u][i] * w;
-            }
-        }
-    }
-    if (lane == 0) {
-        sm_m[wave] = top;
-        sm_l[wave] = sum;
-    }
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) sm_v[wave][lane + 64 * i] = v[i];
-    __syncthreads();
-    top = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    const float ts = top == KV_NEG_INF ? 0.0f : top;
-    float fade[kWaves], out = 0.0f;
-    sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-        fade[k] = __builtin_amdgcn_exp2f(sm_m[k] - ts);
-        sum += sm_l[k] * fade[k];
-    }
-    const uint32_t d = threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) out += sm_v[k][d] * fade[k];
-    if (d < D) a.out[row * D + d] = (uint16_t)pack2<DTYPE>(sum == 0.0f ? 0.0f : out / sum, 0.0f);
-    if (d == 0) put_sum(a, row, ts, sum);
-}
-
 template <int D, int CODES, int DTYPE>
 void attend_go(const KvAttend &a, hipStream_t s) {
     const dim3 grid(a.splits * a.row_blocks, a.c.heads, a.c.batch);
@@ -356,7 +278,6 @@ void attend_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 // Rows up to which a wave takes all rows and its own pages; above, the rows of
 // a workgroup share a page brought to 16 bits once, in LDS.
 constexpr uint64_t kFewRows = 32;
-constexpr uint64_t kTarget = 512;
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
                             uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
@@ -368,10 +289,13 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    // two workgroups for each of 256 compute units, and a page for each of a
-    // workgroup's waves (four a unit: long 111 us instead of 104, draft 55
-    // instead of 48, batch 72 instead of 61, scored 54 instead of 61)
-    uint64_t splits = units ? (kTarget + units - 1) / units : 1;
+    // Workgroups in flight are 3 a compute unit with 16 rows, 2 with more.
+    // The lengths differ, so few heads are cut into a third more pieces than
+    // that, which even out; where the heads alone nearly fill the unit, a cut
+    // leaves a few pieces over and costs more than it evens out (64 sequences
+    // x 8 heads: whole 62 us, in halves 73).
+    const uint64_t target = p.rows == 16 ? 1024 : 512;
+    uint64_t splits = units == 0 || units >= 512 ? 1 : (target + units - 1) / units;
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave
@@ -394,8 +318,8 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
 
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s) {
     if (a.rows == kKvPromptRows) {
-        const hipError_t e = launch_kv_prompt(a, codes, dtype, s);
-        if (e != hipSuccess) return e;
+        const hipError_t p = launch_kv_prompt(a, codes, dtype, s);
+        if (p != hipSuccess) return p;
     } else {
         switch (a.c.dim) {
             case 64: attend_codes<64>(a, codes, dtype, s); break;
@@ -406,14 +330,9 @@ hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t
             default: return hipErrorInvalidValue;
         }
     }
-    if (a.splits > 1) {
-        const dim3 grid(a.max_new * a.c.heads * a.group, a.c.batch);
-        if (dtype == kBf16)
-            hipLaunchKernelGGL((k_kv_join<kBf16>), grid, dim3(kThreads), 0, s, a);
-        else
-            hipLaunchKernelGGL((k_kv_join<kFp16>), grid, dim3(kThreads), 0, s, a);
-    }
-    if (a.weight) return launch_kv_weigh(a, codes, dtype, s);
+    const hipError_t e = launch_kv_finish(a, dtype, s);
+    if (e != hipSuccess) return e;
+    if (a.weight && !a.scores) return launch_kv_weigh(a, codes, dtype, s);
     return hipGetLastError();
 }
 
