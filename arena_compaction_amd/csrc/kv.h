@@ -47,7 +47,6 @@ struct KvAppend {
     uint64_t tokens;
     const int32_t *starts;  // batch + 1, or null: one token a sequence
     uint32_t max_new;
-    bool vec_k, vec_v;      // 16-byte loads are aligned
     float *weight;          // [batch][heads][cap], or null
     int32_t *pos;
     const int32_t *first_pos;
@@ -61,7 +60,6 @@ struct KvAttend {
     uint64_t tokens;
     const int32_t *starts;
     uint32_t max_new, max_len, group;
-    bool vec_q;
     float scale;
     uint16_t *out;   // [tokens][heads * group][dim]
     float *lse;      // [tokens][heads * group], or null

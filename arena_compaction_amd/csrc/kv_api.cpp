@@ -38,11 +38,6 @@ KvCache cache_of(const defrag_kv_cache *c) {
                    reinterpret_cast<unsigned long long *>(c->n_invalid_dev)};
 }
 
-// 16-bit rows read 8 elements at a time.
-bool can_vector(const void *p, int64_t row, int64_t head) {
-    return aligned(p, 16) && row % 8 == 0 && head % 8 == 0;
-}
-
 int dtype_ok(int32_t t) { return t == DEFRAG_KV_BF16 || t == DEFRAG_KV_FP16; }
 
 int check_new(const defrag_kv_cache *c, const int32_t *starts, uint64_t tokens, uint32_t max_new) {
@@ -135,9 +130,7 @@ int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
     const KvAppend k{cache_of(c),
                      static_cast<const uint16_t *>(a->k_dev), static_cast<const uint16_t *>(a->v_dev),
                      a->k_row, a->k_head, a->v_row, a->v_head, a->tokens, a->starts_dev, a->max_new,
-                     can_vector(a->k_dev, a->k_row, a->k_head),
-                     can_vector(a->v_dev, a->v_row, a->v_head), a->weight_dev, a->pos_dev,
-                     a->first_pos_dev, a->weight_stride};
+                     a->weight_dev, a->pos_dev, a->first_pos_dev, a->weight_stride};
     return launch_kv_append(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
 }
 
@@ -158,6 +151,10 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
             (uint64_t)a->max_new * c->heads * a->group +
                     (a->weight_dev ? (a->max_len / 256 + 1ull) * c->heads : 0) > kMaxGrid)
             return DEFRAG_EINVAL;
+        // the weights' workgroups have up to 1024 lanes
+        if (a->weight_dev && !p.score_bytes &&
+            (a->max_len / kKvPage + 1ull) * c->batch * c->heads > kMaxGrid / 4)
+            return DEFRAG_EINVAL;
         rc = check_ws(ws_dev, ws_bytes, p.total);
         if (rc) return rc;
     }
@@ -174,7 +171,6 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     k.max_new = a->max_new;
     k.max_len = a->max_len;
     k.group = a->group;
-    k.vec_q = can_vector(a->q_dev, a->q_row, a->q_head);
     k.scale = a->scale;
     k.out = static_cast<uint16_t *>(a->out_dev);
     k.lse = a->lse_dev;

@@ -23,16 +23,11 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kTileStride = kKvPage + 4;  // bytes; rows start in other banks
 
+// (2-byte alignment will do: gfx950 reads 16 bytes from any address)
 template <int DTYPE>
-__device__ inline void load8(const uint16_t *p, bool vec, float (&x)[8]) {
+__device__ inline void load8(const uint16_t *p, float (&x)[8]) {
     uint16_t h[8];
-    if (vec) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
-        __builtin_memcpy(h, &w, 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = p[i];
-    }
+    __builtin_memcpy(h, p, 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = to_float<DTYPE>(h[i]);
 }
@@ -78,8 +73,8 @@ __global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
         if (item < n) {
             const uint64_t t = src + item / kPer;
             const int d = item % kPer * 8;
-            load8<DTYPE>(a.k + (int64_t)t * a.k_row + h * a.k_head + d, a.vec_k, kx[i]);
-            load8<DTYPE>(a.v + (int64_t)t * a.v_row + h * a.v_head + d, a.vec_v, vx[i]);
+            load8<DTYPE>(a.k + (int64_t)t * a.k_row + h * a.k_head + d, kx[i]);
+            load8<DTYPE>(a.v + (int64_t)t * a.v_row + h * a.v_head + d, vx[i]);
         }
     }
     const int ke0 = exp_of_pow2(sc[0]), ve0 = exp_of_pow2(sc[1]);

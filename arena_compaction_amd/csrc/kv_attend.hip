@@ -124,8 +124,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
         u32x4 pw[R][2];
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
-            const float fade = soft_page(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
-            pack_weights(w[rt], pw[rt]);
+            const float fade = soft_scores(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
+            float sum = 0.0f;
+            soft_weights(w[rt][0], w[rt][1], pw[rt][0], sum);
+            soft_weights(w[rt][2], w[rt][3], pw[rt][1], sum);
+            soft[rt].l = __builtin_fmaf(sum, pow2(-ei), soft[rt].l);
             if (__builtin_amdgcn_ballot_w64(fade != 1.0f)) {
 #pragma unroll
                 for (int dt = 0; dt < kTiles; ++dt)

@@ -179,89 +179,116 @@ __global__ __launch_bounds__(kThreads) void k_kv_finish(KvAttend a, uint32_t joi
 }
 
 template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(D <= 96 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
-    constexpr int kSteps = D / 32, kN = D <= 96 ? 16 : 8, kStride = kN * 16;  // waves, rows a turn
+__global__ __launch_bounds__(D <= 64 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
+    constexpr int kSteps = D / 32, kN = D <= 64 ? 16 : 8;  // waves
+    constexpr int kPieces = D / 8, kPitch = kPieces + 1;  // of 16 bytes; odd, so that rows start in other banks
     __shared__ float sm[kN][kKvPage];
-    const uint32_t h = blockIdx.y, b = blockIdx.z;
+    __shared__ u32x4 sm_q[kN][16 * kPitch];
+    // heads first: the first pages, which most rows see, start first
+    const uint32_t units = a.c.heads * a.c.batch, unit = blockIdx.x % units;
+    const uint32_t h = unit % a.c.heads, b = unit / a.c.heads;
     const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
     const int n = lane % 16, g = lane / 16, G = (int)a.group;
     bool bad;
     const Seq s = sequence(a, b, &bad);
-    const int p = blockIdx.x, base = p * kKvPage;
+    const int p = (int)(blockIdx.x / units), base = p * kKvPage;
     if (base >= s.len || s.count == 0) return;
     const uint64_t off = wave_uniform(page_offset(a.c, b, p));
     if (off == kNoPage) return;
     const float f = a.scale * kLog2e * page_scales(a.c, a.c.arena + off, h)[0];
     u32x4 kk[4][kSteps];
     {
-        uint32_t kraw[4][D / 16];
-        load_keys<D>(a.c.arena + off + (uint64_t)h * 2 * kKvPage * D, lane, kraw);
+        const uint8_t *strip = a.c.arena + off + (uint64_t)h * 2 * kKvPage * D + g * 8;
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-            for (int st = 0; st < kSteps; ++st)
-                kk[tt][st] = widen8<CODES, DTYPE>(kraw[tt][2 * st], kraw[tt][2 * st + 1]);
+            for (int st = 0; st < kSteps; ++st) {
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(strip + token_of(tt, n) * D + st * 32);
+                kk[tt][st] = widen8<CODES, DTYPE>(x[0], x[1]);
+            }
     }
     float acc[16] = {};
     const int rows = s.count * G;
     const uint64_t heads = (uint64_t)a.c.heads * G;
-    // this lane's row, its token and head among the group's, and where its
-    // query and sums are; kStride rows on in each turn
-    int r = (base > s.had ? (base - s.had) * G / 16 * 16 : 0) + wave * 16 + n;  // earlier rows see nothing here
-    int t = r / G, hg = r - t * G;
-    const int dt = kStride / G, dg = kStride - dt * G;
-    const uint16_t *q = a.q + (int64_t)(s.first + t) * a.q_row + (int64_t)(h * G + hg) * a.q_head;
-    const float2 *sums = a.sums + (s.first + t) * heads + (uint64_t)h * G + hg;
-    const int64_t q_on = dt * a.q_row + dg * a.q_head, q_wrap = a.q_row - G * a.q_head;
-    const int64_t s_on = (int64_t)dt * heads + dg, s_wrap = (int64_t)heads - G;
-    u32x4 qn[kSteps];
-    float2 mln = make_float2(0.0f, 0.0f);
-    auto load = [&]() {
+    // Tiles of 16 rows, every kN-th, from the last one down, since all pages'
+    // rows end there: workgroups that start together read the same queries
+    // together, out of L2.  A tile's first token is the wave's (t0) and its
+    // address scalar; a lane adds where its row lies from there, which is the
+    // same in every turn where the group's heads divide the rows of a turn.
+    // Queries are loaded with neighbouring lanes on neighbouring bytes and
+    // dealt out through LDS, each wave's own: as the operand wants them,
+    // neighbouring lanes on neighbouring rows, L1 would serve 16 bytes at a
+    // time, and be what the kernel waits for.
+    const int least = (base > s.had ? (base - s.had) * G / 16 : 0) + wave;  // earlier rows see nothing here
+    const int tiles = (rows + 15) / 16;
+    const int turns = tiles > least ? (tiles - least + kN - 1) / kN : 0;
+    const uint32_t by_group = ((1u << 20) + G - 1) / G;  // v / G = v * by_group >> 20 for v < G + 16
+    const bool same = kN * 16 % G == 0;
+    const int see0 = s.had + 1 - base - g * 16;
+    int64_t q_at[kSteps];  // in elements, from the tile's first token
+    int sum_at = 0, lane_t = 0;
+    auto place = [&](int v0, int most) __attribute__((always_inline)) {  // v0: the tile's first row less t0 * G
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) qn[st] = u32x4{0, 0, 0, 0};
-        if (r < rows) {
-            mln = *sums;
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) qn[st] = load_q8(q + dim_of<D>(st, g), a.vec_q);
+        for (int i = 0; i < kSteps; ++i) {
+            const int item = i * 64 + lane, row = item / kPieces;
+            const int v = v0 + (row < most ? row : 0), t = (int)((uint32_t)v * by_group >> 20);
+            q_at[i] = t * a.q_row + (v - t * G) * a.q_head + item % kPieces * 8;
         }
+        const int v = v0 + (n < most ? n : 0);
+        lane_t = (int)((uint32_t)v * by_group >> 20);
+        sum_at = lane_t * (int)heads + (v - lane_t * G);
     };
-    load();
-    const int turns = (rows - (r - n) + kStride - 1) / kStride;  // the same in all lanes
-    for (int x = 0; x < turns; ++x) {
-        const int see = r < rows ? s.had + t + 1 - base - g * 16 : 0;
-        const float2 ml = mln;
+    u32x4 q[kSteps];
+    float2 ml = make_float2(0.0f, 0.0f);
+    int see = 0;
+    auto load = [&](int x, bool last) __attribute__((always_inline)) {  // last: some rows may not be there
+        const int t0 = wave_uniform(x * 16 / G), v0 = x * 16 - t0 * G, most = last ? rows - x * 16 : 16;
+        if (last || !same) place(v0, most);
+        const uint16_t *tile = a.q + (int64_t)(s.first + t0) * a.q_row + (int64_t)h * G * a.q_head;
+        ml = a.sums[(s.first + t0) * heads + (uint64_t)h * G + sum_at];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) q[i] = load_q8(tile + q_at[i]);
+        see = n < most ? see0 + t0 + lane_t : 0;
+        if (last && same) place(v0, 16);
+    };
+    u32x4 *const mine = sm_q[wave];
+    int x = least + (turns - 1) * kN;
+    if (turns) load(x, true);
+    for (int k = 0; k < turns; ++k) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int item = i * 64 + lane;
+            mine[item / kPieces * kPitch + item % kPieces] = q[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u32x4 qq[kSteps];
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) qq[st] = mine[n * kPitch + st * 4 + g];
+        const float2 now = ml;
+        const int see_now = see;
+        const bool edge = k == 0 || x * 16 / G + s.had + 1 - base < 64;  // some row misses some token
+        x = x - kN > least ? x - kN : least;                             // (after the last turn: its own rows again)
+        load(x, false);
         f32x4 w[4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
             w[tt] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int st = 0; st < kSteps; ++st) w[tt] = mfma16<DTYPE>(kk[tt][st], qn[st], w[tt]);
+            for (int st = 0; st < kSteps; ++st) w[tt] = mfma16<DTYPE>(kk[tt][st], qq[st], w[tt]);
         }
-        r += kStride;
-        t += dt;
-        hg += dg;
-        q += q_on;
-        sums += s_on;
-        if (hg >= G) {
-            hg -= G;
-            ++t;
-            q += q_wrap;
-            sums += s_wrap;
-        }
-        load();
-        if (__builtin_amdgcn_ballot_w64(see < 16)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i / 4][i % 4], f, -ml.x));
-                if (i < see) acc[i] = __builtin_fmaf(e, ml.y, acc[i]);
-            }
-        } else {
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(w[i / 4][i % 4], f, -now.x);
+        if (edge) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i / 4][i % 4], f, -ml.x));
-                acc[i] = __builtin_fmaf(e, ml.y, acc[i]);
-            }
+            for (int i = 0; i < 16; ++i)
+                if (i >= see_now) w[i / 4][i % 4] = KV_NEG_INF;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(w[i / 4][i % 4]), now.y, acc[i]);
+        __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -283,7 +310,7 @@ __global__ __launch_bounds__(D <= 96 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
 
 template <int D, int CODES>
 void weigh_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid((a.max_len + kKvPage - 1) / kKvPage, a.c.heads, a.c.batch), block(D <= 96 ? 1024 : 512);
+    const dim3 grid(a.c.heads * a.c.batch * ((a.max_len + kKvPage - 1) / kKvPage)), block(D <= 64 ? 1024 : 512);
     if (dtype == kBf16)
         hipLaunchKernelGGL((k_kv_weigh<D, CODES, kBf16>), grid, block, 0, s, a);
     else

@@ -100,12 +100,11 @@ __device__ inline void load_keys(const uint8_t *strip, int lane, uint32_t (&k)[4
     }
 }
 
-// Eight 16-bit numbers of a query row; zeros for a row that is not there.
-__device__ inline u32x4 load_q8(const uint16_t *p, bool vec) {
-    if (vec) return *reinterpret_cast<const u32x4 *>(p);
+// Eight 16-bit numbers; 2-byte alignment will do (gfx950 reads 16 bytes from
+// any address, in one instruction).
+__device__ inline u32x4 load_q8(const uint16_t *p) {
     u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+    __builtin_memcpy(&r, p, 16);
     return r;
 }
 

@@ -3,12 +3,12 @@
 //
 // The mathematics is that of kv_attend.hip; what differs is who holds what.
 // With many rows the cost is the matrix products and, per score, an exponent,
-// so a workgroup takes 128 rows, 32 a wave, and all its waves go over the
-// same pages: each page is loaded once, its codes brought to 16 bits once (a
-// quarter of a page a wave) and put into LDS in the very order in which the
-// matrix instructions' operands are read, 16 bytes a lane, in a line.  Two
-// pages are in LDS, one being summed and one being filled, while the codes of
-// a third are on their way.
+// so a workgroup takes 128 rows, and all its waves go over the same pages:
+// each page is loaded once, its codes brought to 16 bits once (a share of the
+// page a wave) and put into LDS in the very order in which the matrix
+// instructions' operands are read, 16 bytes a lane, in a line.  Two pages are
+// in LDS, one being summed and one being filled, while the codes of a third
+// are on their way.
 //
 // Workgroups of one key/value head run on one XCD where the heads are a
 // multiple of 8, so that its pages stay in that XCD's L2; the last rows,
@@ -18,10 +18,19 @@
 namespace ac {
 namespace {
 
+// 32 rows a wave; above 128 dimensions 16, whose sums and queries leave two
+// waves a SIMD their registers.
+template <int D>
+constexpr int kPromptWaves = D <= 128 ? 4 : 8;
+
 template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_kv_prompt(KvAttend a) {
-    constexpr int R = 2, kSteps = D / 32, kTiles = D / 16, kRows = (int)kKvPromptRows;
-    constexpr int kKeyJobs = (D + 63) / 64, kValueJobs = (kTiles + kWaves - 1) / kWaves;
+__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_prompt(KvAttend a) {
+    constexpr int kN = kPromptWaves<D>, kRows = (int)kKvPromptRows, R = kRows / 16 / kN;
+    constexpr int kSteps = D / 32, kTiles = D / 16;
+    constexpr int kBatch = kTiles % 4 ? 3 : 4, kBatches = kTiles / kBatch;  // value tiles read at a time
+    // a wave's share of a page: of the keys' 4 tiles x chunks of 64 dimensions
+    // and of the values' tiles, every kN-th
+    constexpr int kChunks = (D + 63) / 64, kKeyJobs = (4 * kChunks + kN - 1) / kN, kValueJobs = (kTiles + kN - 1) / kN;
     __shared__ u32x4 sm_k[2][4 * kSteps * 64], sm_v[2][kTiles * 2 * 64];
     __shared__ int sm_nan;
     const uint32_t units = a.c.batch * a.c.heads, unit = blockIdx.x % units, piece = blockIdx.x / units;
@@ -69,112 +78,192 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void k_kv_prompt(KvAtte
         if (off != kNoPage) scales = *reinterpret_cast<const f32x2 *>(page_scales(a.c, a.c.arena + off, h));
         if (counts && __builtin_popcountll(good) != np)
             atomicAdd(a.c.n_invalid, (unsigned long long)(np - __builtin_popcountll(good)));
-        // a wave's share of a page: key tile `wave`, and every fourth of the value tiles
-        u32x4 kr[kKeyJobs], vr[kValueJobs];
-        auto load = [&](int i) {
+        struct Raw {
+            u32x4 k[kKeyJobs], v[kValueJobs];
+        };
+        Raw ra, rz;
+        // (where the waves outnumber what is left, the last piece again: loads
+        // are never under a condition, see k_kv_attend)
+        auto load = [&](int i, Raw &r) __attribute__((always_inline)) {
             const uint8_t *strip = strips + lane_u64(off, i);
-            const uint8_t *row = strip + token_of(wave, n) * D;
+            const uint8_t *row = strip + token_of(wave % 4, n) * D;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) kr[c] = *reinterpret_cast<const u32x4 *>(row + c * 64 + g * 16);
-            if constexpr (D % 64 != 0) {
-                const u32x2 x = *reinterpret_cast<const u32x2 *>(row + D / 64 * 64 + g * 8);
-                kr[kKeyJobs - 1] = u32x4{x[0], x[1], 0, 0};
+            for (int x = 0; x < kKeyJobs; ++x) {
+                if (D % 64 != 0 && x == kChunks - 1) {
+                    const u32x2 w = *reinterpret_cast<const u32x2 *>(row + x * 64 + g * 8);
+                    r.k[x] = u32x4{w[0], w[1], 0, 0};
+                } else {
+                    const int c = wave / 4 + x * (kN / 4);
+                    r.k[x] = *reinterpret_cast<const u32x4 *>(row + (c < kChunks ? c : kChunks - 1) * 64 + g * 16);
+                }
             }
 #pragma unroll
-            for (int c = 0; c < kValueJobs; ++c) {
-                const int dt = wave + c * kWaves;
-                if (dt < kTiles)
-                    vr[c] = *reinterpret_cast<const u32x4 *>(strip + kKvPage * D + (dt * 16 + n) * kKvPage + g * 16);
+            for (int x = 0; x < kValueJobs; ++x) {
+                const int dt = wave + x * kN, at = kTiles % kN == 0 || dt < kTiles ? dt : kTiles - 1;
+                r.v[x] = *reinterpret_cast<const u32x4 *>(strip + kKvPage * D + (at * 16 + n) * kKvPage + g * 16);
             }
         };
-        auto store = [&](int i, int to) {
+        // values that are not the cache's own, or are no numbers (as in
+        // k_kv_attend); few pages have any
+        auto clean = [&](int i, Raw &r) __attribute__((always_inline)) {
             const int base = (p0 + i) * kKvPage;
+            if (base + kKvPage > s.len) {
 #pragma unroll
-            for (int c = 0; c < kKeyJobs; ++c) {
-                sm_k[to][(wave * kSteps + 2 * c) * 64 + lane] = widen8<CODES, DTYPE>(kr[c][0], kr[c][1]);
-                if (2 * c + 1 < kSteps)
-                    sm_k[to][(wave * kSteps + 2 * c + 1) * 64 + lane] = widen8<CODES, DTYPE>(kr[c][2], kr[c][3]);
+                for (int c = 0; c < kValueJobs; ++c)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) r.v[c][x] = only_there(r.v[c][x], s.len - base - g * 16 - 4 * x);
             }
-            uint32_t nan = 0;
+            if constexpr (CODES == kE4m3) {
+                if (base + kKvPage > block_least) {
+                    uint32_t nan = 0;
 #pragma unroll
-            for (int c = 0; c < kValueJobs; ++c) {
-                const int dt = wave + c * kWaves;
-                if (base + kKvPage > s.len) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) vr[c][x] = only_there(vr[c][x], s.len - base - g * 16 - 4 * x);
-                }
-                if constexpr (CODES == kE4m3) {  // as in k_kv_attend
-                    if (base + kKvPage > block_least && dt < kTiles) {
+                    for (int c = 0; c < kValueJobs; ++c) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t no = nan_codes(vr[c][x]);
-                            vr[c][x] &= ~((no >> 7) * 255u);
+                            const uint32_t no = nan_codes(r.v[c][x]);
+                            r.v[c][x] &= ~((no >> 7) * 255u);
                             nan |= no;
                         }
                     }
-                }
-                if (dt < kTiles) {
-                    sm_v[to][dt * 128 + lane] = widen8<CODES, kFp16>(vr[c][0], vr[c][1]);
-                    sm_v[to][dt * 128 + 64 + lane] = widen8<CODES, kFp16>(vr[c][2], vr[c][3]);
+                    if (nan) sm_nan = 1;
                 }
             }
-            if (nan) sm_nan = 1;
+        };
+        auto store_keys = [&](int to, int x, Raw &r) __attribute__((always_inline)) {
+            const int c = wave / 4 + x * (kN / 4);
+            if (4 * kChunks % kN == 0 || c < kChunks) {
+                u32x4 *p = &sm_k[to][(wave % 4 * kSteps + 2 * c) * 64 + lane];
+                p[0] = widen8<CODES, DTYPE>(r.k[x][0], r.k[x][1]);
+                if (D % 64 == 0 || x != kChunks - 1) p[64] = widen8<CODES, DTYPE>(r.k[x][2], r.k[x][3]);
+            }
+        };
+        auto store_values = [&](int to, int x, Raw &r) __attribute__((always_inline)) {
+            const int dt = wave + x * kN;
+            if (kTiles % kN == 0 || dt < kTiles) {
+                sm_v[to][dt * 128 + lane] = widen8<CODES, kFp16>(r.v[x][0], r.v[x][1]);
+                sm_v[to][dt * 128 + 64 + lane] = widen8<CODES, kFp16>(r.v[x][2], r.v[x][3]);
+            }
+        };
+        auto store = [&](int to, Raw &r) __attribute__((always_inline)) {
+#pragma unroll
+            for (int c = 0; c < kKeyJobs; ++c) store_keys(to, c, r);
+#pragma unroll
+            for (int c = 0; c < kValueJobs; ++c) store_values(to, c, r);
         };
         arrived(scales[0]);
         arrived(scales[1]);
+        // page i is summed from LDS while the next one's codes, loaded two
+        // pages before, are brought to 16 bits, and a third page's are loaded
         uint64_t todo = good;
-        int cur = 0;
-        if (todo) {
-            load(__builtin_ctzll(todo));
-            store(__builtin_ctzll(todo), 0);
+        auto take = [&]() __attribute__((always_inline)) {
+            const int i = todo ? __builtin_ctzll(todo) : -1;
+            todo &= todo - 1;
+            return i;
+        };
+        int i = take(), next = take(), after = -1;
+        if (i >= 0) {
+            load(i, ra);
+            load(next >= 0 ? next : i, rz);
+            clean(i, ra);
+            store(0, ra);
             __syncthreads();
         }
-        while (todo) {
-            const int i = __builtin_ctzll(todo), base = (p0 + i) * kKvPage;
-            todo &= todo - 1;
-            const int next = todo ? __builtin_ctzll(todo) : -1;
-            if (next >= 0) load(next);
+        // the page in buffer `cur`; the next one's codes are in `now`, those
+        // of the one after it go to `then`
+        auto sum_page = [&](const int cur, Raw &now, Raw &then) __attribute__((always_inline)) {
+            const int base = (p0 + i) * kKvPage;
+            after = take();
+            load(after >= 0 ? after : i, then);
+            if (next >= 0) clean(next, now);
             if (base < most) {
                 const float f = a.scale * kLog2e * lane_f32(scales[0], i);
                 const int ei = value_exp(lane_f32(scales[1], i));
+                // Operands are read a stage ahead of their products; nothing
+                // moves across the stages' borders, or the reads would sink to
+                // where they are used and be waited for one by one.
                 f32x4 w[R][4];
+                u32x4 kk[2][kSteps], vv[2][kBatch];
+                auto read_keys = [&](int tt) {
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st) kk[tt % 2][st] = sm_k[cur][(tt * kSteps + st) * 64 + lane];
+                };
+                auto read_values = [&](int at) {  // batch `at` of the first half's, then the second's
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        vv[at % 2][k] =
+                            sm_v[cur][(at % kBatches * kBatch + k) * 128 + at / kBatches * 64 + lane];
+                };
+                read_keys(0);
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt) {
+                    if (tt < 3)
+                        read_keys(tt + 1);
+                    else
+                        read_values(0);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int rt = 0; rt < R; ++rt) w[rt][tt] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int st = 0; st < kSteps; ++st) {
-                        const u32x4 kk = sm_k[cur][(tt * kSteps + st) * 64 + lane];
+                    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-                        for (int rt = 0; rt < R; ++rt) w[rt][tt] = mfma16<DTYPE>(kk, q[rt][st], w[rt][tt]);
-                    }
+                        for (int rt = 0; rt < R; ++rt) w[rt][tt] = mfma16<DTYPE>(kk[tt % 2][st], q[rt][st], w[rt][tt]);
+                    // a share of the next page (of the last: what is there once more)
+#pragma unroll
+                    for (int c = 0; c < kKeyJobs; ++c)
+                        if (c % 4 == tt) store_keys(cur ^ 1, c, now);
+#pragma unroll
+                    for (int c = 0; c < kValueJobs; ++c)
+                        if ((kKeyJobs + c) % 4 == tt) store_values(cur ^ 1, c, now);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                u32x4 pw[R][2];
+                float fade[R];
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt)
+                    fade[rt] = soft_scores(soft[rt], w[rt], f, ei, base + kKvPage > least, lim[rt] - base - g * 16);
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
-                    const float fade =
-                        soft_page(soft[rt], w[rt], f, ei, base + kKvPage > least, lim[rt] - base - g * 16);
-                    pack_weights(w[rt], pw[rt]);
-                    if (__builtin_amdgcn_ballot_w64(fade != 1.0f)) {
+                    if (__builtin_amdgcn_ballot_w64(fade[rt] != 1.0f)) {
 #pragma unroll
                         for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) o[rt][dt][x] *= fade;
+                            for (int x = 0; x < 4; ++x) o[rt][dt][x] *= fade[rt];
                     }
                 }
+                // the first half's products run beside the second half's exponents
+                float sum[R] = {};
+                u32x4 pw[R][2];
 #pragma unroll
-                for (int dt = 0; dt < kTiles; ++dt) {
+                for (int rt = 0; rt < R; ++rt) soft_weights(w[rt][0], w[rt][1], pw[rt][0], sum[rt]);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const u32x4 vv = sm_v[cur][dt * 128 + x * 64 + lane];
+                for (int at = 0; at < 2 * kBatches; ++at) {
+                    if (at + 1 < 2 * kBatches) read_values(at + 1);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int rt = 0; rt < R; ++rt) o[rt][dt] = mfma16<kFp16>(vv, pw[rt][x], o[rt][dt]);
-                    }
+                    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                        for (int rt = 0; rt < R; ++rt) {
+                            f32x4 &to = o[rt][at % kBatches * kBatch + k];
+                            to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches], to);
+                        }
+#pragma unroll
+                    for (int rt = 0; rt < R; ++rt)
+                        if (at == (rt < kBatches ? rt : kBatches - 1))
+                            soft_weights(w[rt][2], w[rt][3], pw[rt][1], sum[rt]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) soft[rt].l = __builtin_fmaf(sum[rt], pow2(-ei), soft[rt].l);
+            } else {
+                store(cur ^ 1, now);
             }
-            if (next >= 0) store(next, cur ^ 1);
             __syncthreads();
-            cur ^= 1;
+            i = next;
+            next = after;
+        };
+        while (i >= 0) {
+            sum_page(0, rz, ra);
+            if (i < 0) break;
+            sum_page(1, ra, rz);
         }
     }
     if constexpr (CODES == kE4m3) {
@@ -223,9 +312,9 @@ template <int D, int CODES>
 void prompt_go(const KvAttend &a, int dtype, hipStream_t s) {
     const dim3 grid(a.splits * a.row_blocks * a.c.heads * a.c.batch);
     if (dtype == kBf16)
-        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kBf16>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kBf16>), grid, dim3(kPromptWaves<D> * 64), 0, s, a);
     else
-        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kFp16>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kFp16>), grid, dim3(kPromptWaves<D> * 64), 0, s, a);
 }
 
 template <int D>

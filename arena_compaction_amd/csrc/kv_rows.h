@@ -49,12 +49,12 @@ struct Soft {
     float m, l;
 };
 
-// Scores of a page (sums over codes, in w) to weights 2^(f * score + ev - m),
-// which replace them.  `see`: how many of the lane's 16 tokens the row sees,
-// looked at where `edge` says that some row misses some.  Returns what the
-// row's earlier sums are to be multiplied by (1 almost always: the maximum
-// moves only when a weight would pass 2^kRoom).
-__device__ inline float soft_page(Soft &s, f32x4 (&w)[4], float f, int ei, bool edge, int see) {
+// Scores of a page (sums over codes, in w) to exponents f * score + ev - m,
+// at most kRoom, which replace them.  `see`: how many of the lane's 16 tokens
+// the row sees, looked at where `edge` says that some row misses some.
+// Returns what the row's earlier sums are to be multiplied by (1 almost
+// always: the maximum moves only when an exponent would pass kRoom).
+__device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, bool edge, int see) {
     const bool first = s.m == KV_NEG_INF;
     const float c = (float)ei - (first ? 0.0f : s.m);
     float top = KV_NEG_INF;
@@ -87,25 +87,20 @@ __device__ inline float soft_page(Soft &s, f32x4 (&w)[4], float f, int ei, bool 
                 for (int i = 0; i < 4; ++i) w[tt][i] -= by;
         }
     }
-    float sum = 0.0f;
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[tt][i] = __builtin_amdgcn_exp2f(w[tt][i]);
-            sum += w[tt][i];
-        }
-    s.l = __builtin_fmaf(sum, pow2(-ei), s.l);
     return fade;
 }
 
-// Weights as the operand of two products over 32 tokens each.
-__device__ inline void pack_weights(const f32x4 (&w)[4], u32x4 (&p)[2]) {
+// Exponents of 8 of the lane's tokens (two tiles) to weights: the operand of
+// a product over 32 tokens, and their sum added to `sum`.
+__device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, u32x4 &p, float &sum) {
+    float e[8];
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-        p[tt / 2][tt % 2 * 2] = pack2<kFp16>(w[tt][0], w[tt][1]);
-        p[tt / 2][tt % 2 * 2 + 1] = pack2<kFp16>(w[tt][2], w[tt][3]);
+    for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(i < 4 ? w0[i] : w1[i - 4]);
+        sum += e[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack2<kFp16>(e[2 * i], e[2 * i + 1]);
 }
 
 // Exponent of a page's value scale (a page never written may hold a scale of
@@ -167,7 +162,7 @@ __device__ inline void load_rows(const KvAttend &a, const Seq &s, uint32_t h, in
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
             q[rt][st] = u32x4{0, 0, 0, 0};
-            if (real) q[rt][st] = load_q8(p + dim_of<D>(st, g), a.vec_q);
+            if (real) q[rt][st] = load_q8(p + dim_of<D>(st, g));
         }
     }
 }
