@@ -381,6 +381,8 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_digit(KvEvict a) {
     int begin, end;
     piece_range(a, (int)c, n, &begin, &end);
     Edge edge{0, 0, 0};
+    uint32_t key[kPieceKeys];  // of the piece's first block, under way while the digit before is found
+    uint32_t safe = load_keys_of<kPieceKeys>(r, begin, end, key);
     if constexpr (DIGIT == 1) {
         int bad = 0, total;
         // pages that begin in the piece (pieces and the budget are whole pages)
@@ -423,8 +425,7 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_digit(KvEvict a) {
     clear_bins(hist, kBins);
     __syncthreads();
     for (int base = begin; base < end; base += kSelThreads * kPieceKeys) {
-        uint32_t key[kPieceKeys];
-        const uint32_t safe = load_keys_of<kPieceKeys>(r, base, end, key);
+        if (base != begin) safe = load_keys_of<kPieceKeys>(r, base, end, key);
 #pragma unroll
         for (int k = 0; k < kPieceKeys; ++k) {
             if (base + (tid / 64 * kPieceKeys + k) * 64 + tid % 64 >= end) continue;
@@ -522,52 +523,90 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_list(KvEvict a) {
     }
 }
 
+// A value code stands alone in its 64 bytes: a token's are D such rows apart.
+// Read byte by byte from memory, every lane would cost L1 an access of its
+// own (163 us for 32 x 8190 tokens cut to 4096, where this takes LATER), so
+// the strips that hold the page's tokens pass through LDS whole, one after the
+// other -- few, since moved tokens lie in order -- and bytes are picked there.
 template <int D, int CODES>
 __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
-    __shared__ const uint8_t *from[kKvPage];  // a token's first value code
+    __shared__ u32x2 sm_v[2][D * kKvPage / 8];
     __shared__ int place[kKvPage];
     __shared__ float scale[2][kKvPage];
     __shared__ float red[2][kFoldThreads / 64];
-    const uint32_t j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    // neighbouring pages on one of the 8 XCDs: they take tokens from the same
+    // strips, which its L2 then holds
+    const uint32_t per_xcd = gridDim.x / 8;
+    const uint32_t j = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+    const uint32_t h = blockIdx.y, b = blockIdx.z;
     const uint64_t row = (uint64_t)b * a.c.heads + h;
     const int tid = threadIdx.x, lane = tid % 64;
     if (!a.fold[row]) return;
+    // every wave: token `lane` of the page, where it comes from
     const int own = (int)(j * kKvPage) + lane;
     int s = a.src[row * a.budget + own];
     if (__builtin_amdgcn_ballot_w64(s != own) == 0) return;
-    if (tid < kKvPage) {
-        if (s < 0) {
-            s = a.moved[row * a.budget + ~s];
+    if (s < 0) {
+        s = a.moved[row * a.budget + ~s];
+        if (tid < kKvPage) {
             a.weight_out[row * a.cap_out + own] = a.weight[row * a.cap + s];
             a.pos_out[row * a.cap_out + own] = a.pos[row * a.cap + s];
         }
-        uint8_t *page = page_at(a.c, b, (uint64_t)s / kKvPage);
-        const float *sc = page_scales(a.c, page, h);
+    }
+    const int from = s / kKvPage;
+    const uint64_t stay = __builtin_amdgcn_ballot_w64(s == own);
+    const uint64_t strip = page_offset(a.c, b, from) + (uint64_t)h * 2 * kKvPage * D;
+    if (tid < kKvPage) {
+        const float *sc = page_scales(a.c, a.c.arena + strip - (uint64_t)h * 2 * kKvPage * D, h);
         place[tid] = s % kKvPage;
-        from[tid] = page + (uint64_t)h * 2 * kKvPage * D + kKvPage * D + s % kKvPage;
         scale[0][tid] = sc[0];
         scale[1][tid] = sc[1];
     }
-    __syncthreads();
-    uint8_t *page = page_at(a.c, b, j);
-    float *sc = page_scales(a.c, page, h);
-    uint8_t *kc = page + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
     // keys: 8 dimensions of a token a lane; values: 4 tokens of a dimension,
     // a lane's tokens the same for all of its dimensions
     constexpr int kK = D / 32, kV = D / 16, kPer = D / 8;
-    u32x2 kw[kK];
-    uint8_t vb[kV][4];
+    u32x2 kw[kK], raw[kK];
+    uint32_t vw[kV] = {};
     const int t0 = tid % 16 * 4, dv = tid / 16;
+    uint64_t todo = ~0ull;
+    auto load = [&](int at) __attribute__((always_inline)) {
+        const uint8_t *p = a.c.arena + lane_u64(strip, at) + kKvPage * D;
+#pragma unroll
+        for (int i = 0; i < kK; ++i) raw[i] = reinterpret_cast<const u32x2 *>(p)[tid + i * kFoldThreads];
+    };
+    load(0);
+    int cur = 0, at = 0;
+    while (todo) {
+        const uint64_t here = __builtin_amdgcn_ballot_w64(from == __builtin_amdgcn_readlane(from, at));
+        todo &= ~here;
+#pragma unroll
+        for (int i = 0; i < kK; ++i) sm_v[cur][tid + i * kFoldThreads] = raw[i];
+        at = todo ? __builtin_ctzll(todo) : at;
+        load(at);  // the last one once more
+        __syncthreads();
+        const uint32_t mine = (uint32_t)(here >> t0) & 15u;
+        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(sm_v[cur]) + dv * kKvPage;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if ((mine >> e) & 1) {
+                const uint8_t *p = bytes + place[t0 + e];
+#pragma unroll
+                for (int i = 0; i < kV; ++i) vw[i] |= (uint32_t)p[i * 16 * kKvPage] << (8 * e);
+            }
+        }
+        cur ^= 1;
+    }
+    // (a buffer is filled again only behind the barrier after the one that
+    // follows its last reads)
+    const uint64_t base = page_offset(a.c, b, j);
+    float *sc = page_scales(a.c, a.c.arena + base, h);
+    const int ke_was = exp_of_pow2(sc[0]);
+    uint8_t *kc = a.c.arena + base + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
 #pragma unroll
     for (int i = 0; i < kK; ++i) {
         const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
-        kw[i] = *reinterpret_cast<const u32x2 *>(from[t] - kKvPage * D + place[t] * (D - 1) + d);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint8_t *p = from[t0 + e] + dv * kKvPage;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) vb[i][e] = p[i * 16 * kKvPage];
+        const uint64_t p = (uint64_t)__shfl((long long)strip, t);
+        kw[i] = *reinterpret_cast<const u32x2 *>(a.c.arena + p + place[t] * D + d);
     }
     float km = 0.0f, vm = 0.0f;
 #pragma unroll
@@ -583,9 +622,12 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
     }
     const float g[4] = {scale[1][t0], scale[1][t0 + 1], scale[1][t0 + 2], scale[1][t0 + 3]};
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vm = fmaxf(vm, finite_abs(code_value<CODES, 0>(vb[i][e]) * g[e]));
+    for (int i = 0; i < kV; ++i) {
+        vm = fmaxf(vm, finite_abs(code_value<CODES, 0>(vw[i]) * g[0]));
+        vm = fmaxf(vm, finite_abs(code_value<CODES, 1>(vw[i]) * g[1]));
+        vm = fmaxf(vm, finite_abs(code_value<CODES, 2>(vw[i]) * g[2]));
+        vm = fmaxf(vm, finite_abs(code_value<CODES, 3>(vw[i]) * g[3]));
+    }
     km = wave_max0(km);
     vm = wave_max0(vm);
     if (lane == 0) {
@@ -600,6 +642,8 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
 #pragma unroll
     for (int i = 0; i < kK; ++i) {
         const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
+        // at the page's old scale, tokens that stay keep their codes
+        if (ke == ke_was && ((stay >> t) & 1)) continue;
         const float f = scale[0][t] * ki;
         u32x2 w;
         w[0] = requant4<CODES>(kw[i][0], f);
@@ -609,8 +653,8 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
 #pragma unroll
     for (int i = 0; i < kV; ++i)
         *reinterpret_cast<uint32_t *>(vc + (dv + i * 16) * kKvPage + t0) = to_codes4<CODES>(
-            code_value<CODES, 0>(vb[i][0]) * (g[0] * vi), code_value<CODES, 0>(vb[i][1]) * (g[1] * vi),
-            code_value<CODES, 0>(vb[i][2]) * (g[2] * vi), code_value<CODES, 0>(vb[i][3]) * (g[3] * vi));
+            code_value<CODES, 0>(vw[i]) * (g[0] * vi), code_value<CODES, 1>(vw[i]) * (g[1] * vi),
+            code_value<CODES, 2>(vw[i]) * (g[2] * vi), code_value<CODES, 3>(vw[i]) * (g[3] * vi));
     if (tid == 0) {
         sc[0] = pow2(ke);
         sc[1] = pow2(ve);
