@@ -528,25 +528,36 @@ def defrag_kv_page_bytes(heads: int, dim: int) -> int:
     return nb
 
 
+def _kv_ptr(t, dtype: torch.dtype, n: int, dev: int, what: str) -> int:
+    """The address of a contiguous tensor of dtype on GPU dev with at least n
+    elements (one test on the way: a call of a few microseconds has a dozen)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or dev < 0 \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor on the arena's GPU")
+    if t.numel() < n:
+        raise ValueError(f"{what}: {t.numel()} elements, {n} needed")
+    return t.data_ptr()
+
+
 def _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid) -> defrag_kv_cache:
     """The defrag_kv_cache of a call and the checks of its tensors."""
-    _need(arena, torch.uint8, 0, "arena")
-    _need(pages, torch.int64, 0, "pages")
-    _need(lens, torch.int32, 0, "lens")
-    _need(n_invalid, torch.int64, 1, "n_invalid")
-    if codes not in KV_CODES:
+    kind = KV_CODES.get(codes)
+    if kind is None:
         raise ValueError(f"codes: {codes}, expected one of {list(KV_CODES)}")
-    if pages.dim() != 2 or lens.dim() != 1 or pages.shape[0] != lens.shape[0]:
-        raise ValueError("pages: [batch, pages] and lens: [batch] expected")
-    for t, what in ((pages, "pages"), (lens, "lens"), (n_invalid, "n_invalid")):
-        _same_device(t, arena, what)
-    return defrag_kv_cache(_ptr(arena), arena.numel(), _ptr(pages), pages.shape[1], _ptr(lens),
-                           pages.shape[0], heads, dim, KV_CODES[codes], _ptr(n_invalid))
-
-
-def _same_device(t, arena, what: str) -> None:
-    if t is not None and t.device != arena.device:
-        raise ValueError(f"{what}: on {t.device}, the arena is on {arena.device}")
+    dev = arena.get_device() if isinstance(arena, torch.Tensor) else -1
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"arena: on GPU {dev}, the current one is {torch.cuda.current_device()}")
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages: [batch, pages] expected")
+    batch, stride = pages.shape
+    if not isinstance(lens, torch.Tensor) or lens.dtype is not torch.int32 or lens.dim() != 1 \
+            or lens.shape[0] != batch:
+        raise ValueError("lens: int32 [batch] expected, as many as pages has rows")
+    return defrag_kv_cache(_kv_ptr(arena, torch.uint8, 0, dev, "arena"), arena.numel(),
+                           _kv_ptr(pages, torch.int64, 0, dev, "pages"), stride,
+                           _kv_ptr(lens, torch.int32, 0, dev, "lens"), batch, heads, dim, kind,
+                           None if n_invalid is None else
+                           _kv_ptr(n_invalid, torch.int64, 1, dev, "n_invalid"))
 
 
 def _kv_rows(t, arena, what: str, dim: Optional[int] = None, heads: Optional[int] = None) -> None:
@@ -556,19 +567,17 @@ def _kv_rows(t, arena, what: str, dim: Optional[int] = None, heads: Optional[int
     if t.dim() != 3 or (dim is not None and t.shape[2] != dim) or \
             (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{what}: shape {tuple(t.shape)}")
-    if not t.is_cuda or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{what}: expected a GPU tensor with a dense last dimension")
-    _same_device(t, arena, what)
+    if not t.is_cuda or t.get_device() != arena.get_device() or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what}: expected a tensor on the arena's GPU with a dense last dimension")
 
 
 def _kv_plane(t, arena, dtype, shape, what: str) -> int:
     """Checks a contiguous [batch, heads, places] tensor; its number of places."""
     if t is None:
         return 0
-    _need(t, dtype, 0, what)
-    if t.dim() != 3 or tuple(t.shape[:2]) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, [{shape[0]}, {shape[1]}, places] expected")
-    _same_device(t, arena, what)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 3 or t.shape[:2] != shape:
+        raise ValueError(f"{what}: expected {dtype} [{shape[0]}, {shape[1]}, places]")
+    _kv_ptr(t, dtype, 0, arena.get_device(), what)
     return t.shape[2]
 
 
@@ -578,17 +587,26 @@ def _kv_new(starts, max_new, tokens: int, batch: int, arena) -> int:
         if tokens != batch:
             raise ValueError(f"starts: {tokens} tokens of {batch} sequences need it")
         return min(1, tokens)
-    _need(starts, torch.int32, batch + 1, "starts")
-    _same_device(starts, arena, "starts")
+    _kv_ptr(starts, torch.int32, batch + 1, arena.get_device(), "starts")
     return tokens if max_new is None else min(int(max_new), tokens)
 
 
-def _kv_scratch(nbytes: int, stream, device) -> torch.Tensor:
+def _kv_stream(stream, dev: int) -> int:
+    """The stream's handle.  The current one is asked for as a handle:
+    torch.cuda.current_stream() makes an object first, for 3 us."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _kv_scratch(shape, dtype, stream, device) -> torch.Tensor:
     """Memory for one call, from the pool of the stream that it runs on."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Optional[int] = None,
@@ -612,12 +630,13 @@ def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Opti
     cap2 = _kv_plane(pos, arena, torch.int32, (batch, heads), "pos")
     if weight is not None and pos is not None and cap != cap2:
         raise ValueError("pos: another number of places than weight")
-    _need(first_pos, torch.int32, batch, "first_pos")
-    _same_device(first_pos, arena, "first_pos")
+    dev = arena.get_device()
+    if first_pos is not None:
+        _kv_ptr(first_pos, torch.int32, batch, dev, "first_pos")
     a = defrag_kv_append_args(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
                               v.stride(0), v.stride(1), KV_DTYPES[k.dtype], most, tokens,
-                              _ptr(starts), _ptr(weight), _ptr(pos), _ptr(first_pos), cap or cap2)
-    rc = lib.defrag_kv_append(ctypes.byref(a), _stream(stream))
+                              _opt(starts), _opt(weight), _opt(pos), _opt(first_pos), cap or cap2)
+    rc = lib.defrag_kv_append(a, _kv_stream(stream, dev))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_append")
 
@@ -642,29 +661,27 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
     most = _kv_new(starts, max_new, tokens, batch, arena)
     if max_len is None:
         max_len = pages.shape[1] * KV_PAGE_TOKENS
+    dev = arena.get_device()
     if out is None:
-        if stream is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            with torch.cuda.stream(stream):
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out: another shape or dtype than q")
-    _same_device(out, arena, "out")
-    _need(lse, torch.float32, tokens * q_heads, "lse")
-    _same_device(lse, arena, "lse")
+        out = _kv_scratch(q.shape, q.dtype, stream, q.device)
+    elif not isinstance(out, torch.Tensor) or out.shape != q.shape:
+        raise ValueError("out: another shape than q")
+    else:
+        _kv_ptr(out, q.dtype, 0, dev, "out")
+    if lse is not None:
+        _kv_ptr(lse, torch.float32, tokens * q_heads, dev, "lse")
     cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
     a = defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
-                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _ptr(starts), most,
-                              max_len, dim ** -0.5 if scale is None else scale, 0, _ptr(out),
-                              _ptr(lse), _ptr(weight), cap)
+                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
+                              max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
+                              _opt(lse), _opt(weight), cap)
     if ws is None:
-        need = lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a))
+        need = lib.defrag_kv_attend_workspace_bytes(a)
         if need == 0:
             raise DefragError(DEFRAG_EINVAL, "defrag_kv_attend")
-        ws = _kv_scratch(need, stream, q.device)
-    _same_device(ws, arena, "ws")
-    rc = lib.defrag_kv_attend(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+        ws = _kv_scratch(need, torch.uint8, stream, q.device)
+    rc = lib.defrag_kv_attend(a, _kv_ptr(ws, torch.uint8, 0, dev, "ws"), ws.numel(),
+                              _kv_stream(stream, dev))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_attend")
     return out
@@ -692,26 +709,25 @@ def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, po
     cap_out = _kv_plane(weight_out, arena, torch.float32, (batch, heads), "weight_out")
     if _kv_plane(pos_out, arena, torch.int32, (batch, heads), "pos_out") != cap_out or pos_out is None:
         raise ValueError("pos_out: another shape than weight_out")
-    if lens_out is None or weight_out is None:
-        raise ValueError("weight_out, pos_out and lens_out are needed")
-    _need(lens_out, torch.int32, batch, "lens_out")
-    _same_device(lens_out, arena, "lens_out")
+    dev = arena.get_device()
+    if weight_out is None:
+        raise ValueError("weight_out: needed, with pos_out and lens_out")
     if next_pos is None:
         next_pos = lens
-    _need(next_pos, torch.int32, batch, "next_pos")
-    _same_device(next_pos, arena, "next_pos")
     if max_len is None:
         max_len = min(pages.shape[1] * KV_PAGE_TOKENS, cap)
-    a = defrag_kv_evict_args(ctypes.pointer(c), budget, max_len, sink, recent, _ptr(next_pos),
-                             _ptr(weight), _ptr(pos), cap, _ptr(weight_out), _ptr(pos_out), cap_out,
-                             _ptr(lens_out))
+    a = defrag_kv_evict_args(ctypes.pointer(c), budget, max_len, sink, recent,
+                             _kv_ptr(next_pos, torch.int32, batch, dev, "next_pos"),
+                             weight.data_ptr(), pos.data_ptr(), cap, weight_out.data_ptr(),
+                             pos_out.data_ptr(), cap_out,
+                             _kv_ptr(lens_out, torch.int32, batch, dev, "lens_out"))
     if ws is None:
-        need = lib.defrag_kv_evict_workspace_bytes(ctypes.byref(a))
+        need = lib.defrag_kv_evict_workspace_bytes(a)
         if need == 0:
             raise DefragError(DEFRAG_EINVAL, "defrag_kv_evict")
-        ws = _kv_scratch(need, stream, arena.device)
-    _same_device(ws, arena, "ws")
-    rc = lib.defrag_kv_evict(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream))
+        ws = _kv_scratch(need, torch.uint8, stream, arena.device)
+    rc = lib.defrag_kv_evict(a, _kv_ptr(ws, torch.uint8, 0, dev, "ws"), ws.numel(),
+                             _kv_stream(stream, dev))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_evict")
 

@@ -10,34 +10,34 @@
 // half a unit); it grows at most once a page for a growing maximum.
 //
 // One workgroup a (page, head): every code of the strip and both scales are
-// its own, so nothing is shared and the result does not depend on order.
-// The new tokens' elements are read once, kept in registers through the
-// reduction of the maximum, and written as codes; values go through LDS,
-// since they lie token by token in the input and dimension by dimension in
-// the page.
+// its own, so nothing is shared and the result does not depend on order.  A
+// lane takes 4 tokens x 8 dimensions of both: in the input 16 bytes a token,
+// in the page 8 bytes of each key row and 4 of each value row, so that the
+// values turn from token by token to dimension by dimension within the lane
+// (through LDS, byte by byte, a prompt's pages took 26 us where this takes
+// LATER).  The input is read once and kept in its 16 bits through the
+// reduction of the maximum.
 #include "kv_device.h"
 
 namespace ac {
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kTileStride = kKvPage + 4;  // bytes; rows start in other banks
-
 // (2-byte alignment will do: gfx950 reads 16 bytes from any address)
+__device__ inline u32x4 load8(const uint16_t *p) {
+    u32x4 r;
+    __builtin_memcpy(&r, p, 16);
+    return r;
+}
+
 template <int DTYPE>
-__device__ inline void load8(const uint16_t *p, float (&x)[8]) {
-    uint16_t h[8];
-    __builtin_memcpy(h, p, 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float<DTYPE>(h[i]);
+__device__ inline float nth(const u32x4 &x, int i) {
+    return to_float<DTYPE>((uint16_t)(x[i / 2] >> (16 * (i % 2))));
 }
 
 template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
-    constexpr int kPer = D / 8;                              // 8-element pieces of a token
-    constexpr int kItems = kKvPage * kPer / kAppendThreads;  // pieces a lane holds
-    __shared__ float red[2][kAppendThreads / 64];
-    __shared__ __align__(16) uint8_t tile[D * kTileStride];
+__global__ __launch_bounds__(2 * D) void k_kv_append(KvAppend a) {
+    constexpr int kN = 2 * D, kPer = D / 8;  // lanes; pieces of 8 dimensions
+    __shared__ float red[2][kN / 64];
     const uint32_t h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x;
     uint64_t first;
@@ -60,33 +60,31 @@ __global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
         if (a.c.n_invalid && h == 0 && tid == 0) atomicAdd(a.c.n_invalid, 1ull);
         return;
     }
-    const uint64_t src = first + (uint64_t)(base + lo - len);  // the input's token at place lo
+    const int64_t src = (int64_t)first + base - len;  // the input's token at place 0, were it there
     float *sc = page_scales(a.c, page, h);
     uint8_t *kc = page + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
-    const int n = (hi - lo) * kPer;
+    const int d = tid % kPer * 8, q = lo / 4 + tid / kPer, t0 = 4 * q;
+    const bool mine = t0 < hi;
 
-    float kx[kItems][8], vx[kItems][8];
+    u32x4 k[4], v[4];
     float km = 0.0f, vm = 0.0f;
+    if (mine) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int item = tid + i * kAppendThreads;
-        if (item < n) {
-            const uint64_t t = src + item / kPer;
-            const int d = item % kPer * 8;
-            load8<DTYPE>(a.k + (int64_t)t * a.k_row + h * a.k_head + d, kx[i]);
-            load8<DTYPE>(a.v + (int64_t)t * a.v_row + h * a.v_head + d, vx[i]);
+        for (int e = 0; e < 4; ++e) {  // for places without a new token the nearest one that has
+            const int t = t0 + e < lo ? lo : t0 + e < hi ? t0 + e : hi - 1;
+            k[e] = load8(a.k + (src + t) * a.k_row + h * a.k_head + d);
+            v[e] = load8(a.v + (src + t) * a.v_row + h * a.v_head + d);
         }
     }
     const int ke0 = exp_of_pow2(sc[0]), ve0 = exp_of_pow2(sc[1]);
+    if (mine) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        if (tid + i * kAppendThreads < n) {
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                km = fmaxf(km, finite_abs(kx[i][e]));
-                vm = fmaxf(vm, finite_abs(vx[i][e]));
+            for (int i = 0; i < 8; ++i) {
+                km = fmaxf(km, finite_abs(nth<DTYPE>(k[e], i)));
+                vm = fmaxf(vm, finite_abs(nth<DTYPE>(v[e], i)));
             }
-        }
     }
     km = wave_max0(km);
     vm = wave_max0(vm);
@@ -95,8 +93,11 @@ __global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
         red[1][tid / 64] = vm;
     }
     __syncthreads();
-    km = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    vm = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+#pragma unroll
+    for (int w = 0; w < kN / 64; ++w) {
+        km = fmaxf(km, red[0][w]);
+        vm = fmaxf(vm, red[1][w]);
+    }
     int ke = scale_exp<CODES>(km), ve = scale_exp<CODES>(vm);
     if (lo > 0) {
         ke = ke0 > ke ? ke0 : ke;
@@ -107,26 +108,41 @@ __global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
     const float vf = lo > 0 ? ldexpf(1.0f, ve0 - ve) : 1.0f;
     const float ki = pow2(-ke), vi = pow2(-ve);
 
+    if (mine) {
+        // dwords that also hold places outside [lo, hi) are read first: older
+        // tokens in them are brought to the new scale, places behind the last
+        // one left as they are
+        uint32_t fresh = 0;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int item = tid + i * kAppendThreads;
-        if (item < n) {
-            const int t = lo + item / kPer, d = item % kPer * 8;
-            const float *x = kx[i];
-            u32x2 w;
-            w[0] = to_codes4<CODES>(x[0] * ki, x[1] * ki, x[2] * ki, x[3] * ki);
-            w[1] = to_codes4<CODES>(x[4] * ki, x[5] * ki, x[6] * ki, x[7] * ki);
-            *reinterpret_cast<u32x2 *>(kc + t * D + d) = w;
-            const float *y = vx[i];
-            w[0] = to_codes4<CODES>(y[0] * vi, y[1] * vi, y[2] * vi, y[3] * vi);
-            w[1] = to_codes4<CODES>(y[4] * vi, y[5] * vi, y[6] * vi, y[7] * vi);
+        for (int e = 0; e < 4; ++e)
+            if (t0 + e >= lo && t0 + e < hi) fresh |= 255u << (8 * e);
+        const int old = lo - t0;
+        const uint32_t older = old <= 0 ? 0u : (1u << (8 * old)) - 1u;  // old < 4, since q >= lo / 4
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                tile[(d + e) * kTileStride + t] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+        for (int i = 0; i < 8; ++i) {
+            uint32_t *p = reinterpret_cast<uint32_t *>(vc + (d + i) * kKvPage + t0);
+            uint32_t w = to_codes4<CODES>(nth<DTYPE>(v[0], i) * vi, nth<DTYPE>(v[1], i) * vi,
+                                          nth<DTYPE>(v[2], i) * vi, nth<DTYPE>(v[3], i) * vi);
+            if (fresh != ~0u) {
+                const uint32_t was = *p, again = vf != 1.0f ? requant4<CODES>(was, vf) : was;
+                w = (w & fresh) | (again & older) | (was & ~(fresh | older));
+            }
+            *p = w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (t0 + e >= lo && t0 + e < hi) {
+                u32x2 w;
+                w[0] = to_codes4<CODES>(nth<DTYPE>(k[e], 0) * ki, nth<DTYPE>(k[e], 1) * ki,
+                                        nth<DTYPE>(k[e], 2) * ki, nth<DTYPE>(k[e], 3) * ki);
+                w[1] = to_codes4<CODES>(nth<DTYPE>(k[e], 4) * ki, nth<DTYPE>(k[e], 5) * ki,
+                                        nth<DTYPE>(k[e], 6) * ki, nth<DTYPE>(k[e], 7) * ki);
+                *reinterpret_cast<u32x2 *>(kc + (t0 + e) * D + d) = w;
+            }
         }
     }
     if (lo > 0 && kf != 1.0f) {
-        for (int i = tid; i < lo * kPer; i += kAppendThreads) {
+        for (int i = tid; i < lo * kPer; i += kN) {
             u32x2 *p = reinterpret_cast<u32x2 *>(kc) + i;
             u32x2 w = *p;
             w[0] = requant4<CODES>(w[0], kf);
@@ -134,27 +150,12 @@ __global__ __launch_bounds__(kAppendThreads) void k_kv_append(KvAppend a) {
             *p = w;
         }
     }
-    __syncthreads();
-    // four tokens of one dimension at a time; a dword that also holds places
-    // outside [lo, hi) is read first, older tokens in it brought to the new
-    // scale, places behind the last one left as they are
-    const int q0 = (vf != 1.0f) ? 0 : lo / 4, q1 = (hi + 3) / 4, nq = q1 - q0;
-    for (int i = tid; i < nq * D; i += kAppendThreads) {
-        const int d = i / nq, q = q0 + i % nq;
-        uint32_t *p = reinterpret_cast<uint32_t *>(vc + d * kKvPage) + q;
-        uint32_t w = 0;
-        if (4 * q + 4 > lo) w = *reinterpret_cast<const uint32_t *>(tile + d * kTileStride + 4 * q);
-        if (4 * q < lo || 4 * q + 4 > hi) {
-            const uint32_t was = *p, again = vf != 1.0f ? requant4<CODES>(was, vf) : was;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * q + e;
-                const uint32_t m = 255u << (8 * e);
-                if (t < lo) w = (w & ~m) | (again & m);
-                if (t >= hi) w = (w & ~m) | (was & m);
-            }
+    if (lo >= 4 && vf != 1.0f) {  // dwords of older tokens alone
+        const int nq = lo / 4;
+        for (int i = tid; i < nq * D; i += kN) {
+            uint32_t *p = reinterpret_cast<uint32_t *>(vc + i / nq * kKvPage) + i % nq;
+            *p = requant4<CODES>(*p, vf);
         }
-        *p = w;
     }
     if (tid == 0) {
         sc[0] = pow2(ke);
@@ -179,9 +180,9 @@ __global__ void k_kv_zero(unsigned long long *p) {
 template <int D, int CODES>
 void append_go(const KvAppend &a, int dtype, dim3 grid, hipStream_t s) {
     if (dtype == kBf16)
-        hipLaunchKernelGGL((k_kv_append<D, CODES, kBf16>), grid, dim3(kAppendThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kBf16>), grid, dim3(2 * D), 0, s, a);
     else
-        hipLaunchKernelGGL((k_kv_append<D, CODES, kFp16>), grid, dim3(kAppendThreads), 0, s, a);
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kFp16>), grid, dim3(2 * D), 0, s, a);
 }
 
 template <int D>
