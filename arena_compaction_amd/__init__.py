@@ -597,12 +597,24 @@ def _kv_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _kv_scratch(shape, dtype, stream, device) -> torch.Tensor:
+def _kv_new_empty(like: torch.Tensor, shape, stream) -> torch.Tensor:
     """Memory for one call, from the pool of the stream that it runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape)
+
+
+def _kv_scratch(need: int, ws, arena, stream, what: str):
+    """(workspace tensor, address, bytes) of a call that needs `need` bytes."""
+    if need == 0:
+        raise DefragError(DEFRAG_EINVAL, what)
+    if ws is not None:
+        return ws, _kv_ptr(ws, torch.uint8, 0, arena.get_device(), "ws"), ws.numel()
+    if need == 1:   # none
+        return None, None, 0
+    ws = _kv_new_empty(arena, (need,), stream)
+    return ws, ws.data_ptr(), need
 
 
 def _opt(t):
@@ -663,7 +675,7 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
         max_len = pages.shape[1] * KV_PAGE_TOKENS
     dev = arena.get_device()
     if out is None:
-        out = _kv_scratch(q.shape, q.dtype, stream, q.device)
+        out = _kv_new_empty(q, q.shape, stream)
     elif not isinstance(out, torch.Tensor) or out.shape != q.shape:
         raise ValueError("out: another shape than q")
     else:
@@ -675,13 +687,9 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
                               KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
                               max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
                               _opt(lse), _opt(weight), cap)
-    if ws is None:
-        need = lib.defrag_kv_attend_workspace_bytes(a)
-        if need == 0:
-            raise DefragError(DEFRAG_EINVAL, "defrag_kv_attend")
-        ws = _kv_scratch(need, torch.uint8, stream, q.device)
-    rc = lib.defrag_kv_attend(a, _kv_ptr(ws, torch.uint8, 0, dev, "ws"), ws.numel(),
-                              _kv_stream(stream, dev))
+    need = lib.defrag_kv_attend_workspace_bytes(a)
+    ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_attend")
+    rc = lib.defrag_kv_attend(a, at, size, _kv_stream(stream, dev))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_attend")
     return out
@@ -721,13 +729,9 @@ def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, po
                              weight.data_ptr(), pos.data_ptr(), cap, weight_out.data_ptr(),
                              pos_out.data_ptr(), cap_out,
                              _kv_ptr(lens_out, torch.int32, batch, dev, "lens_out"))
-    if ws is None:
-        need = lib.defrag_kv_evict_workspace_bytes(a)
-        if need == 0:
-            raise DefragError(DEFRAG_EINVAL, "defrag_kv_evict")
-        ws = _kv_scratch(need, torch.uint8, stream, arena.device)
-    rc = lib.defrag_kv_evict(a, _kv_ptr(ws, torch.uint8, 0, dev, "ws"), ws.numel(),
-                             _kv_stream(stream, dev))
+    need = lib.defrag_kv_evict_workspace_bytes(a)
+    ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_evict")
+    rc = lib.defrag_kv_evict(a, at, size, _kv_stream(stream, dev))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_evict")
 

@@ -12,7 +12,7 @@ namespace {
 constexpr uint64_t kMaxTokens = 1u << 29;
 constexpr uint64_t kMaxGrid = (1u << 24) - 1;
 constexpr uint64_t kMaxEvict = 1u << 25;  // tokens of an evicted sequence
-constexpr uint64_t kLeastWs = 256;  // so that 0 can mean "refused"
+constexpr uint64_t kLeastWs = 1;  // none is needed: 0 means "refused"
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 

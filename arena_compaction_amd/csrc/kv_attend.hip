@@ -25,9 +25,14 @@
 namespace ac {
 namespace {
 
+// Waves of a SIMD that share its registers: 3 where a page's codes and the
+// sums of 16 rows fit a third of them.
+template <int D, int DTYPE, int R, bool KEEP>
+constexpr int kWavesASimd = D > 128 ? 1 : R == 1 && !(D == 128 && DTYPE == kFp16 && KEEP) ? 3 : 2;
+
 // KEEP: scores are kept for the weights.
 template <int D, int CODES, int DTYPE, int R, bool KEEP>
-__global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_attend(KvAttend a) {
+__global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_kv_attend(KvAttend a) {
     constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 16 * R, kJoin = 4;
     __shared__ f32x4 sm_o[kWaves][R * kJoin * 64];
     __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
@@ -121,7 +126,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
             }
         }
         const bool edge = base + kKvPage > see_least;
-        u32x4 pw[R][2];
+        Weights<DTYPE> pw[R][2];
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
             const float fade = soft_scores(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
@@ -164,8 +169,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : R == 1 ? 3 : 2) void k_kv_a
             const u32x4 v1 = widen8<CODES, kFp16>(vraw[dt][2], vraw[dt][3]);
 #pragma unroll
             for (int rt = 0; rt < R; ++rt) {
-                o[rt][dt] = mfma16<kFp16>(v0, pw[rt][0], o[rt][dt]);
-                o[rt][dt] = mfma16<kFp16>(v1, pw[rt][1], o[rt][dt]);
+                o[rt][dt] = weigh_values(v0, pw[rt][0], o[rt][dt]);
+                o[rt][dt] = weigh_values(v1, pw[rt][1], o[rt][dt]);
             }
         }
         get_values(next);

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_pr
                 }
                 // the first half's products run beside the second half's exponents
                 float sum[R] = {};
-                u32x4 pw[R][2];
+                Weights<DTYPE> pw[R][2];
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) soft_weights(w[rt][0], w[rt][1], pw[rt][0], sum[rt]);
 #pragma unroll
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_pr
 #pragma unroll
                         for (int rt = 0; rt < R; ++rt) {
                             f32x4 &to = o[rt][at % kBatches * kBatch + k];
-                            to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches], to);
+                            to = weigh_values(vv[at % 2][k], pw[rt][at / kBatches], to);
                         }
 #pragma unroll
                     for (int rt = 0; rt < R; ++rt)

@@ -90,9 +90,22 @@ __device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, boo
     return fade;
 }
 
-// Exponents of 8 of the lane's tokens (two tiles) to weights: the operand of
-// a product over 32 tokens, and their sum added to `sum`.
-__device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, u32x4 &p, float &sum) {
+// Weights of 8 of the lane's tokens as the operand of a product over 32
+// tokens.  float16 rounds a weight by up to 2^-11, an eighth of what an output
+// in bfloat16 is rounded by; beside one in float16 it would show (errors half
+// as large again), so there what the rounding left out is a second operand.
+template <int DTYPE>
+struct Weights {
+    u32x4 high;
+};
+template <>
+struct Weights<kFp16> {
+    u32x4 high, low;
+};
+
+// From the exponents of two tiles; adds the weights' sum to `sum`.
+template <int DTYPE>
+__device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, Weights<DTYPE> &p, float &sum) {
     float e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -100,7 +113,23 @@ __device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, u32x4 &p, 
         sum += e[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack2<kFp16>(e[2 * i], e[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t both = pack2<kFp16>(e[2 * i], e[2 * i + 1]);
+        p.high[i] = both;
+        if constexpr (DTYPE == kFp16) {
+            const half2v h = __builtin_bit_cast(half2v, both);
+            p.low[i] = pack2<kFp16>(__builtin_fmaf((float)h[0], -1.0f, e[2 * i]),
+                                    __builtin_fmaf((float)h[1], -1.0f, e[2 * i + 1]));
+        }
+    }
+}
+
+// to += values x weights, over 32 tokens.
+template <int DTYPE>
+__device__ inline f32x4 weigh_values(const u32x4 &values, const Weights<DTYPE> &p, f32x4 to) {
+    to = mfma16<kFp16>(values, p.high, to);
+    if constexpr (DTYPE == kFp16) to = mfma16<kFp16>(values, p.low, to);
+    return to;
 }
 
 // Exponent of a page's value scale (a page never written may hold a scale of

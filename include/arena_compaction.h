@@ -582,8 +582,8 @@ typedef struct defrag_kv_attend_args {
     uint64_t weight_stride;          /* at least max_len                     */
 } defrag_kv_attend_args;
 
-/* Bytes of workspace (256-byte aligned) that defrag_kv_attend needs (at
- * least 256); 0 for arguments that it refuses. */
+/* Bytes of workspace (256-byte aligned) that defrag_kv_attend needs, 1
+ * where it needs none; 0 for arguments that it refuses. */
 size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *args);
 int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_bytes,
                      hipStream_t stream);
