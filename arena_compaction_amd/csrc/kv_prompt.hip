@@ -24,7 +24,7 @@ template <int D>
 constexpr int kPromptWaves = D <= 128 ? 4 : 8;
 
 template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_prompt(KvAttend a) {
+__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && DTYPE == kBf16 ? 3 : 2) void k_kv_prompt(KvAttend a) {
     constexpr int kN = kPromptWaves<D>, kRows = (int)kKvPromptRows, R = kRows / 16 / kN;
     constexpr int kSteps = D / 32, kTiles = D / 16;
     constexpr int kBatch = kTiles % 4 ? 3 : 4, kBatches = kTiles / kBatch;  // value tiles read at a time
@@ -233,7 +233,8 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_pr
                 float sum[R] = {};
                 Weights<DTYPE> pw[R][2];
 #pragma unroll
-                for (int rt = 0; rt < R; ++rt) soft_weights(w[rt][0], w[rt][1], pw[rt][0], sum[rt]);
+                for (int rt = 0; rt < R; ++rt)
+                    soft_weights<DTYPE>(w[rt][0], w[rt][1], pw[rt][0], sum[rt]);
 #pragma unroll
                 for (int at = 0; at < 2 * kBatches; ++at) {
                     if (at + 1 < 2 * kBatches) read_values(at + 1);
@@ -243,16 +244,26 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 ? 3 : 2) void k_kv_pr
 #pragma unroll
                         for (int rt = 0; rt < R; ++rt) {
                             f32x4 &to = o[rt][at % kBatches * kBatch + k];
-                            to = weigh_values(vv[at % 2][k], pw[rt][at / kBatches], to);
+                            to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches].high, to);
                         }
+                    if constexpr (DTYPE == kFp16) {
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                            for (int rt = 0; rt < R; ++rt) {
+                                f32x4 &to = o[rt][at % kBatches * kBatch + k];
+                                to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches].low, to);
+                            }
+                    }
 #pragma unroll
                     for (int rt = 0; rt < R; ++rt)
                         if (at == (rt < kBatches ? rt : kBatches - 1))
-                            soft_weights(w[rt][2], w[rt][3], pw[rt][1], sum[rt]);
+                            soft_weights<DTYPE>(w[rt][2], w[rt][3], pw[rt][1], sum[rt]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-                for (int rt = 0; rt < R; ++rt) soft[rt].l = __builtin_fmaf(sum[rt], pow2(-ei), soft[rt].l);
+                for (int rt = 0; rt < R; ++rt)
+                    soft[rt].l = __builtin_fmaf(sum[rt], pow2(-ei), soft[rt].l);
             } else {
                 store(cur ^ 1, now);
             }

@@ -106,7 +106,10 @@ struct Weights<kFp16> {
 // From the exponents of two tiles; adds the weights' sum to `sum`.
 template <int DTYPE>
 __device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, Weights<DTYPE> &p, float &sum) {
-    float e[8];
+    float e[8], minus = -1.0f;
+    // (kept from the compiler, which would make two instructions of widening
+    // and subtracting; a product with a float16 operand widens by itself)
+    if constexpr (DTYPE == kFp16) asm("" : "+v"(minus));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         e[i] = __builtin_amdgcn_exp2f(i < 4 ? w0[i] : w1[i - 4]);
@@ -118,8 +121,8 @@ __device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, Weights<DT
         p.high[i] = both;
         if constexpr (DTYPE == kFp16) {
             const half2v h = __builtin_bit_cast(half2v, both);
-            p.low[i] = pack2<kFp16>(__builtin_fmaf((float)h[0], -1.0f, e[2 * i]),
-                                    __builtin_fmaf((float)h[1], -1.0f, e[2 * i + 1]));
+            p.low[i] = pack2<kFp16>(__builtin_fmaf((float)h[0], minus, e[2 * i]),
+                                    __builtin_fmaf((float)h[1], minus, e[2 * i + 1]));
         }
     }
 }
