@@ -519,3 +519,18 @@ def test_offsets_past_32_bits(ac):
     ac.defrag_kv_evict(big, pages, ints([131, 141]), 64, w.cuda(), pos.cuda(), wo, po, lo, 64, INT8)
     evict(c, [131, 141], 64, w, pos, 0, 0, [131, 141])
     same(c, big[base:])
+
+
+def test_example(ac):
+    """The example: generation, eviction and compaction of one arena (it checks
+    that attention over the moved pages gives the same bits)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "kv_cache.py")
+    spec = importlib.util.spec_from_file_location("kv_cache_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    report = example.main(["--steps", "300", "--batch", "3", "--heads", "2", "--dim", "64", "--budget", "128",
+                           "--slack", "64"])
+    assert len(report) >= 2 and all(after == 0.0 for _, _, after in report)
+    assert any(frag > 0.0 for _, frag, _ in report)
