@@ -177,6 +177,37 @@ __device__ inline float across_groups(float x, Op op) {
     return op(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
 }
 
+// The largest magnitudes among codes, byte by byte: magnitudes ascend with
+// their codes' bits, so whole bytes are compared, two to a 16-bit lane, and
+// scaled once at the end.  A NaN counts as 0.
+struct ByteMax {
+    uint32_t even = 0, odd = 0;  // bytes 0 and 2, bytes 1 and 3
+};
+__device__ inline uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    using u16x2 = __attribute__((__vector_size__(4))) uint16_t;
+    const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
+}
+template <int CODES>
+__device__ inline void byte_max(ByteMax &m, uint32_t w) {
+    uint32_t mag;
+    if constexpr (CODES == kE4m3) {
+        mag = w & 0x7F7F7F7Fu & ~((nan_codes(w) >> 7) * 255u);
+    } else {
+        const uint32_t neg = (w >> 7) & 0x01010101u;
+        mag = (w ^ (neg * 255u)) + neg;  // -128 is no code of append's, but stays 128
+    }
+    m.even = max_u16x2(m.even, mag & 0x00FF00FFu);
+    m.odd = max_u16x2(m.odd, (mag >> 8) & 0x00FF00FFu);
+}
+template <int CODES>
+__device__ inline float magnitude(uint32_t byte) {
+    if constexpr (CODES == kE4m3)
+        return code_value<kE4m3, 0>(byte);
+    else
+        return (float)byte;
+}
+
 // Largest of the wave's values (each at least 0), in every lane.
 __device__ inline float wave_max0(float x) {
     return wave_reduce(x, [](float a, float b) { return fmaxf(a, b); });

@@ -528,44 +528,89 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_list(KvEvict a) {
 // own (163 us for 32 x 8190 tokens cut to 4096, where this takes LATER), so
 // the strips that hold the page's tokens pass through LDS whole, one after the
 // other -- few, since moved tokens lie in order -- and bytes are picked there.
+// Keys and values of a page are two workgroups: each waits for little, and
+// more of them are under way.
 template <int D, int CODES>
 __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
     __shared__ u32x2 sm_v[2][D * kKvPage / 8];
+    __shared__ uint64_t strip_of[kKvPage];
     __shared__ int place[kKvPage];
-    __shared__ float scale[2][kKvPage];
-    __shared__ float red[2][kFoldThreads / 64];
+    __shared__ float scale[kKvPage];
+    __shared__ float red[kFoldThreads / 64];
     // neighbouring pages on one of the 8 XCDs: they take tokens from the same
     // strips, which its L2 then holds
-    const uint32_t per_xcd = gridDim.x / 8;
-    const uint32_t j = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * per_xcd + blockIdx.x / 8;
+    const uint32_t pages = gridDim.x / 2, x = blockIdx.x % pages, per_xcd = pages / 8;
+    const bool values = blockIdx.x < pages;
+    const uint32_t j = pages % 8 ? x : x % 8 * per_xcd + x / 8;
     const uint32_t h = blockIdx.y, b = blockIdx.z;
     const uint64_t row = (uint64_t)b * a.c.heads + h;
     const int tid = threadIdx.x, lane = tid % 64;
-    if (!a.fold[row]) return;
     // every wave: token `lane` of the page, where it comes from
     const int own = (int)(j * kKvPage) + lane;
+    if (!a.fold[row]) return;
     int s = a.src[row * a.budget + own];
     if (__builtin_amdgcn_ballot_w64(s != own) == 0) return;
     if (s < 0) {
         s = a.moved[row * a.budget + ~s];
-        if (tid < kKvPage) {
+        if (!values && tid < kKvPage) {
             a.weight_out[row * a.cap_out + own] = a.weight[row * a.cap + s];
             a.pos_out[row * a.cap_out + own] = a.pos[row * a.cap + s];
         }
     }
     const int from = s / kKvPage;
     const uint64_t stay = __builtin_amdgcn_ballot_w64(s == own);
-    const uint64_t strip = page_offset(a.c, b, from) + (uint64_t)h * 2 * kKvPage * D;
+    const uint64_t page = page_offset(a.c, b, from), strip = page + (uint64_t)h * 2 * kKvPage * D;
+    const uint64_t base = page_offset(a.c, b, j);
+    float *sc = page_scales(a.c, a.c.arena + base, h);
+    uint8_t *kc = a.c.arena + base + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
     if (tid < kKvPage) {
-        const float *sc = page_scales(a.c, a.c.arena + strip - (uint64_t)h * 2 * kKvPage * D, h);
         place[tid] = s % kKvPage;
-        scale[0][tid] = sc[0];
-        scale[1][tid] = sc[1];
+        scale[tid] = page_scales(a.c, a.c.arena + page, h)[values];
+        strip_of[tid] = strip;
     }
-    // keys: 8 dimensions of a token a lane; values: 4 tokens of a dimension,
-    // a lane's tokens the same for all of its dimensions
     constexpr int kK = D / 32, kV = D / 16, kPer = D / 8;
-    u32x2 kw[kK], raw[kK];
+    float most = 0.0f;
+    if (!values) {  // 8 dimensions of a token a lane
+        const int e_was = exp_of_pow2(sc[0]);
+        __syncthreads();
+        u32x2 kw[kK];
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
+            kw[i] = *reinterpret_cast<const u32x2 *>(a.c.arena + strip_of[t] + place[t] * D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            ByteMax m;
+            byte_max<CODES>(m, kw[i][0]);
+            byte_max<CODES>(m, kw[i][1]);
+            const uint32_t two = max_u16x2(m.even, m.odd), top = two >> 16 > (two & 0xFFFFu) ? two >> 16 : two & 0xFFFFu;
+            most = fmaxf(most, magnitude<CODES>(top) * scale[(tid + i * kFoldThreads) / kPer]);
+        }
+        most = wave_max0(most);
+        if (lane == 0) red[tid / 64] = most;
+        __syncthreads();  // all of the page's keys have been read, too
+        most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        const int e = scale_exp<CODES>(most);
+        const float inv = pow2(-e);
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
+            // at the page's old scale, tokens that stay keep their codes
+            if (e == e_was && ((stay >> t) & 1)) continue;
+            const float f = scale[t] * inv;
+            u32x2 w = kw[i];
+            if (f != 1.0f) {
+                w[0] = requant4<CODES>(w[0], f);
+                w[1] = requant4<CODES>(w[1], f);
+            }
+            *reinterpret_cast<u32x2 *>(kc + t * D + d) = w;
+        }
+        if (tid == 0) sc[0] = pow2(e);
+        return;
+    }
+    // 4 tokens of a dimension a lane, its tokens the same for all of its dimensions
+    u32x2 raw[kK];
     uint32_t vw[kV] = {};
     const int t0 = tid % 16 * 4, dv = tid / 16;
     uint64_t todo = ~0ull;
@@ -594,76 +639,35 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
                 for (int i = 0; i < kV; ++i) vw[i] |= (uint32_t)p[i * 16 * kKvPage] << (8 * e);
             }
         }
-        cur ^= 1;
+        cur ^= 1;  // filled again only behind the next barrier, which follows these reads
     }
-    // (a buffer is filled again only behind the barrier after the one that
-    // follows its last reads)
-    const uint64_t base = page_offset(a.c, b, j);
-    float *sc = page_scales(a.c, a.c.arena + base, h);
-    const int ke_was = exp_of_pow2(sc[0]);
-    uint8_t *kc = a.c.arena + base + (uint64_t)h * 2 * kKvPage * D, *vc = kc + kKvPage * D;
+    const float g[4] = {scale[t0], scale[t0 + 1], scale[t0 + 2], scale[t0 + 3]};
+    ByteMax m;
 #pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
-        const uint64_t p = (uint64_t)__shfl((long long)strip, t);
-        kw[i] = *reinterpret_cast<const u32x2 *>(a.c.arena + p + place[t] * D + d);
-    }
-    float km = 0.0f, vm = 0.0f;
+    for (int i = 0; i < kV; ++i) byte_max<CODES>(m, vw[i]);
+    most = fmaxf(fmaxf(magnitude<CODES>(m.even & 255u) * g[0], magnitude<CODES>(m.odd & 255u) * g[1]),
+                 fmaxf(magnitude<CODES>(m.even >> 16) * g[2], magnitude<CODES>(m.odd >> 16) * g[3]));
+    most = wave_max0(most);
+    if (lane == 0) red[tid / 64] = most;
+    __syncthreads();
+    most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const int e = scale_exp<CODES>(most);
+    const float inv = pow2(-e);
+    // codes of a scale that stays are the new ones as they are
+    if (g[0] * inv != 1.0f || g[1] * inv != 1.0f || g[2] * inv != 1.0f || g[3] * inv != 1.0f) {
 #pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const float f = scale[0][(tid + i * kFoldThreads) / kPer];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            km = fmaxf(km, finite_abs(code_value<CODES, 0>(kw[i][x]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 1>(kw[i][x]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 2>(kw[i][x]) * f));
-            km = fmaxf(km, finite_abs(code_value<CODES, 3>(kw[i][x]) * f));
-        }
-    }
-    const float g[4] = {scale[1][t0], scale[1][t0 + 1], scale[1][t0 + 2], scale[1][t0 + 3]};
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        vm = fmaxf(vm, finite_abs(code_value<CODES, 0>(vw[i]) * g[0]));
-        vm = fmaxf(vm, finite_abs(code_value<CODES, 1>(vw[i]) * g[1]));
-        vm = fmaxf(vm, finite_abs(code_value<CODES, 2>(vw[i]) * g[2]));
-        vm = fmaxf(vm, finite_abs(code_value<CODES, 3>(vw[i]) * g[3]));
-    }
-    km = wave_max0(km);
-    vm = wave_max0(vm);
-    if (lane == 0) {
-        red[0][tid / 64] = km;
-        red[1][tid / 64] = vm;
-    }
-    __syncthreads();  // all of the page has been read, too
-    km = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    vm = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
-    const int ke = scale_exp<CODES>(km), ve = scale_exp<CODES>(vm);
-    const float ki = pow2(-ke), vi = pow2(-ve);
-#pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
-        // at the page's old scale, tokens that stay keep their codes
-        if (ke == ke_was && ((stay >> t) & 1)) continue;
-        const float f = scale[0][t] * ki;
-        u32x2 w;
-        w[0] = requant4<CODES>(kw[i][0], f);
-        w[1] = requant4<CODES>(kw[i][1], f);
-        *reinterpret_cast<u32x2 *>(kc + t * D + d) = w;
+        for (int i = 0; i < kV; ++i)
+            vw[i] = to_codes4<CODES>(code_value<CODES, 0>(vw[i]) * (g[0] * inv), code_value<CODES, 1>(vw[i]) * (g[1] * inv),
+                                     code_value<CODES, 2>(vw[i]) * (g[2] * inv), code_value<CODES, 3>(vw[i]) * (g[3] * inv));
     }
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-        *reinterpret_cast<uint32_t *>(vc + (dv + i * 16) * kKvPage + t0) = to_codes4<CODES>(
-            code_value<CODES, 0>(vw[i]) * (g[0] * vi), code_value<CODES, 1>(vw[i]) * (g[1] * vi),
-            code_value<CODES, 2>(vw[i]) * (g[2] * vi), code_value<CODES, 3>(vw[i]) * (g[3] * vi));
-    if (tid == 0) {
-        sc[0] = pow2(ke);
-        sc[1] = pow2(ve);
-    }
+    for (int i = 0; i < kV; ++i) *reinterpret_cast<uint32_t *>(vc + (dv + i * 16) * kKvPage + t0) = vw[i];
+    if (tid == 0) sc[1] = pow2(e);
 }
 
 template <int D>
 void fold_go(const KvEvict &a, int codes, hipStream_t s) {
-    const dim3 grid(a.budget / kKvPage, a.c.heads, a.c.batch);
+    const dim3 grid(2 * (a.budget / kKvPage), a.c.heads, a.c.batch);
     if (codes == kE4m3)
         hipLaunchKernelGGL((k_kv_fold<D, kE4m3>), grid, dim3(kFoldThreads), 0, s, a);
     else
