@@ -29,6 +29,43 @@ __device__ inline u32x4 load8(const uint16_t *p) {
     return r;
 }
 
+// Two 16-bit numbers' magnitudes as bits, which ascend with them: the largest
+// finite ones go to `most`; the top bits of `odd` are set by what is not finite.
+template <int DTYPE>
+__device__ inline void max_bits(uint32_t w, uint32_t &most, uint32_t &odd) {
+    const uint32_t m = w & 0x7FFF7FFFu;
+    const uint32_t past = (m + (DTYPE == kBf16 ? 0x00800080u : 0x04000400u)) & 0x80008000u;  // 0x8000 less infinity's
+    odd |= past;
+    most = max_u16x2(most, m & ~((past >> 15) * 0xFFFFu));
+}
+
+// Four finite numbers times inv, a scale's inverse that brings them within
+// the codes' range, to the nearest codes.
+template <int CODES>
+__device__ inline uint32_t finite_codes4(float a, float b, float c, float d, float inv) {
+    if constexpr (CODES == kE4m3) {
+        int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true);
+        return (uint32_t)r;
+    } else {
+        // 1.5 * 2^23 added: a float's last place is then 1, so the sum is
+        // rounded to a whole number (ties to even), its low byte the code
+        const float magic = 12582912.0f;
+        const uint32_t x = __builtin_bit_cast(uint32_t, __builtin_fmaf(a, inv, magic));
+        const uint32_t y = __builtin_bit_cast(uint32_t, __builtin_fmaf(b, inv, magic));
+        const uint32_t z = __builtin_bit_cast(uint32_t, __builtin_fmaf(c, inv, magic));
+        const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_fmaf(d, inv, magic));
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w, z, 0x0C0C0400u), __builtin_amdgcn_perm(y, x, 0x0C0C0400u),
+                                     0x05040100u);
+    }
+}
+
+// The same for any numbers where `odd` says that some are not finite.
+template <int CODES>
+__device__ inline uint32_t codes4(float a, float b, float c, float d, float inv, bool odd) {
+    return odd ? to_codes4<CODES>(a * inv, b * inv, c * inv, d * inv) : finite_codes4<CODES>(a, b, c, d, inv);
+}
+
 template <int DTYPE>
 __device__ inline float nth(const u32x4 &x, int i) {
     return to_float<DTYPE>((uint16_t)(x[i / 2] >> (16 * (i % 2))));
@@ -77,15 +114,20 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(KvAppend a) {
         }
     }
     const int ke0 = exp_of_pow2(sc[0]), ve0 = exp_of_pow2(sc[1]);
+    uint32_t odd_bits = 0;
     if (mine) {
+        uint32_t kb = 0, vb = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                km = fmaxf(km, finite_abs(nth<DTYPE>(k[e], i)));
-                vm = fmaxf(vm, finite_abs(nth<DTYPE>(v[e], i)));
+            for (int i = 0; i < 4; ++i) {
+                max_bits<DTYPE>(k[e][i], kb, odd_bits);
+                max_bits<DTYPE>(v[e][i], vb, odd_bits);
             }
+        km = fmaxf(to_float<DTYPE>((uint16_t)kb), to_float<DTYPE>((uint16_t)(kb >> 16)));
+        vm = fmaxf(to_float<DTYPE>((uint16_t)vb), to_float<DTYPE>((uint16_t)(vb >> 16)));
     }
+    const bool odd = __builtin_amdgcn_ballot_w64(odd_bits != 0) != 0;
     km = wave_max0(km);
     vm = wave_max0(vm);
     if (tid % 64 == 0) {
@@ -121,8 +163,8 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(KvAppend a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t *p = reinterpret_cast<uint32_t *>(vc + (d + i) * kKvPage + t0);
-            uint32_t w = to_codes4<CODES>(nth<DTYPE>(v[0], i) * vi, nth<DTYPE>(v[1], i) * vi,
-                                          nth<DTYPE>(v[2], i) * vi, nth<DTYPE>(v[3], i) * vi);
+            uint32_t w = codes4<CODES>(nth<DTYPE>(v[0], i), nth<DTYPE>(v[1], i), nth<DTYPE>(v[2], i), nth<DTYPE>(v[3], i),
+                                       vi, odd);
             if (fresh != ~0u) {
                 const uint32_t was = *p, again = vf != 1.0f ? requant4<CODES>(was, vf) : was;
                 w = (w & fresh) | (again & older) | (was & ~(fresh | older));
@@ -133,10 +175,10 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(KvAppend a) {
         for (int e = 0; e < 4; ++e) {
             if (t0 + e >= lo && t0 + e < hi) {
                 u32x2 w;
-                w[0] = to_codes4<CODES>(nth<DTYPE>(k[e], 0) * ki, nth<DTYPE>(k[e], 1) * ki,
-                                        nth<DTYPE>(k[e], 2) * ki, nth<DTYPE>(k[e], 3) * ki);
-                w[1] = to_codes4<CODES>(nth<DTYPE>(k[e], 4) * ki, nth<DTYPE>(k[e], 5) * ki,
-                                        nth<DTYPE>(k[e], 6) * ki, nth<DTYPE>(k[e], 7) * ki);
+                w[0] = codes4<CODES>(nth<DTYPE>(k[e], 0), nth<DTYPE>(k[e], 1), nth<DTYPE>(k[e], 2), nth<DTYPE>(k[e], 3),
+                                     ki, odd);
+                w[1] = codes4<CODES>(nth<DTYPE>(k[e], 4), nth<DTYPE>(k[e], 5), nth<DTYPE>(k[e], 6), nth<DTYPE>(k[e], 7),
+                                     ki, odd);
                 *reinterpret_cast<u32x2 *>(kc + (t0 + e) * D + d) = w;
             }
         }

@@ -27,6 +27,7 @@ __device__ inline const float *part_sums(const KvAttend &a, uint64_t all, uint64
     return a.part + (uint64_t)a.splits * all * a.c.dim + row * 2;
 }
 
+constexpr uint32_t kKeptTokens = 2 * kThreads;  // of a workgroup that adds up kept scores
 constexpr uint32_t kFewParts = 16;  // a wave a row, above them a workgroup a row
 
 // Row and head `unit` of sequence b from its parts k = first, first + STEP...
@@ -122,25 +123,28 @@ __global__ __launch_bounds__(kThreads) void k_kv_finish(KvAttend a, uint32_t joi
         put_row<DTYPE>(a, row, lane, top, sum, v);
         return;
     }
-    // weights of 256 tokens of a head from the kept scores (at most 16 rows)
+    // weights of 512 tokens of a head from the kept scores (at most 16 rows)
     const uint32_t y = blockIdx.x - join_blocks, h = y % a.c.heads;
-    const int j = (int)(y / a.c.heads * kThreads) + tid;
-    const int rows = s.count * G;
-    if ((int)(y / a.c.heads * kThreads) >= s.len || rows == 0) return;
+    const int j0 = (int)(y / a.c.heads * kKeptTokens), rows = s.count * G;
+    if (j0 >= s.len || rows == 0) return;
     const uint64_t unit = (uint64_t)b * a.c.heads + h;
-    const float *p = a.scores + (unit * a.score_pages + j / kKvPage) * a.score_rows * kKvPage;
-    p += (j % 16 / 4 * 4 + j % 64 / 16) * (int)a.score_rows * 4 + j % 4;
     // (scores of a page that is none were never written; they are not used)
-    float score[16], was = 0.0f;
-    float *const to = a.weight + unit * a.cap + j;
-    const bool in = j < s.len && (uint64_t)j < a.cap;
-    if (in) {
+    float score[2][16], was[2] = {};
+    bool there[2];
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (r < rows) score[r] = p[r * 4];
-        was = *to;
+    for (int x = 0; x < 2; ++x) {
+        const int j = j0 + x * kThreads + tid;
+        there[x] = j < s.len && (uint64_t)j < a.cap;
+        if (there[x]) {
+            const float *p = a.scores + (unit * a.score_pages + j / kKvPage) * a.score_rows * kKvPage;
+            p += (j % 16 / 4 * 4 + j % 64 / 16) * (int)a.score_rows * 4 + j % 4;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (r < rows) score[x][r] = p[r * 4];
+            was[x] = a.weight[unit * a.cap + j];
+            there[x] = page_offset(a.c, b, j / kKvPage) != kNoPage;
+        }
     }
-    const bool there = in && page_offset(a.c, b, j / kKvPage) != kNoPage;
     if (wave == 0) {  // a row a lane, its parts over the four groups of lanes
         const int r = lane % 16, parts = parts_of(a, s, 0);
         const uint64_t row = (s.first + (r < rows ? r / G : 0)) * heads + (uint64_t)h * G + (r < rows ? r % G : 0);
@@ -169,13 +173,18 @@ __global__ __launch_bounds__(kThreads) void k_kv_finish(KvAttend a, uint32_t joi
         }
     }
     __syncthreads();
-    if (!there) return;
-    const int from = j > s.had ? (j - s.had) * G : 0;  // earlier rows do not see the token
-    float sum = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-        if (r < rows && r >= from) sum = __builtin_fmaf(__builtin_amdgcn_exp2f(score[r] - sm_m[r]), sm_l[r], sum);
-    *to = was + sum;
+    for (int x = 0; x < 2; ++x) {
+        const int j = j0 + x * kThreads + tid;
+        if (!there[x]) continue;
+        const int from = j > s.had ? (j - s.had) * G : 0;  // earlier rows do not see the token
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (r < rows && r >= from)
+                sum = __builtin_fmaf(__builtin_amdgcn_exp2f(score[x][r] - sm_m[r]), sm_l[r], sum);
+        a.weight[unit * a.cap + j] = was[x] + sum;
+    }
 }
 
 template <int D, int CODES, int DTYPE>
@@ -330,7 +339,7 @@ void weigh_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 hipError_t launch_kv_finish(const KvAttend &a, int dtype, hipStream_t s) {
     const uint32_t units = a.max_new * a.c.heads * a.group;
     const uint32_t join = a.splits == 1 ? 0 : a.splits <= kFewParts ? (units + kWaves - 1) / kWaves : units;
-    const uint32_t weigh = a.scores ? (a.max_len + kThreads - 1) / kThreads * a.c.heads : 0;
+    const uint32_t weigh = a.scores ? (a.max_len + kKeptTokens - 1) / kKeptTokens * a.c.heads : 0;
     if (join + weigh == 0) return hipSuccess;
     const dim3 grid(join + weigh, a.c.batch);
     if (dtype == kBf16)
