@@ -575,9 +575,10 @@ def _kv_plane(t, arena, dtype, shape, what: str) -> int:
     """Checks a contiguous [batch, heads, places] tensor; its number of places."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 3 or t.shape[:2] != shape:
-        raise ValueError(f"{what}: expected {dtype} [{shape[0]}, {shape[1]}, places]")
-    _kv_ptr(t, dtype, 0, arena.get_device(), what)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 3 \
+            or t.shape[:2] != shape or not t.is_contiguous() or t.get_device() != arena.get_device():
+        raise ValueError(f"{what}: expected a contiguous {dtype} [{shape[0]}, {shape[1]}, places] "
+                         "on the arena's GPU")
     return t.shape[2]
 
 
