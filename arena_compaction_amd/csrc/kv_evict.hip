@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_list(KvEvict a) {
 
 // A value code stands alone in its 64 bytes: a token's are D such rows apart.
 // Read byte by byte from memory, every lane would cost L1 an access of its
-// own (163 us for 32 x 8190 tokens cut to 4096, where this takes LATER), so
+// own (163 us for 32 x 8190 tokens cut to 4096, where this takes 111), so
 // the strips that hold the page's tokens pass through LDS whole, one after the
 // other -- few, since moved tokens lie in order -- and bytes are picked there.
 // Keys and values of a page are two workgroups: each waits for little, and
