@@ -131,6 +131,17 @@ def test_attend_many_rows(ac, weight):
         assert check_attend(ac, c, lens, q, group, [count, count, 1], weight=weight)[1] == 0
 
 
+@pytest.mark.parametrize("heads,group,dim,codes,dtype", SHAPES)
+@pytest.mark.parametrize("count", [17, 18, 31, 33])
+def test_attend_weights_of_part_tiles(ac, heads, group, dim, codes, dtype, count):
+    """Rows that do not fill their last tile of 16, of the last sequence: no row behind them is there to be read."""
+    lens, counts = [40, 65 + count], [3, count]
+    c = Cache([-(-n // PAGE) for n in lens], heads, dim, codes, fill=0x7F)
+    c.fill_random(lens, 41, spread=2)
+    q = queries(sum(counts), heads * group, dim, dtype, 42)
+    assert check_attend(ac, c, lens, q, group, counts, max_new=count)[1] == 0
+
+
 def test_attend_large_scores(ac):
     """One token takes all the weight; others lie far below it."""
     for dtype, codes in ((torch.bfloat16, INT8), (torch.float16, E4M3)):
