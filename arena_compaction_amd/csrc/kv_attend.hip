@@ -62,6 +62,7 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
     const int see_least = s.had + rb * kRows / G + 1;  // of the block's first row
     f32x4 o[R][kTiles];
     Soft soft[R];
+    Rounding<DTYPE> rounding[R];
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         soft[rt] = Soft{KV_NEG_INF, 0.0f};
@@ -130,20 +131,24 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
             }
         }
         const bool edge = base + kKvPage > see_least;
-        Weights<DTYPE> pw[R][2];
+        u32x4 pw[R][2];
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
             const float fade = soft_scores(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
             float sum = 0.0f;
-            soft_weights(w[rt][0], w[rt][1], pw[rt][0], sum);
-            soft_weights(w[rt][2], w[rt][3], pw[rt][1], sum);
+            pw[rt][0] = soft_weights(w[rt][0], w[rt][1], sum);
+            pw[rt][1] = soft_weights(w[rt][2], w[rt][3], sum);
             soft[rt].l = __builtin_fmaf(sum, pow2(-ei), soft[rt].l);
             if (__builtin_amdgcn_ballot_w64(fade != 1.0f)) {
 #pragma unroll
                 for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[rt][dt][x] *= fade;
+                rounding[rt].fade(fade);
             }
+            rounding[rt].add(pw[rt][0]);
+            rounding[rt].add(pw[rt][1]);
+            rounding[rt].add_exact(sum);
         }
         if (base + kKvPage > s.len) {
 #pragma unroll
@@ -173,8 +178,8 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
             const u32x4 v1 = widen8<CODES, kFp16>(vraw[dt][2], vraw[dt][3]);
 #pragma unroll
             for (int rt = 0; rt < R; ++rt) {
-                o[rt][dt] = weigh_values(v0, pw[rt][0], o[rt][dt]);
-                o[rt][dt] = weigh_values(v1, pw[rt][1], o[rt][dt]);
+                o[rt][dt] = mfma16<kFp16>(v0, pw[rt][0], o[rt][dt]);
+                o[rt][dt] = mfma16<kFp16>(v1, pw[rt][1], o[rt][dt]);
             }
         }
         get_values(next);
@@ -208,7 +213,7 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
         const int x = rt * 16 + n;
         float top = fmaxf(fmaxf(sm_m[0][x], sm_m[1][x]), fmaxf(sm_m[2][x], sm_m[3][x]));
         if (top == KV_NEG_INF) top = 0.0f;
-        const float fade = __builtin_amdgcn_exp2f(soft[rt].m - top);
+        const float fade = __builtin_amdgcn_exp2f(soft[rt].m - top) * rounding[rt].factor();
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll

@@ -68,6 +68,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
     const int most = first < rows ? s.had + last / G + 1 : 0;
     f32x4 o[R][kTiles];
     Soft soft[R];
+    Rounding<DTYPE> rounding[R];
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         soft[rt] = Soft{KV_NEG_INF, 0.0f};
@@ -235,14 +236,15 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
                         for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
                             for (int x = 0; x < 4; ++x) o[rt][dt][x] *= fade[rt];
+                        rounding[rt].fade(fade[rt]);
                     }
                 }
                 // the first half's products run beside the second half's exponents
                 float sum[R] = {};
-                Weights<DTYPE> pw[R][2];
+                u32x4 pw[R][2];
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt)
-                    soft_weights<DTYPE>(w[rt][0], w[rt][1], pw[rt][0], sum[rt]);
+                    pw[rt][0] = soft_weights(w[rt][0], w[rt][1], sum[rt]);
 #pragma unroll
                 for (int at = 0; at < 2 * kBatches; ++at) {
                     if (at + 1 < 2 * kBatches) read_values(at + 1);
@@ -252,26 +254,24 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
 #pragma unroll
                         for (int rt = 0; rt < R; ++rt) {
                             f32x4 &to = o[rt][at % kBatches * kBatch + k];
-                            to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches].high, to);
+                            to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches], to);
                         }
-                    if constexpr (DTYPE == kFp16) {
+                    if (at % kBatches == 0) {
 #pragma unroll
-                        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                            for (int rt = 0; rt < R; ++rt) {
-                                f32x4 &to = o[rt][at % kBatches * kBatch + k];
-                                to = mfma16<kFp16>(vv[at % 2][k], pw[rt][at / kBatches].low, to);
-                            }
+                        for (int rt = 0; rt < R; ++rt) rounding[rt].add(pw[rt][at / kBatches]);
                     }
 #pragma unroll
                     for (int rt = 0; rt < R; ++rt)
                         if (at == (rt < kBatches ? rt : kBatches - 1))
-                            soft_weights<DTYPE>(w[rt][2], w[rt][3], pw[rt][1], sum[rt]);
+                            pw[rt][1] = soft_weights(w[rt][2], w[rt][3], sum[rt]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt)
+                {
                     soft[rt].l = __builtin_fmaf(sum[rt], pow2(-ei), soft[rt].l);
+                    rounding[rt].add_exact(sum[rt]);
+                }
             } else {
                 store(cur ^ 1, now);
             }
@@ -303,11 +303,12 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         const float sum = across_groups(soft[rt].l, [](float x, float y) { return x + y; });
+        const float factor = rounding[rt].factor();
         const int r = first + rt * 16 + n;
         if (r >= rows) continue;
         const uint64_t row = (s.first + r / G) * heads + (uint64_t)h * G + r % G;
         if (active == 1) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = sum == 0.0f ? 0.0f : factor / sum;
 #pragma unroll
             for (int dt = 0; dt < kTiles; ++dt) {
                 u32x2 x;
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
         } else {
             float *part = a.part + ((uint64_t)split * all + row) * D;
 #pragma unroll
-            for (int dt = 0; dt < kTiles; ++dt) *reinterpret_cast<f32x4 *>(part + dt * 16 + g * 4) = o[rt][dt];
+            for (int dt = 0; dt < kTiles; ++dt) *reinterpret_cast<f32x4 *>(part + dt * 16 + g * 4) = o[rt][dt] * factor;
             if (g == 0)
                 *reinterpret_cast<f32x2 *>(a.part + (uint64_t)a.splits * all * D + ((uint64_t)split * all + row) * 2) =
                     f32x2{soft[rt].m, sum};

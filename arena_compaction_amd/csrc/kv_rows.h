@@ -91,49 +91,58 @@ __device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, boo
 }
 
 // Weights of 8 of the lane's tokens as the operand of a product over 32
-// tokens.  float16 rounds a weight by up to 2^-11, an eighth of what an output
-// in bfloat16 is rounded by; beside one in float16 it would show (errors half
-// as large again), so there what the rounding left out is a second operand.
-template <int DTYPE>
-struct Weights {
-    u32x4 high;
-};
-template <>
-struct Weights<kFp16> {
-    u32x4 high, low;
-};
-
-// From the exponents of two tiles; adds the weights' sum to `sum`.
-template <int DTYPE>
-__device__ inline void soft_weights(const f32x4 &w0, const f32x4 &w1, Weights<DTYPE> &p, float &sum) {
-    float e[8], minus = -1.0f;
-    // (kept from the compiler, which would make two instructions of widening
-    // and subtracting; a product with a float16 operand widens by itself)
-    if constexpr (DTYPE == kFp16) asm("" : "+v"(minus));
+// tokens, from the exponents of two tiles; adds the weights' sum to `sum`.
+__device__ inline u32x4 soft_weights(const f32x4 &w0, const f32x4 &w1, float &sum) {
+    float e[8];
+    u32x4 p;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         e[i] = __builtin_amdgcn_exp2f(i < 4 ? w0[i] : w1[i - 4]);
         sum += e[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t both = pack2<kFp16>(e[2 * i], e[2 * i + 1]);
-        p.high[i] = both;
-        if constexpr (DTYPE == kFp16) {
-            const half2v h = __builtin_bit_cast(half2v, both);
-            p.low[i] = pack2<kFp16>(__builtin_fmaf((float)h[0], minus, e[2 * i]),
-                                    __builtin_fmaf((float)h[1], minus, e[2 * i + 1]));
-        }
-    }
+    for (int i = 0; i < 4; ++i) p[i] = pack2<kFp16>(e[2 * i], e[2 * i + 1]);
+    return p;
 }
 
-// to += values x weights, over 32 tokens.
+// float16 rounds a weight by up to 2^-11, an eighth of what an output in
+// bfloat16 is rounded by; beside one in float16 it would show (errors half as
+// large again).  There the weights are summed twice, as they were and as they
+// were rounded, and the result is multiplied by the sums' quotient: of each
+// weight's rounding only what differs from their mean is left, which is least
+// where one or a few large weights make the result (errors a seventh larger;
+// carrying the rest of each weight as a second operand left none, and took 490
+// us where this takes 420, over 8200 tokens x 32 heads of 64).  Both sums are
+// of 2^(t - m) with the value scale in it, so that pages count by what they add.
 template <int DTYPE>
-__device__ inline f32x4 weigh_values(const u32x4 &values, const Weights<DTYPE> &p, f32x4 to) {
-    to = mfma16<kFp16>(values, p.high, to);
-    if constexpr (DTYPE == kFp16) to = mfma16<kFp16>(values, p.low, to);
-    return to;
-}
+struct Rounding {
+    __device__ void add(const u32x4 &) {}
+    __device__ void add_exact(float) {}
+    __device__ void fade(float) {}
+    __device__ float factor() const { return 1.0f; }
+};
+template <>
+struct Rounding<kFp16> {
+    float exact = 0.0f, rounded = 0.0f;  // this lane's shares
+    __device__ void add(const u32x4 &p) {
+        const half2v ones = {(_Float16)1.0f, (_Float16)1.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t two = p[i];
+            rounded = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, two), ones, rounded, false);
+        }
+    }
+    __device__ void add_exact(float sum) { exact += sum; }
+    __device__ void fade(float f) {
+        exact *= f;
+        rounded *= f;
+    }
+    __device__ float factor() const {
+        const auto plus = [](float x, float y) { return x + y; };
+        const float all = across_groups(exact, plus), all_rounded = across_groups(rounded, plus);
+        return all_rounded == 0.0f ? 1.0f : all / all_rounded;
+    }
+};
 
 // Exponent of a page's value scale (a page never written may hold a scale of
 // 0: its 2^-ei must stay finite).
