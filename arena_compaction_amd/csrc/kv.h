@@ -25,6 +25,9 @@ constexpr int kKvExpMin = -64;    // least exponent of a scale
 constexpr uint32_t kKvMaxDim = 256;
 constexpr uint32_t kKvPromptRows = 128;  // query rows of a workgroup over a prompt
 
+// Waves of a workgroup that makes weights from the keys again.
+inline __host__ __device__ constexpr uint32_t kv_weigh_waves(uint32_t dim) { return dim <= 64 ? 16 : 8; }
+
 inline __host__ __device__ uint64_t kv_page_bytes(uint32_t heads, uint32_t dim) {
     return (uint64_t)heads * (2ull * kKvPage * dim + 8);
 }
@@ -73,6 +76,10 @@ struct KvAttend {
     float *scores;   // [batch][heads][score_pages][tile 4][group 4][score_rows][4], or null
     uint32_t score_pages, score_rows;
     float2 *sums;    // [tokens * heads * group]: m and 1 / sum of 2^(t - m), or null
+    // weights made from the keys again: pieces of the rows, tiles of 16 rows
+    // in each, and what each piece adds to a token (where there is more than one)
+    uint32_t weigh_pieces, weigh_tiles;
+    float *weigh_part;  // [pieces][batch][heads][score_pages][64]
 };
 
 struct KvEvict {
@@ -103,8 +110,8 @@ struct KvEvictPlan {
 KvEvictPlan kv_evict_plan(uint32_t batch, uint32_t heads, uint32_t budget, uint32_t max_len);
 
 struct KvAttendPlan {
-    uint32_t rows, row_blocks, splits, per_split, score_rows;
-    uint64_t part_bytes, score_bytes, sum_bytes, total;
+    uint32_t rows, row_blocks, splits, per_split, score_rows, weigh_pieces, weigh_tiles;
+    uint64_t part_bytes, score_bytes, sum_bytes, weigh_bytes, total;
 };
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,

@@ -185,6 +185,9 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     k.score_pages = (a->max_len + kKvPage - 1) / kKvPage;
     k.score_rows = p.score_rows;
     k.sums = p.sum_bytes ? reinterpret_cast<float2 *>(ws + p.part_bytes + p.score_bytes) : nullptr;
+    k.weigh_pieces = p.weigh_pieces;
+    k.weigh_tiles = p.weigh_tiles;
+    k.weigh_part = p.weigh_bytes ? reinterpret_cast<float *>(ws + p.part_bytes + p.score_bytes + p.sum_bytes) : nullptr;
     return launch_kv_attend(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
 }
 

@@ -329,7 +329,24 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
         p.score_bytes = (uint64_t)batch * heads * pages * rows * kKvPage * 4;
     }
     p.sum_bytes = scored ? (all * 8 + 255) / 256 * 256 : 0;
-    p.total = p.part_bytes + p.score_bytes + p.sum_bytes;
+    if (scored && !p.score_rows) {
+        // A workgroup a (page, head).  Where those are fewer than compute
+        // units, each takes a piece of the rows, of at least 4 turns of its
+        // waves, and another launch adds up (2 x 206 tokens x 3 heads of 256,
+        // 16 query heads each, 24 (page, head)s: whole 36 us, in 7 pieces 21);
+        // where they are more, pieces cost what their starts take (516: whole
+        // 250 us, in 4 pieces 293).
+        const uint64_t cells = (uint64_t)batch * heads * pages, waves = kv_weigh_waves(dim);
+        const uint64_t turns = ((rows + 15) / 16 + waves - 1) / waves, most = (turns + 3) / 4;
+        uint64_t pieces = cells == 0 || cells >= 256 ? 1 : (512 + cells - 1) / cells;
+        if (pieces > most) pieces = most;
+        if (pieces < 1) pieces = 1;
+        const uint64_t each = (turns + pieces - 1) / pieces;
+        p.weigh_tiles = (uint32_t)(each * waves);
+        p.weigh_pieces = (uint32_t)(turns ? (turns + each - 1) / each : 1);
+        if (p.weigh_pieces > 1) p.weigh_bytes = cells * p.weigh_pieces * kKvPage * 4;
+    }
+    p.total = p.part_bytes + p.score_bytes + p.sum_bytes + p.weigh_bytes;
     return p;
 }
 

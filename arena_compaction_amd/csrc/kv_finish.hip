@@ -9,7 +9,7 @@
 //                work out m and l from the parts themselves;
 //   k_kv_weigh   many rows: makes the scores again.  One workgroup a (page,
 //                head) holds the page's keys and goes over all the rows that
-//                see it.
+//                see it, or a piece of them, whose sums k_kv_add adds up.
 // The second is bound by the vector pipe (65% of the cycles) with an exponent
 // and two fused products a score: 250 us for 8200 tokens x 32 heads of 64.  The
 // first moves 36 MB for 48 x 8000 tokens x 4 heads, 28 of them scores, in 14 us.
@@ -191,21 +191,36 @@ __global__ __launch_bounds__(kThreads) void k_kv_finish(KvAttend a, uint32_t joi
     }
 }
 
+// Tiles of 16 rows [first, end) of a piece of the rows that see something of
+// the page from token `base` on; none: false.
+__device__ inline bool piece_tiles(const KvAttend &a, const Seq &s, int base, int piece, int *first, int *end) {
+    const int tiles = (s.count * (int)a.group + 15) / 16, each = (int)a.weigh_tiles;
+    const int least = base > s.had ? (base - s.had) * (int)a.group / 16 : 0;  // earlier rows see nothing here
+    *first = least > piece * each ? least : piece * each;
+    *end = tiles < (piece + 1) * each ? tiles : (piece + 1) * each;
+    return *first < *end;
+}
+
 template <int D, int CODES, int DTYPE>
-__global__ __launch_bounds__(D <= 64 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
-    constexpr int kSteps = D / 32, kN = D <= 64 ? 16 : 8;  // waves
+__global__ __launch_bounds__(kv_weigh_waves(D) * 64) void k_kv_weigh(KvAttend a) {
+    constexpr int kSteps = D / 32, kN = (int)kv_weigh_waves(D);
     constexpr int kPieces = D / 8, kPitch = kPieces + 1;  // of 16 bytes; odd, so that rows start in other banks
     __shared__ float sm[kN][kKvPage];
     __shared__ u32x4 sm_q[kN][16 * kPitch];
-    // heads first: the first pages, which most rows see, start first
+    // the last rows first: every page's rows end there, so that workgroups
+    // that start together read the same queries
     const uint32_t units = a.c.heads * a.c.batch, unit = blockIdx.x % units;
     const uint32_t h = unit % a.c.heads, b = unit / a.c.heads;
+    const uint32_t piece = a.weigh_pieces - 1 - blockIdx.x / (units * a.score_pages);
     const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
     const int n = lane % 16, g = lane / 16, G = (int)a.group;
     bool bad;
     const Seq s = sequence(a, b, &bad);
-    const int p = (int)(blockIdx.x / units), base = p * kKvPage;
+    const int p = (int)(blockIdx.x / units % a.score_pages), base = p * kKvPage;
     if (base >= s.len || s.count == 0) return;
+    const int rows = s.count * (int)a.group;
+    int first, tiles;
+    if (!piece_tiles(a, s, base, (int)piece, &first, &tiles)) return;
     const uint64_t off = wave_uniform(page_offset(a.c, b, p));
     if (off == kNoPage) return;
     const float f = a.scale * kLog2e * page_scales(a.c, a.c.arena + off, h)[0];
@@ -221,19 +236,17 @@ __global__ __launch_bounds__(D <= 64 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
             }
     }
     float acc[16] = {};
-    const int rows = s.count * G;
     const uint64_t heads = (uint64_t)a.c.heads * G;
     // Tiles of 16 rows, every kN-th, from the last one down, since all pages'
-    // rows end there: workgroups that start together read the same queries
-    // together, out of L2.  A tile's first token is the wave's (t0) and its
+    // rows end there: workgroups that start together go through the same
+    // queries together, out of L2.  A tile's first token is the wave's (t0) and its
     // address scalar; a lane adds where its row lies from there, which is the
     // same in every turn where the group's heads divide the rows of a turn.
     // Queries are loaded with neighbouring lanes on neighbouring bytes and
     // dealt out through LDS, each wave's own: as the operand wants them,
     // neighbouring lanes on neighbouring rows, L1 would serve 16 bytes at a
     // time, and be what the kernel waits for.
-    const int least = (base > s.had ? (base - s.had) * G / 16 : 0) + wave;  // earlier rows see nothing here
-    const int tiles = (rows + 15) / 16;
+    const int least = first + wave;
     const int turns = tiles > least ? (tiles - least + kN - 1) / kN : 0;
     const uint32_t by_group = ((1u << 20) + G - 1) / G;  // v / G = v * by_group >> 20 for v < G + 16
     const bool same = kN * 16 % G == 0;
@@ -315,17 +328,38 @@ __global__ __launch_bounds__(D <= 64 ? 1024 : 512) void k_kv_weigh(KvAttend a) {
         if (n == 0) sm[wave][g * 16 + i] = v;
     }
     __syncthreads();
-    if (tid < kKvPage && base + tid < s.len && (uint64_t)(base + tid) < a.cap) {
+    if (tid < kKvPage && base + tid < s.len) {
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < kN; ++k) sum += sm[k][tid];
-        a.weight[((uint64_t)b * a.c.heads + h) * a.cap + base + tid] += sum;
+        if (a.weigh_part)
+            a.weigh_part[(((uint64_t)piece * a.c.batch + b) * a.c.heads + h) * a.score_pages * kKvPage + base + tid] = sum;
+        else
+            a.weight[((uint64_t)b * a.c.heads + h) * a.cap + base + tid] += sum;
     }
+}
+
+// Adds up what the pieces of the rows made, a token a lane, in their order.
+__global__ __launch_bounds__(kThreads) void k_kv_add(KvAttend a) {
+    const uint32_t h = blockIdx.y, b = blockIdx.z;
+    const int j = (int)(blockIdx.x * kThreads + threadIdx.x), base = j / kKvPage * kKvPage;
+    bool bad;
+    const Seq s = sequence(a, b, &bad);
+    if (j >= s.len || s.count == 0) return;
+    if (page_offset(a.c, b, j / kKvPage) == kNoPage) return;
+    const uint64_t unit = (uint64_t)b * a.c.heads + h, step = (uint64_t)a.c.batch * a.c.heads * a.score_pages * kKvPage;
+    const float *part = a.weigh_part + unit * a.score_pages * kKvPage + j;
+    float sum = 0.0f;
+    for (uint32_t k = 0; k < a.weigh_pieces; ++k) {
+        int first, tiles;
+        if (piece_tiles(a, s, base, (int)k, &first, &tiles)) sum += part[k * step];
+    }
+    a.weight[unit * a.cap + j] += sum;
 }
 
 template <int D, int CODES>
 void weigh_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid(a.c.heads * a.c.batch * ((a.max_len + kKvPage - 1) / kKvPage)), block(D <= 64 ? 1024 : 512);
+    const dim3 grid(a.c.heads * a.c.batch * a.score_pages * a.weigh_pieces), block(kv_weigh_waves(D) * 64);
     if (dtype == kBf16)
         hipLaunchKernelGGL((k_kv_weigh<D, CODES, kBf16>), grid, block, 0, s, a);
     else
@@ -364,6 +398,10 @@ hipError_t launch_kv_weigh(const KvAttend &a, int codes, int dtype, hipStream_t 
         case 192: weigh_codes<192>(a, codes, dtype, s); break;
         case 256: weigh_codes<256>(a, codes, dtype, s); break;
         default: return hipErrorInvalidValue;
+    }
+    if (a.weigh_part) {
+        const dim3 grid((a.max_len + kThreads - 1) / kThreads, a.c.heads, a.c.batch);
+        hipLaunchKernelGGL(k_kv_add, grid, dim3(kThreads), 0, s, a);
     }
     return hipGetLastError();
 }

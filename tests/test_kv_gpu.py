@@ -142,6 +142,16 @@ def test_attend_weights_of_part_tiles(ac, heads, group, dim, codes, dtype, count
     assert check_attend(ac, c, lens, q, group, counts, max_new=count)[1] == 0
 
 
+@pytest.mark.parametrize("dim,codes,dtype", [(64, E4M3, torch.float16), (128, INT8, torch.bfloat16), (256, E4M3, torch.bfloat16)])
+def test_attend_weights_in_pieces(ac, dim, codes, dtype):
+    """Few heads and many rows: each page's weights are made in pieces of the rows, ends of which see nothing of it."""
+    lens, counts = [700, 130, 0, 450], [611, 129, 0, 1]
+    c = Cache([-(-n // PAGE) for n in lens], 1, dim, codes, fill=0x7F)
+    c.fill_random(lens, 43, spread=2)
+    q = queries(sum(counts), 7, dim, dtype, 44)
+    assert check_attend(ac, c, lens, q, 7, counts, max_new=611)[1] == 0
+
+
 def test_attend_large_scores(ac):
     """One token takes all the weight; others lie far below it."""
     for dtype, codes in ((torch.bfloat16, INT8), (torch.float16, E4M3)):
