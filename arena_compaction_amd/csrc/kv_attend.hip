@@ -296,6 +296,43 @@ void attend_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 // a workgroup share a page brought to 16 bits once, in LDS.
 constexpr uint64_t kFewRows = 32;
 
+namespace {
+
+// Pieces of the cache for few rows.  Workgroups in flight are 3 a compute unit
+// with 16 rows, 2 with more.  The lengths differ, so few heads are cut into a
+// third more pieces than that, which even out; where the heads alone nearly
+// fill the unit, a cut leaves a few pieces over and costs more than it evens
+// out (64 sequences x 8 heads: whole 62 us, in halves 73).
+uint64_t few_splits(uint64_t units, uint32_t rows) {
+    const uint64_t target = rows == 16 ? 1024 : 512;
+    return units == 0 || units >= 512 ? 1 : (target + units - 1) / units;
+}
+
+// Pieces for many rows: those that should end first.  A step is a page; beside
+// another workgroup on its compute unit one takes 2 us for 128 dimensions,
+// alone 1.5 (above 128 dimensions it always is); a cut costs 18 us, and 1 us for
+// 40 workgroups, since each writes its sums for the join (one sequence, 16
+// query heads a head, 8 heads of 128, 63 pages: 128 tokens whole 96 us, in 2
+// pieces 75, in 4 64, in 8 74; 256 tokens whole 106, in 4 pieces 113).
+uint64_t prompt_splits(uint64_t units, uint64_t pages, uint32_t max_new, uint32_t dim) {
+    const uint64_t slots = dim <= 128 ? 512 : 256;
+    uint64_t best = 1, least = ~0ull;
+    if (units == 0 || units >= slots) return 1;
+    const uint64_t own = max_new / (2 * kKvPage), seen = pages > own ? pages - own : 1;  // by a mean row
+    for (uint64_t n = 1; n <= pages && units * n <= 2 * slots; n += n / 8 + 1) {
+        const uint64_t per = (pages + n - 1) / n, jobs = units * ((seen + per - 1) / per), rounds = (jobs + slots - 1) / slots;
+        const uint64_t step = dim <= 128 && jobs <= 256 ? 3 : 4;  // in half microseconds of 128 dimensions
+        const uint64_t cost = rounds * per * step + (n > 1 ? 36 + jobs / 20 : 0);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
                             uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
     KvAttendPlan p{};
@@ -306,13 +343,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    // Workgroups in flight are 3 a compute unit with 16 rows, 2 with more.
-    // The lengths differ, so few heads are cut into a third more pieces than
-    // that, which even out; where the heads alone nearly fill the unit, a cut
-    // leaves a few pieces over and costs more than it evens out (64 sequences
-    // x 8 heads: whole 62 us, in halves 73).
-    const uint64_t target = p.rows == 16 ? 1024 : 512;
-    uint64_t splits = units == 0 || units >= 512 ? 1 : (target + units - 1) / units;
+    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, p.rows);
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave
