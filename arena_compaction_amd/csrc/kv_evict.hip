@@ -529,6 +529,12 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_list(KvEvict a) {
     }
 }
 
+// Old scale over new one.  Every code but 0 and NaN fits the new scale, so its
+// quotient is at most 448 / 2^-9; a kept token of zeros may come from a page
+// whose scale is any number of powers larger, and has to stay zeros where the
+// quotient would be infinite.
+__device__ inline float scale_quotient(float was, float inv) { return fminf(was * inv, 0x1p18f); }
+
 // A value code stands alone in its 64 bytes: a token's are D such rows apart.
 // Read byte by byte from memory, every lane would cost L1 an access of its
 // own (163 us for 32 x 8190 tokens cut to 4096, where this takes 111), so
@@ -604,7 +610,7 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
             const int item = tid + i * kFoldThreads, t = item / kPer, d = item % kPer * 8;
             // at the page's old scale, tokens that stay keep their codes
             if (e == e_was && ((stay >> t) & 1)) continue;
-            const float f = scale[t] * inv;
+            const float f = scale_quotient(scale[t], inv);
             u32x2 w = kw[i];
             if (f != 1.0f) {
                 w[0] = requant4<CODES>(w[0], f);
@@ -660,11 +666,13 @@ __global__ __launch_bounds__(kFoldThreads) void k_kv_fold(KvEvict a) {
     const int e = scale_exp<CODES>(most);
     const float inv = pow2(-e);
     // codes of a scale that stays are the new ones as they are
-    if (g[0] * inv != 1.0f || g[1] * inv != 1.0f || g[2] * inv != 1.0f || g[3] * inv != 1.0f) {
+    const float f[4] = {scale_quotient(g[0], inv), scale_quotient(g[1], inv), scale_quotient(g[2], inv),
+                        scale_quotient(g[3], inv)};
+    if (f[0] != 1.0f || f[1] != 1.0f || f[2] != 1.0f || f[3] != 1.0f) {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-            vw[i] = to_codes4<CODES>(code_value<CODES, 0>(vw[i]) * (g[0] * inv), code_value<CODES, 1>(vw[i]) * (g[1] * inv),
-                                     code_value<CODES, 2>(vw[i]) * (g[2] * inv), code_value<CODES, 3>(vw[i]) * (g[3] * inv));
+            vw[i] = to_codes4<CODES>(code_value<CODES, 0>(vw[i]) * f[0], code_value<CODES, 1>(vw[i]) * f[1],
+                                     code_value<CODES, 2>(vw[i]) * f[2], code_value<CODES, 3>(vw[i]) * f[3]);
     }
 #pragma unroll
     for (int i = 0; i < kV; ++i) *reinterpret_cast<uint32_t *>(vc + (dv + i * 16) * kKvPage + t0) = vw[i];
