@@ -316,7 +316,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
                 x[1] = pack2<DTYPE>(o[rt][dt][2] * inv, o[rt][dt][3] * inv);
                 *reinterpret_cast<u32x2 *>(a.out + row * D + dt * 16 + g * 4) = x;
             }
-            if (g == 0) put_sum(a, row, soft[rt].m, sum);
+            if (g == 0) put_sum(a, row, soft[rt].m == KV_NEG_INF ? 0.0f : soft[rt].m, sum);
         } else {
             float *part = a.part + ((uint64_t)split * all + row) * D;
 #pragma unroll

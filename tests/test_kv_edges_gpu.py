@@ -6,13 +6,16 @@ the bounds that kv_plain.attend derives, plus half a step of the output's type
 (bf16 2^-8, fp16 2^-11 of the value)."""
 import math
 
+import math
+
 import pytest
 import torch
 
-from kv_plain import PAGE, Cache, evict
+from kv_plain import PAGE, Cache, attend, evict
 
 pytestmark = pytest.mark.gpu
 E4M3, INT8 = torch.float8_e4m3fn, torch.int8
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 
 
 @pytest.fixture(scope="module")
@@ -77,3 +80,47 @@ def test_evict_zeros_of_a_large_scale(ac, codes, dim, power, beside):
     if beside == "zeros":
         assert not c.head(int(c.pages[0, 0]), 0)[0].float().any()
     same_pages(c, arena)
+
+
+# ---- attend: rows whose every score is -infinity ----------------------------
+
+@pytest.mark.parametrize("heads,group,dim,codes,dtype,past,count", [
+    (2, 1, 64, E4M3, torch.bfloat16, 60, 40),       # many rows, weights from the keys again
+    (1, 4, 128, INT8, torch.float16, 700, 80),      # in pieces, the cache cut
+    (1, 2, 256, E4M3, torch.float16, 3, 200),
+    (2, 2, 64, INT8, torch.bfloat16, 300, 5),       # few rows, from the keys again
+    (2, 2, 64, E4M3, torch.float16, 300, 2),        # from kept scores
+    (1, 8, 192, E4M3, torch.bfloat16, 4990, 1)])    # from kept scores, the cache cut
+def test_attend_rows_of_minus_infinity(ac, heads, group, dim, codes, dtype, past, count):
+    """Their sums are empty: output 0, logarithm -infinity, and no weight for
+    any token from them; the others are as they would be without them."""
+    n = past + count
+    c = Cache([-(-n // PAGE)], heads, dim, codes, fill=0x7F)
+    c.fill_random([n], 71)
+    for off in c.pages[0].tolist():
+        for h in range(heads):
+            c.head(off, h)[0].view(torch.uint8)[:, 0] = 0x30   # e4m3 0.5, int8 48: above 0
+    gen = torch.Generator().manual_seed(72)
+    q = torch.randn(count, heads * group, dim, generator=gen).to(dtype)
+    none = torch.zeros(count, heads * group, dtype=torch.bool)
+    none[::3, ::2] = True
+    calm = torch.where(none[..., None], torch.zeros_like(q), q)
+    q = calm.clone()
+    q[..., 0] = torch.where(none, -math.inf, q[..., 0])
+    out_, bound, lse_, lbound, _, wbound = attend(c, [n], calm, group, [count], dim ** -0.5)
+    add = torch.zeros(heads, n, dtype=torch.float64)
+    for h in range(heads):
+        k = c.numbers(0, n, h)[0]
+        for g in range(group):
+            s = calm[:, h * group + g].double() @ k.t() * dim ** -0.5
+            s = s.masked_fill(torch.arange(n)[None, :] > past + torch.arange(count)[:, None], -math.inf)
+            add[h] += torch.softmax(s, -1)[~none[:, h * group + g]].sum(0)
+    lse = torch.empty(count, heads * group, device="cuda")
+    w = torch.full((1, heads, c.pages.shape[1] * PAGE + 3), 0.25, device="cuda")
+    out = ac.defrag_kv_attend(c.arena.cuda(), c.pages.cuda(), ints([n]), q.cuda(), heads, codes, starts=ints([0, count]),
+                              lse=lse, weight=w).double().cpu()
+    lse, w = lse.double().cpu(), w[0].double().cpu()
+    assert (out[none] == 0).all() and (lse[none] == -math.inf).all()
+    assert ((out - out_).abs() <= bound * (1 + HALF[dtype]) + out_.abs() * HALF[dtype] + 2.0 ** -25)[~none].all()
+    assert ((lse - lse_).abs() <= lbound + 2.0 ** -22)[~none].all()
+    assert ((w[:, :n] - 0.25 - add).abs() <= wbound[0] + (add + 0.25) * 2.0 ** -23).all() and (w[:, n:] == 0.25).all()
