@@ -10,7 +10,11 @@
 // the value scale inside the exponent, w_rj = 2^(t_rj - m) multiplies value
 // codes of any page, and sum_j w_rj / ev is the softmax's sum, one factor a
 // page.  m lies 13 to 15 below the running maximum of t: float16 weights then
-// reach down to 2^-37 of the largest before they lose their last bit.
+// reach down to 2^-37 of the largest before they lose their last bit.  With
+// the value scale in them that is a reach of w * ev, and a token of small
+// values behind one of large values would lose what it gives to dimensions
+// where the large ones are 0; pages therefore go by bands of value scales,
+// small ones first (kBand in kv_rows.h).
 //
 // A wave takes whole pages, one at a time, with its own running maximum and
 // sums; a page's codes are loaded while the page before it is summed, keys
@@ -90,15 +94,31 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt) vraw[dt] = *reinterpret_cast<const u32x4 *>(from + dt * 16 * kKvPage);
     };
-    // positions of the set bits of `good` are the pages that are there
-    uint64_t todo = good;
+    // positions of the set bits of `good` are the pages that are there; of
+    // `todo` those of the band under way, of `later` the bands above it
+    uint64_t todo = 0, later = good;
     uint32_t no_numbers = 0;
-    if (todo) {
-        get_keys(__builtin_ctzll(todo));
-        get_values(__builtin_ctzll(todo));
+    if (good) {
+        get_keys(__builtin_ctzll(good));
+        get_values(__builtin_ctzll(good));
     }
     arrived(scales[0]);
     arrived(scales[1]);
+    const int exp_here = off == kNoPage ? kNoExp : value_exp(scales[1]);
+    auto next_band = [&]() __attribute__((always_inline)) {
+        const int left = (later >> lane) & 1 ? exp_here : kNoExp;
+        todo = later & __builtin_amdgcn_ballot_w64(left <= least_of(left) + kBand);
+        later &= ~todo;
+    };
+    const int near = exp_here - __builtin_amdgcn_readlane(exp_here, good ? __builtin_ctzll(good) : 0) + kBand / 2;
+    if (good & __builtin_amdgcn_ballot_w64(near < 0 || near > kBand)) {
+        next_band();
+        get_keys(__builtin_ctzll(todo));
+        get_values(__builtin_ctzll(todo));
+    } else {  // one band
+        todo = good;
+        later = 0;
+    }
     while (todo) {
         const int i = __builtin_ctzll(todo);
         todo &= todo - 1;
@@ -183,6 +203,11 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
             }
         }
         get_values(next);
+        if (!todo && later) {
+            next_band();
+            get_keys(__builtin_ctzll(todo));
+            get_values(__builtin_ctzll(todo));
+        }
     }
     if constexpr (CODES == kE4m3) {
         if (__builtin_amdgcn_ballot_w64(no_numbers != 0)) {

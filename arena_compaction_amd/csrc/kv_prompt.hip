@@ -79,14 +79,40 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
     __syncthreads();
 
     const uint8_t *strips = a.c.arena + (uint64_t)h * 2 * kKvPage * D;
-    for (int p0 = p_lo; p0 < p_hi; p0 += 64) {
+    // Bands of value scales (kv_rows.h).  Up to 64 pages their scales are at
+    // hand in the one turn of the loop below; where there are more, all are
+    // read first, 256 pages at a time.
+    const bool many = p_hi - p_lo > 64;
+    int from = kNoExp, highest = -kNoExp;
+    if (many) {
+        for (int p0 = p_lo + lane; p0 < p_hi + lane; p0 += 256) {
+            uint64_t off[4];
+            float scale[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) off[x] = p0 + x * 64 < p_hi ? page_offset(a.c, b, p0 + x * 64) : kNoPage;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (off[x] != kNoPage) scale[x] = page_scales(a.c, a.c.arena + off[x], h)[1];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (off[x] == kNoPage) continue;
+                const int e = value_exp(scale[x]);
+                from = e < from ? e : from;
+                highest = e > highest ? e : highest;
+            }
+        }
+        from = least_of(from);
+        highest = most_of(highest);
+    }
+    bool first_band = true;
+    for (int p0 = p_lo; p0 < p_hi;) {
         const int np = p_hi - p0 < 64 ? p_hi - p0 : 64;
         const uint64_t off = lane < np ? page_offset(a.c, b, p0 + lane) : kNoPage;
-        const uint64_t good = __builtin_amdgcn_ballot_w64(off != kNoPage);
+        const uint64_t there = __builtin_amdgcn_ballot_w64(off != kNoPage);
         f32x2 scales = {0, 0};
         if (off != kNoPage) scales = *reinterpret_cast<const f32x2 *>(page_scales(a.c, a.c.arena + off, h));
-        if (counts && __builtin_popcountll(good) != np)
-            atomicAdd(a.c.n_invalid, (unsigned long long)(np - __builtin_popcountll(good)));
+        if (counts && first_band && __builtin_popcountll(there) != np)
+            atomicAdd(a.c.n_invalid, (unsigned long long)(np - __builtin_popcountll(there)));
         struct Raw {
             u32x4 k[kKeyJobs], v[kValueJobs];
         };
@@ -161,6 +187,16 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
         };
         arrived(scales[0]);
         arrived(scales[1]);
+        const int exp_here = off == kNoPage ? kNoExp : value_exp(scales[1]);
+        if (!many && first_band && there) {
+            const int e0 = __builtin_amdgcn_readlane(exp_here, __builtin_ctzll(there)), near = exp_here - e0 + kBand / 2;
+            from = e0 - kBand / 2;
+            if (there & __builtin_amdgcn_ballot_w64(near < 0 || near > kBand)) {  // not one band
+                from = least_of(exp_here);
+                highest = most_of(off == kNoPage ? -kNoExp : exp_here);
+            }
+        }
+        const uint64_t good = there & __builtin_amdgcn_ballot_w64(exp_here >= from && exp_here <= from + kBand);
         // page i is summed from LDS while the next one's codes, loaded two
         // pages before, are brought to 16 bits, and a third page's are loaded
         uint64_t todo = good;
@@ -283,6 +319,11 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
             sum_page(0, rz, ra);
             if (i < 0) break;
             sum_page(1, ra, rz);
+        }
+        p0 += 64;
+        if (p0 >= p_hi && (from += kBand + 1) <= highest) {  // once more, over the next band
+            first_band = false;
+            p0 = p_lo;
         }
     }
     if constexpr (CODES == kE4m3) {

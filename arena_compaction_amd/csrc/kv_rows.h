@@ -151,6 +151,21 @@ __device__ inline int value_exp(float scale) {
     return e < -100 ? -100 : e;
 }
 
+// A running maximum holds for pages whose value scales are at most 2^kBand
+// apart; pages are taken by such bands, from the smallest scales up.  A larger
+// scale that comes later makes the earlier sums fade in 32 bits, where nothing
+// is lost; the other way round it would leave the later weights below what
+// float16 holds.  A page's weight is then rounded as if it were at least
+// 2^(kBand - 38) of the row's sum.  Most caches are one band, seen by a ballot.
+constexpr int kBand = 8;
+constexpr int kNoExp = 1 << 20;  // of a page that is none: above every exponent
+__device__ inline int least_of(int e) {
+    return wave_reduce(e, [](int x, int y) { return x < y ? x : y; });
+}
+__device__ inline int most_of(int e) {
+    return wave_reduce(e, [](int x, int y) { return x > y ? x : y; });
+}
+
 // Codes of four tokens from place k on, of which the first `there` are the
 // cache's own; the others may hold no numbers and become 0.
 __device__ inline uint32_t only_there(uint32_t codes, int there) {

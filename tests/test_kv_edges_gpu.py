@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from kv_plain import PAGE, Cache, attend, evict
+from test_kv_gpu import queries
 
 pytestmark = pytest.mark.gpu
 E4M3, INT8 = torch.float8_e4m3fn, torch.int8
@@ -124,3 +125,67 @@ def test_attend_rows_of_minus_infinity(ac, heads, group, dim, codes, dtype, past
     assert ((out - out_).abs() <= bound * (1 + HALF[dtype]) + out_.abs() * HALF[dtype] + 2.0 ** -25)[~none].all()
     assert ((lse - lse_).abs() <= lbound + 2.0 ** -22)[~none].all()
     assert ((w[:, :n] - 0.25 - add).abs() <= wbound[0] + (add + 0.25) * 2.0 ** -23).all() and (w[:, n:] == 0.25).all()
+
+
+# ---- attend: value scales far apart -----------------------------------------
+
+def far_apart(heads, dim, codes, n, power, where):
+    """Pages of large values that are 0 in the upper half of the dimensions, and pages of small ones."""
+    pages = -(-n // PAGE)
+    c = Cache([pages], heads, dim, codes, fill=0x7F)
+    gen = torch.Generator().manual_seed(81)
+    for j in range(pages):
+        k, v = torch.randn(2, min(PAGE, n - j * PAGE), heads, dim, generator=gen).unbind()
+        large = {"first": j == 0, "between": j % 3 == 1, "steps": j % 4 != 3, "waves": j // 4 % 3 == 0}[where]
+        if large:
+            v[..., dim // 2:] = 0.0
+            v *= 2.0 ** (power if where != "steps" else power * (3 - j % 4) / 3)
+        c.append_page(0, j, k, v)
+    return c
+
+
+def check_far_apart(c, out, lse, q, group, n):
+    """A weight may be off by 2^-30 of the row's largest instead of kv_plain's
+    2^-38: 2^8 lies between a band's scales."""
+    count, dtype = q.shape[0], q.dtype
+    want, bound, lse_, lbound, _, _ = attend(c, [n], q, group, [count], c.D ** -0.5)
+    floor = torch.stack([c.numbers(0, n, h)[1].abs().sum(0) for h in range(c.H)]).repeat_interleave(group, 0) * 2.0 ** -30
+    out, lse = out.double().cpu(), lse.double().cpu()
+    past = torch.isinf(out) & (want * out.sign() + bound >= torch.finfo(dtype).max)
+    err = torch.where(past, 0.0, out - want).abs()
+    tol = (bound + floor) * (1 + HALF[dtype]) + want.abs() * HALF[dtype] + 2.0 ** -25
+    assert (err <= tol).all(), f"{(err / tol).max()} of the bound"
+    assert ((lse - lse_).abs() <= lbound + 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("heads,group,dim,codes,dtype,n,count", [
+    (1, 4, 64, INT8, torch.bfloat16, 400, 100), (1, 3, 128, E4M3, torch.float16, 400, 150),
+    (1, 2, 64, E4M3, torch.bfloat16, 4300, 70), (1, 2, 192, INT8, torch.float16, 300, 40),
+    (2, 2, 96, E4M3, torch.bfloat16, 300, 90), (1, 2, 256, E4M3, torch.bfloat16, 500, 60)])
+@pytest.mark.parametrize("power", [12, 31, 50, 100])
+@pytest.mark.parametrize("where", ["first", "between", "steps"])
+def test_attend_value_scales_far_apart(ac, heads, group, dim, codes, dtype, n, count, power, where):
+    """Where the large pages are 0 the small ones alone make the output, to its
+    full accuracy wherever the large ones lie: many rows."""
+    c = far_apart(heads, dim, codes, n, power, where)
+    q = queries(count, heads * group, dim, dtype, 82)
+    lse = torch.empty(count, heads * group, device="cuda")
+    out = ac.defrag_kv_attend(c.arena.cuda(), c.pages.cuda(), ints([n]), q.cuda(), heads, codes, starts=ints([0, count]), lse=lse)
+    check_far_apart(c, out, lse, q, group, n)
+
+
+@pytest.mark.parametrize("heads,group,dim,codes,dtype,count", [
+    (2, 2, 64, E4M3, torch.bfloat16, 1), (1, 4, 128, INT8, torch.float16, 5), (2, 8, 96, E4M3, torch.float16, 4),
+    (1, 4, 192, INT8, torch.bfloat16, 2), (1, 4, 256, E4M3, torch.float16, 3)])
+@pytest.mark.parametrize("power", [12, 31, 50, 100])
+@pytest.mark.parametrize("where", ["first", "waves", "steps"])
+def test_attend_value_scales_far_apart_few_rows(ac, heads, group, dim, codes, dtype, count, power, where):
+    """The same for few rows, of so many sequences (over the same pages) that a wave has several pages."""
+    n, B = 1500, 520 // heads
+    c = far_apart(heads, dim, codes, n, power, where)
+    q = queries(count, heads * group, dim, dtype, 83)
+    lse = torch.empty(B * count, heads * group, device="cuda")
+    out = ac.defrag_kv_attend(c.arena.cuda(), c.pages.repeat(B, 1).cuda(), ints([n] * B), q.repeat(B, 1, 1).cuda(), heads, codes,
+                              starts=ints([count * b for b in range(B + 1)]), max_new=count, lse=lse)
+    assert torch.equal(out.unflatten(0, (B, count)), out[:count].expand(B, -1, -1, -1))
+    check_far_apart(c, out[:count], lse[:count], q, group, n)
