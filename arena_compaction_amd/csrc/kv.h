@@ -25,6 +25,15 @@ constexpr int kKvExpMin = -64;    // least exponent of a scale
 constexpr uint32_t kKvMaxDim = 256;
 constexpr uint32_t kKvPromptRows = 128;  // query rows of a workgroup over a prompt
 
+// An axis of a grid holds fewer than 2^32 lanes, 2^22 workgroups of 1024.
+// What may need more is numbered through x, row by row of y (block_number in
+// kv_device.h); the last row is filled up with workgroups that leave at once.
+constexpr uint64_t kGridRow = 1u << 21;
+constexpr uint64_t kMaxBlocks = 0x7FFFFFFFu;
+inline dim3 grid_of(uint64_t blocks) {
+    return blocks <= kGridRow ? dim3((uint32_t)blocks) : dim3((uint32_t)kGridRow, (uint32_t)((blocks + kGridRow - 1) / kGridRow));
+}
+
 // Waves of a workgroup that makes weights from the keys again.
 inline __host__ __device__ constexpr uint32_t kv_weigh_waves(uint32_t dim) { return dim <= 64 ? 16 : 8; }
 
@@ -116,6 +125,16 @@ struct KvAttendPlan {
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
                             uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored);
+
+// Workgroups of the launches that follow from the plan.
+inline uint64_t kv_prompt_blocks(uint64_t splits, uint64_t row_blocks, uint64_t heads, uint64_t batch) {
+    return splits * row_blocks * heads * batch;
+}
+inline uint64_t kv_weigh_blocks(uint64_t pages, uint64_t pieces, uint64_t heads, uint64_t batch) {
+    return pages * pieces * heads * batch;
+}
+constexpr uint32_t kKeptTokens = 512;  // of a workgroup that adds up kept scores
+inline uint64_t kv_kept_blocks(uint64_t max_len, uint64_t heads) { return (max_len + kKeptTokens - 1) / kKeptTokens * heads; }
 
 // codes: 0 e4m3, 1 int8; dtype: 0 bfloat16, 1 float16
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);

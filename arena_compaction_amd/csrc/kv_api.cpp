@@ -7,10 +7,10 @@ using namespace ac;
 
 namespace {
 
-// Tokens and places of a call: a grid's first axis holds fewer than 2^32
-// lanes, 2^24 workgroups of 256, and each covers a page.
-constexpr uint64_t kMaxTokens = 1u << 29;
-constexpr uint64_t kMaxGrid = (1u << 24) - 1;
+constexpr uint64_t kMaxTokens = 1u << 29;  // tokens of a call, places of a table's row
+constexpr uint64_t kMaxGrid = (1u << 24) - 1;  // workgroups of 256 along one axis
+constexpr uint64_t kMaxHeadRows = 0x7FFFFC00u;  // query rows of a (sequence, head): the kernels hold them in an int
+constexpr uint64_t kMaxRows = 1ull << 36;       // query rows of a call: sizes in bytes stay below 2^64
 constexpr uint64_t kMaxEvict = 1u << 25;  // tokens of an evicted sequence
 constexpr uint64_t kLeastWs = 1;  // none is needed: 0 means "refused"
 
@@ -48,7 +48,15 @@ int check_new(const defrag_kv_cache *c, const int32_t *starts, uint64_t tokens, 
     return DEFRAG_OK;
 }
 
-int check_attend(const defrag_kv_attend_args *a) {
+KvAttendPlan plan_of(const defrag_kv_attend_args *a) {
+    return kv_attend_plan(a->cache->batch, a->cache->heads, a->group, a->cache->dim, a->tokens,
+                          a->max_new, a->max_len, a->weight_dev != nullptr);
+}
+
+// The plan of a call, and whether its launches fit their grids.  (Rows are
+// joined by a workgroup each at the most, where the cache is cut: fewer than
+// 2^21 of them, as kv_attend_plan cuts few rows or few workgroups.)
+int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
     if (!a) return DEFRAG_EINVAL;
     int rc = check_cache(a->cache);
     if (rc) return rc;
@@ -58,18 +66,25 @@ int check_attend(const defrag_kv_attend_args *a) {
     if (!dtype_ok(a->dtype) || a->group < 1 || a->group > 256 ||
         (uint64_t)c->heads * a->group > 65535 || a->max_len > c->page_stride * kKvPage)
         return DEFRAG_EINVAL;
+    if ((uint64_t)a->max_new * a->group > kMaxHeadRows || a->tokens * c->heads * a->group > kMaxRows)
+        return DEFRAG_EINVAL;
     if (!(a->scale - a->scale == 0.0f)) return DEFRAG_EINVAL;  // not finite
     if (!aligned(a->q_dev, 2) || !aligned(a->out_dev, 16) || !aligned(a->lse_dev, 4) ||
         !aligned(a->weight_dev, 4))
         return DEFRAG_EINVAL;
     if (a->tokens && (!a->q_dev || !a->out_dev)) return DEFRAG_EINVAL;
     if (a->weight_dev && a->weight_stride < a->max_len) return DEFRAG_EINVAL;
+    *p = KvAttendPlan{};
+    if (!a->tokens) return DEFRAG_OK;
+    *p = plan_of(a);
+    if (p->rows == kKvPromptRows && kv_prompt_blocks(p->splits, p->row_blocks, c->heads, c->batch) > kMaxBlocks)
+        return DEFRAG_EINVAL;
+    const uint64_t pages = (a->max_len + (uint64_t)kKvPage - 1) / kKvPage;
+    if (a->weight_dev && !p->score_bytes && kv_weigh_blocks(pages, p->weigh_pieces, c->heads, c->batch) > kMaxBlocks)
+        return DEFRAG_EINVAL;
+    if (p->score_bytes && kv_kept_blocks(a->max_len, c->heads) + (uint64_t)a->max_new * c->heads * a->group > kMaxGrid)
+        return DEFRAG_EINVAL;
     return DEFRAG_OK;
-}
-
-KvAttendPlan plan_of(const defrag_kv_attend_args *a) {
-    return kv_attend_plan(a->cache->batch, a->cache->heads, a->group, a->cache->dim, a->tokens,
-                          a->max_new, a->max_len, a->weight_dev != nullptr);
 }
 
 int check_evict(const defrag_kv_evict_args *a) {
@@ -135,29 +150,19 @@ int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
 }
 
 size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *a) {
-    if (check_attend(a)) return 0;
-    const uint64_t need = a->tokens ? plan_of(a).total : 0;
-    return need > kLeastWs ? need : kLeastWs;
+    KvAttendPlan p;
+    if (check_attend(a, &p)) return 0;
+    return p.total > kLeastWs ? p.total : kLeastWs;
 }
 
 int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_bytes,
                      hipStream_t stream) {
-    int rc = check_attend(a);
+    KvAttendPlan p;
+    int rc = check_attend(a, &p);
     if (rc) return rc;
     const defrag_kv_cache *c = a->cache;
-    const KvAttendPlan p = plan_of(a);
-    if (a->tokens) {
-        if ((uint64_t)p.splits * p.row_blocks * c->batch * c->heads > kMaxGrid ||
-            (uint64_t)a->max_new * c->heads * a->group +
-                    (a->weight_dev ? (a->max_len / 256 + 1ull) * c->heads : 0) > kMaxGrid)
-            return DEFRAG_EINVAL;
-        // the weights' workgroups have up to 1024 lanes
-        if (a->weight_dev && !p.score_bytes &&
-            (a->max_len / kKvPage + 1ull) * c->batch * c->heads > kMaxGrid / 4)
-            return DEFRAG_EINVAL;
-        rc = check_ws(ws_dev, ws_bytes, p.total);
-        if (rc) return rc;
-    }
+    rc = check_ws(ws_dev, ws_bytes, p.total);
+    if (rc) return rc;
     rc = clear_count(c, stream);
     if (rc || !a->tokens) return rc;
     uint8_t *ws = static_cast<uint8_t *>(ws_dev);

@@ -106,6 +106,9 @@ __device__ inline uint32_t requant4(uint32_t w, float f) {
                             code_value<CODES, 2>(w) * f, code_value<CODES, 3>(w) * f);
 }
 
+// Number of a workgroup of grid_of's grids.
+__device__ inline uint32_t block_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 constexpr uint64_t kNoPage = ~0ull;
 
 // A page's offset, or kNoPage where the table's entry is none: outside the

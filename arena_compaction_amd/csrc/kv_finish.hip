@@ -31,7 +31,7 @@ __device__ inline const float *part_sums(const KvAttend &a, uint64_t all, uint64
     return a.part + (uint64_t)a.splits * all * a.c.dim + row * 2;
 }
 
-constexpr uint32_t kKeptTokens = 2 * kThreads;  // of a workgroup that adds up kept scores
+static_assert(kKeptTokens == 2 * kThreads, "two tokens a lane");
 constexpr uint32_t kFewParts = 16;  // a wave a row, above them a workgroup a row
 
 // Row and head `unit` of sequence b from its parts k = first, first + STEP...
@@ -209,14 +209,15 @@ __global__ __launch_bounds__(kv_weigh_waves(D) * 64) void k_kv_weigh(KvAttend a)
     __shared__ u32x4 sm_q[kN][16 * kPitch];
     // the last rows first: every page's rows end there, so that workgroups
     // that start together read the same queries
-    const uint32_t units = a.c.heads * a.c.batch, unit = blockIdx.x % units;
-    const uint32_t h = unit % a.c.heads, b = unit / a.c.heads;
-    const uint32_t piece = a.weigh_pieces - 1 - blockIdx.x / (units * a.score_pages);
+    const uint32_t units = a.c.heads * a.c.batch, block = block_number();
+    if (block >= units * a.score_pages * a.weigh_pieces) return;
+    const uint32_t unit = block % units, h = unit % a.c.heads, b = unit / a.c.heads;
+    const uint32_t piece = a.weigh_pieces - 1 - block / (units * a.score_pages);
     const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
     const int n = lane % 16, g = lane / 16, G = (int)a.group;
     bool bad;
     const Seq s = sequence(a, b, &bad);
-    const int p = (int)(blockIdx.x / units % a.score_pages), base = p * kKvPage;
+    const int p = (int)(block / units % a.score_pages), base = p * kKvPage;
     if (base >= s.len || s.count == 0) return;
     const int rows = s.count * (int)a.group;
     int first, tiles;
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_add(KvAttend a) {
 
 template <int D, int CODES>
 void weigh_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid(a.c.heads * a.c.batch * a.score_pages * a.weigh_pieces), block(kv_weigh_waves(D) * 64);
+    const dim3 grid = grid_of(kv_weigh_blocks(a.score_pages, a.weigh_pieces, a.c.heads, a.c.batch)), block(kv_weigh_waves(D) * 64);
     if (dtype == kBf16)
         hipLaunchKernelGGL((k_kv_weigh<D, CODES, kBf16>), grid, block, 0, s, a);
     else
@@ -379,7 +380,7 @@ void weigh_codes(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 hipError_t launch_kv_finish(const KvAttend &a, int dtype, hipStream_t s) {
     const uint32_t units = a.max_new * a.c.heads * a.group;
     const uint32_t join = a.splits == 1 ? 0 : a.splits <= kFewParts ? (units + kWaves - 1) / kWaves : units;
-    const uint32_t weigh = a.scores ? (a.max_len + kKeptTokens - 1) / kKeptTokens * a.c.heads : 0;
+    const uint32_t weigh = a.scores ? (uint32_t)kv_kept_blocks(a.max_len, a.c.heads) : 0;
     if (join + weigh == 0) return hipSuccess;
     const dim3 grid(join + weigh, a.c.batch);
     if (dtype == kBf16)

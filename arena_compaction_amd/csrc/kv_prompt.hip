@@ -41,7 +41,9 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
     constexpr int kChunks = (D + 63) / 64, kKeyJobs = (4 * kChunks + kN - 1) / kN, kValueJobs = (kTiles + kN - 1) / kN;
     __shared__ u32x4 sm_k[2][4 * kSteps * 64], sm_v[2][kTiles * 2 * 64];
     __shared__ int sm_nan;
-    const uint32_t units = a.c.batch * a.c.heads, unit = blockIdx.x % units, piece = blockIdx.x / units;
+    const uint32_t units = a.c.batch * a.c.heads, block = block_number();
+    if (block >= units * a.row_blocks * a.splits) return;
+    const uint32_t unit = block % units, piece = block / units;
     const uint32_t b = unit / a.c.heads, h = unit % a.c.heads;
     const int split = piece % a.splits, rb = (int)(a.row_blocks - 1 - piece / a.splits);
     const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
@@ -371,7 +373,7 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
 
 template <int D, int CODES>
 void prompt_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid(a.splits * a.row_blocks * a.c.heads * a.c.batch);
+    const dim3 grid = grid_of(kv_prompt_blocks(a.splits, a.row_blocks, a.c.heads, a.c.batch));
     if (dtype == kBf16)
         hipLaunchKernelGGL((k_kv_prompt<D, CODES, kBf16>), grid, dim3(kPromptWaves<D> * 64), 0, s, a);
     else

@@ -563,7 +563,12 @@ int defrag_kv_append(const defrag_kv_append_args *args, hipStream_t stream);
  * logarithm of the softmax's sum; a row that sees nothing gives 0 and
  * -infinity.  weight_dev (batch x heads x weight_stride), where given, is
  * increased by the weight that each cached token receives from all rows of
- * its head's group.  Sums are 32-bit and run in a fixed order. */
+ * its head's group.  Sums are 32-bit and run in a fixed order.
+ * Limits: heads * group <= 65535, max_new * group < 2^31 - 1023, tokens *
+ * heads * group <= 2^36; and of workgroups, batch * heads * ceil(max_new *
+ * group / 128) < 2^31, with weight_dev also batch * heads * ceil(max_len / 64)
+ * < 2^31, or where max_new * group is at most 16, (ceil(max_len / 512) +
+ * max_new * group) * heads < 2^24. */
 typedef struct defrag_kv_attend_args {
     const defrag_kv_cache *cache;
     const void *q_dev;               /* tokens x heads * group x dim         */

@@ -189,3 +189,67 @@ def test_attend_value_scales_far_apart_few_rows(ac, heads, group, dim, codes, dt
                               starts=ints([count * b for b in range(B + 1)]), max_new=count, lse=lse)
     assert torch.equal(out.unflatten(0, (B, count)), out[:count].expand(B, -1, -1, -1))
     check_far_apart(c, out[:count], lse[:count], q, group, n)
+
+
+# ---- attend: grids past one axis --------------------------------------------
+
+def few_seen(ac, c, n, q, group, counts, places, weight, max_new):
+    """Attention of sequences that all hold the same n tokens and bring `counts` new ones, most of which see
+    nothing; checks the rows that see something, and that the others are empty."""
+    B, heads, dim = len(counts), c.H, c.D
+    w = torch.full((B, heads, places), 0.5, device="cuda") if weight else None
+    lse = torch.empty(q.shape[:2], device="cuda")
+    starts = [0]
+    for t in counts:
+        starts.append(starts[-1] + t)
+    stride = -(-places // PAGE) if weight else c.pages.shape[1]
+    pages = torch.full((B, stride), -1, dtype=torch.int64)
+    pages[:, : c.pages.shape[1]] = c.pages
+    out = ac.defrag_kv_attend(c.arena.cuda(), pages.cuda(), ints([n] * B), q, heads, c.codes, starts=ints(starts),
+                              max_new=max_new, max_len=places if weight else None, lse=lse, weight=w)
+    for b in sorted({0, B // 2, B - 1}):
+        see = min(n, counts[b])
+        rows = slice(starts[b + 1] - see, starts[b + 1])
+        want, bound, lse_, lbound, add, wbound = attend(c, [n], q[rows].cpu(), group, [see], dim ** -0.5)
+        got = out[rows].double().cpu()
+        assert ((got - want).abs() <= bound * (1 + HALF[q.dtype]) + want.abs() * HALF[q.dtype] + 2.0 ** -25).all(), b
+        assert ((lse[rows].double().cpu() - lse_).abs() <= lbound + 2.0 ** -22).all(), b
+        if weight:
+            got = w[b].double().cpu()
+            assert ((got[:, :n] - 0.5 - add[0]).abs() <= wbound[0] + (add[0] + 0.5) * 2.0 ** -23).all(), b
+            assert (got[:, n:] == 0.5).all(), b
+        blind = slice(starts[b], starts[b + 1] - see)
+        assert not out[blind].any() and (lse[blind] == -math.inf).all(), b
+
+
+@pytest.mark.parametrize("weight", [False, True])
+def test_attend_long_prompt_of_many_heads(ac, weight):
+    """131,072 tokens of 128 query heads: 2^24 rows of a call, 2^21 of a head."""
+    c = Cache([2], 8, 64, INT8)
+    c.fill_random([100], 91)
+    gen = torch.Generator(device="cuda").manual_seed(92)
+    q = torch.randn(131072, 128, 64, device="cuda", generator=gen, dtype=torch.bfloat16)
+    few_seen(ac, c, 100, q, 16, [131072], 128, weight, 131072)
+
+
+@pytest.mark.parametrize("dim,codes", [(64, E4M3), (192, INT8)])
+def test_attend_prompts_past_one_grid_axis(ac, dim, codes):
+    """64 prompts, max_new left at all their tokens: 2,098,176 workgroups, more than one row of the grid."""
+    c = Cache([2], 8, dim, codes, fill=0x7F)
+    c.fill_random([70], 93)
+    counts = [4097 + (b % 2) for b in range(64)]
+    gen = torch.Generator(device="cuda").manual_seed(94)
+    q = torch.randn(sum(counts), 16, dim, device="cuda", generator=gen, dtype=torch.float16)
+    assert -(-sum(counts) * 2 // 128) * 8 * 64 > 1 << 21
+    few_seen(ac, c, 70, q, 2, counts, 128, False, None)
+
+
+@pytest.mark.parametrize("dim,codes", [(64, E4M3), (128, INT8)])
+def test_attend_weights_past_one_grid_axis(ac, dim, codes):
+    """64 x 32 x 1026 workgroups over the pages of a table for 65,664 tokens."""
+    c = Cache([2], 32, dim, codes, fill=0x7F)
+    c.fill_random([70], 95)
+    gen = torch.Generator(device="cuda").manual_seed(96)
+    counts = [8 - b % 3 for b in range(64)]
+    q = torch.randn(sum(counts), 128, dim, device="cuda", generator=gen, dtype=torch.bfloat16)
+    few_seen(ac, c, 70, q, 4, counts, 1026 * PAGE, True, 8)

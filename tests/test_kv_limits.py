@@ -1,0 +1,56 @@
+"""Sizes of the key/value cache's calls at their limits: what the size query
+accepts the call accepts, and nothing is launched here (the workspace is
+missing, or the arguments are refused)."""
+import ctypes
+
+import pytest
+
+import arena_compaction_amd as ac
+from test_kv import _args
+
+
+def attend_says(**change):
+    """(bytes the query asks for, what the call says without a workspace)."""
+    a = _args(ac.defrag_kv_attend_args, **{"weight_dev": 0x1000, "weight_stride": 1 << 30, **change})
+    need = ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a))
+    assert need != 1, "would be launched"
+    return need, ac.lib.defrag_kv_attend(ctypes.byref(a), None, 0, None)
+
+
+ACCEPTED = [
+    # a prompt of 131,072 tokens, 128 query heads
+    dict(batch=1, heads=8, group=16, dim=128, tokens=131072, max_new=131072, starts_dev=0x1000, page_stride=2048, max_len=131072),
+    # 64 prompts of 4096 tokens, max_new as the binding's default has it
+    dict(batch=64, heads=8, group=8, dim=64, tokens=262144, max_new=262144, starts_dev=0x1000, page_stride=64, max_len=4096),
+    # drafts over a table for 131,072 tokens
+    dict(batch=64, heads=32, group=4, dim=128, tokens=512, max_new=8, starts_dev=0x1000, page_stride=2048, max_len=131072),
+    # more than 2^23 workgroups of 512 lanes
+    dict(batch=64, heads=64, group=8, dim=256, tokens=262145, max_new=262145, starts_dev=0x1000, page_stride=64, max_len=4096)]
+
+
+@pytest.mark.parametrize("sizes", ACCEPTED)
+def test_attend_takes_ordinary_sizes(sizes):
+    need, said = attend_says(**sizes)
+    assert need > 1 and said == ac.DEFRAG_EWORKSPACE
+
+
+LIMITS = [  # the largest that is taken, and the next
+    # query rows of a head
+    (dict(batch=1, heads=1, group=256, tokens=0x7FFFFC, max_new=0x7FFFFC, starts_dev=0x1000), dict(tokens=0x7FFFFD, max_new=0x7FFFFD)),
+    # query rows of a call
+    (dict(batch=64, heads=128, group=1, tokens=1 << 29, max_new=1, starts_dev=0x1000), dict(heads=129)),
+    # workgroups over the rows
+    (dict(batch=65535, heads=255, group=1, tokens=65535, max_new=16384, starts_dev=0x1000), dict(max_new=16385)),
+    # workgroups over the pages
+    (dict(batch=65535, heads=32, group=1, tokens=65535, max_new=33, starts_dev=0x1000, page_stride=2048, max_len=65536), dict(max_len=65537)),
+    # kept scores
+    (dict(batch=4, heads=65535, group=1, tokens=4, max_new=1, page_stride=2048, max_len=130560), dict(max_len=130561)),
+    # heads over all
+    (dict(batch=4, heads=13107, group=5, tokens=4, max_new=1), dict(heads=13108))]
+
+
+@pytest.mark.parametrize("sizes,more", LIMITS)
+def test_attend_limits(sizes, more):
+    need, said = attend_says(**sizes)
+    assert need > 1 and said == ac.DEFRAG_EWORKSPACE
+    assert attend_says(**{**sizes, **more}) == (0, ac.DEFRAG_EINVAL)
