@@ -25,7 +25,8 @@ int check_cache(const defrag_kv_cache *c) {
     if (c->batch > 65535 || c->heads < 1 || c->heads > 65535 || !dim_ok(c->dim)) return DEFRAG_EINVAL;
     if (c->codes != DEFRAG_KV_E4M3 && c->codes != DEFRAG_KV_INT8) return DEFRAG_EINVAL;
     if (c->page_stride * kKvPage > kMaxTokens || c->page_stride > kMaxTokens) return DEFRAG_EINVAL;
-    if (!aligned(c->arena_dev, 32) || !aligned(c->pages_dev, 8) || !aligned(c->lens_dev, 4))
+    if (!aligned(c->arena_dev, 32) || !aligned(c->pages_dev, 8) || !aligned(c->lens_dev, 4) ||
+        !aligned(c->n_invalid_dev, 8))
         return DEFRAG_EINVAL;
     if (c->batch && (!c->lens_dev || (c->page_stride && !c->pages_dev))) return DEFRAG_EINVAL;
     if (c->arena_bytes && !c->arena_dev) return DEFRAG_EINVAL;
@@ -110,7 +111,6 @@ int check_evict(const defrag_kv_evict_args *a) {
 
 int clear_count(const defrag_kv_cache *c, hipStream_t s) {
     if (!c->n_invalid_dev) return DEFRAG_OK;
-    if (!aligned(c->n_invalid_dev, 8)) return DEFRAG_EINVAL;
     return launch_kv_zero(c->n_invalid_dev, s) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
 }
 

@@ -54,3 +54,10 @@ def test_attend_limits(sizes, more):
     need, said = attend_says(**sizes)
     assert need > 1 and said == ac.DEFRAG_EWORKSPACE
     assert attend_says(**{**sizes, **more}) == (0, ac.DEFRAG_EINVAL)
+
+
+@pytest.mark.parametrize("cls,query", [(ac.defrag_kv_attend_args, ac.lib.defrag_kv_attend_workspace_bytes),
+                                       (ac.defrag_kv_evict_args, ac.lib.defrag_kv_evict_workspace_bytes)])
+def test_queries_refuse_the_counter_that_the_calls_refuse(cls, query):
+    assert query(ctypes.byref(_args(cls, n_invalid_dev=0x1008))) > 0
+    assert query(ctypes.byref(_args(cls, n_invalid_dev=0x1004))) == 0
