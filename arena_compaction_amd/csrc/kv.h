@@ -136,6 +136,13 @@ inline uint64_t kv_weigh_blocks(uint64_t pages, uint64_t pieces, uint64_t heads,
 constexpr uint32_t kKeptTokens = 512;  // of a workgroup that adds up kept scores
 inline uint64_t kv_kept_blocks(uint64_t max_len, uint64_t heads) { return (max_len + kKeptTokens - 1) / kKeptTokens * heads; }
 
+// Pages of a sequence that max_new tokens can touch, wherever in a page they
+// begin, of those that a table's row has (at least 1: it counts what is refused).
+inline uint32_t kv_append_pages(uint32_t max_new, uint64_t stride) {
+    const uint64_t n = ((uint64_t)max_new + kKvPage - 2) / kKvPage + 1;
+    return (uint32_t)(n < stride ? n : stride > 1 ? stride : 1);
+}
+
 // codes: 0 e4m3, 1 int8; dtype: 0 bfloat16, 1 float16
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s);

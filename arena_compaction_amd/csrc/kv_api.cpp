@@ -140,6 +140,7 @@ int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
         !aligned(a->weight_dev, 4) || !aligned(a->pos_dev, 4) || !aligned(a->first_pos_dev, 4))
         return DEFRAG_EINVAL;
     if (a->tokens && (!a->k_dev || !a->v_dev)) return DEFRAG_EINVAL;
+    if ((uint64_t)kv_append_pages(a->max_new, c->page_stride) * 2 * c->dim > 0xFFFFFFFFu) return DEFRAG_EINVAL;
     rc = clear_count(c, stream);
     if (rc || !a->tokens) return rc;
     const KvAppend k{cache_of(c),

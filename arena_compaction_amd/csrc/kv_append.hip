@@ -265,8 +265,7 @@ hipError_t launch_kv_zero(uint64_t *p, hipStream_t s) {
 }
 
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s) {
-    // pages that max_new tokens can touch, wherever in a page they begin
-    const dim3 grid((a.max_new + kKvPage - 2) / kKvPage + 1, a.c.heads, a.c.batch);
+    const dim3 grid(kv_append_pages(a.max_new, a.c.stride), a.c.heads, a.c.batch);
     switch (a.c.dim) {
         case 64: append_codes<64>(a, codes, dtype, grid, s); break;
         case 96: append_codes<96>(a, codes, dtype, grid, s); break;

@@ -538,7 +538,8 @@ size_t defrag_kv_page_bytes(uint32_t heads, uint32_t dim);
  * lies outside becomes the largest.  A NaN stays one in E4M3 and becomes 0 in
  * INT8.  Where given, weight_dev and pos_dev (batch x heads x weight_stride)
  * get 0 and the token's position first_pos_dev[b] + its number (first_pos_dev
- * NULL: its place) at the token's place, where that is below weight_stride. */
+ * NULL: its place) at the token's place, where that is below weight_stride.
+ * With 256 dimensions and tokens for it all, page_stride is below 2^23. */
 typedef struct defrag_kv_append_args {
     const defrag_kv_cache *cache;
     const void *k_dev, *v_dev;       /* tokens x heads x dim, 16-bit         */

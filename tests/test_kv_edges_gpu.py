@@ -253,3 +253,19 @@ def test_attend_weights_past_one_grid_axis(ac, dim, codes):
     counts = [8 - b % 3 for b in range(64)]
     q = torch.randn(sum(counts), 128, dim, device="cuda", generator=gen, dtype=torch.bfloat16)
     few_seen(ac, c, 70, q, 4, counts, 1026 * PAGE, True, 8)
+
+
+# ---- append -------------------------------------------------------------------
+
+@pytest.mark.parametrize("stride", [0, 1, 2])
+def test_append_to_tables_of_few_pages(ac, stride):
+    """More new tokens than a row of the table holds: refused and counted, the others written."""
+    c = Cache([stride], 2, 64, INT8, stride=max(stride, 1))
+    pages = c.pages[:, :stride].repeat(2, 1)
+    x = queries(64 * stride + 200, 2, 64, torch.float16, 97)
+    arena, n = c.arena.cuda(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    count = 64 * stride
+    ac.defrag_kv_append(arena, pages.cuda(), ints([0, 0]), x.cuda(), x.cuda(), INT8, starts=ints([0, count, count + 200]), n_invalid=n)
+    assert int(n) == 1
+    c.append(0, 0, x[:count], x[:count])
+    same_pages(c, arena)

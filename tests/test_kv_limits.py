@@ -61,3 +61,9 @@ def test_attend_limits(sizes, more):
 def test_queries_refuse_the_counter_that_the_calls_refuse(cls, query):
     assert query(ctypes.byref(_args(cls, n_invalid_dev=0x1008))) > 0
     assert query(ctypes.byref(_args(cls, n_invalid_dev=0x1004))) == 0
+
+
+def test_append_refuses_a_grid_of_two_to_the_32_lanes():
+    """2^23 pages of 512 lanes each; one page fewer, or tokens for one page fewer, would fit."""
+    a = _args(ac.defrag_kv_append_args, dim=256, page_stride=1 << 23, tokens=1 << 29, max_new=1 << 29, starts_dev=0x1000)
+    assert ac.lib.defrag_kv_append(ctypes.byref(a), None) == ac.DEFRAG_EINVAL
