@@ -704,7 +704,8 @@ def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, po
     whose position is below sink or at least next_pos - recent, then those of
     largest weight; they end in the first budget / 64 pages.  weight (float32)
     and pos (int32): [batch, heads, places]; weight_out, pos_out and lens_out
-    (int32 [batch]) receive the result.  next_pos: int32 [batch] (default:
+    (int32 [batch]) receive the result; weight_out may be weight and pos_out
+    pos, lens_out has to be memory of its own.  next_pos: int32 [batch] (default:
     lens); max_len: no length exceeds it (default: what table and planes
     hold)."""
     if not isinstance(weight, torch.Tensor) or weight.dim() != 3:

@@ -16,6 +16,34 @@ constexpr uint64_t kLeastWs = 1;  // none is needed: 0 means "refused"
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// Bytes of memory; of no bytes or no address they overlap nothing.
+struct Span {
+    const void *p;
+    unsigned __int128 bytes;
+};
+
+// The used part of rows x (stride of them apart) numbers of 4 bytes.
+Span plane(const void *p, uint64_t rows, uint64_t stride, uint64_t used) {
+    return Span{p, rows && used ? ((unsigned __int128)(rows - 1) * stride + used) * 4 : 0};
+}
+
+bool overlap(const Span &a, const Span &b) {
+    const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether outputs overlap one another or an input.
+template <size_t OUT, size_t IN>
+bool any_overlap(const Span (&out)[OUT], const Span (&in)[IN]) {
+    for (size_t i = 0; i < OUT; ++i) {
+        for (size_t j = i + 1; j < OUT; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (const Span &x : in)
+            if (overlap(out[i], x)) return true;
+    }
+    return false;
+}
+
 bool dim_ok(uint32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
 // The parts of a cache that every call needs; lens_dev and pages_dev may be
@@ -106,6 +134,17 @@ int check_evict(const defrag_kv_evict_args *a) {
     if (c->batch && (!a->weight_dev || !a->pos_dev || !a->next_pos_dev || !a->weight_out_dev ||
                      !a->pos_out_dev || !a->lens_out_dev))
         return DEFRAG_EINVAL;
+    // (weights and positions may be replaced where they are: a place below the
+    // budget is written by one lane, from itself or from behind the budget)
+    const uint64_t rows = (uint64_t)c->batch * c->heads;
+    const bool same = a->weight_out_stride == a->weight_stride;
+    const Span out[] = {plane(a->lens_out_dev, 1, 0, c->batch), plane(a->weight_out_dev, rows, a->weight_out_stride, kept),
+                        plane(a->pos_out_dev, rows, a->weight_out_stride, kept)};
+    const Span in[] = {plane(a->weight_out_dev == a->weight_dev && same ? nullptr : a->weight_dev, rows, a->weight_stride, a->max_len),
+                       plane(a->pos_out_dev == a->pos_dev && same ? nullptr : a->pos_dev, rows, a->weight_stride, a->max_len),
+                       plane(c->lens_dev, 1, 0, c->batch), plane(a->next_pos_dev, 1, 0, c->batch),
+                       plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
+    if (any_overlap(out, in)) return DEFRAG_EINVAL;
     return DEFRAG_OK;
 }
 

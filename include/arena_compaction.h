@@ -502,9 +502,9 @@ int defrag_monitor(const defrag_stats_t *stats, const defrag_monitor_cfg *cfg,
  * All three calls run on the caller's stream and return at once; they
  * allocate nothing, create no stream and may be captured into a graph.  A
  * page that append or evict writes belongs to one sequence; pages that are
- * only read may be shared.  Outputs may not overlap inputs.  Every argument
- * is checked on the host before the first launch (DEFRAG_EINVAL,
- * DEFRAG_EWORKSPACE).
+ * only read may be shared.  Outputs may not overlap inputs or one another
+ * (but see evict's weights and positions).  Every argument is checked on the
+ * host before the first launch (DEFRAG_EINVAL, DEFRAG_EWORKSPACE).
  */
 #define DEFRAG_KV_PAGE_TOKENS 64
 #define DEFRAG_KV_E4M3 0
@@ -602,7 +602,9 @@ int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_
  * budget / 64 whose tokens changed gets a new scale and new codes; the pages
  * behind them are free afterwards.  weight_out_dev, pos_out_dev and
  * lens_out_dev describe the result (places behind lens_out are not written);
- * a sequence of at most budget tokens is copied there as it is. */
+ * a sequence of at most budget tokens is copied there as it is.  weight_out_dev
+ * may be weight_dev, and pos_out_dev pos_dev, where the strides are the same;
+ * lens_out_dev has to be memory of its own. */
 typedef struct defrag_kv_evict_args {
     const defrag_kv_cache *cache;
     uint32_t budget;                 /* a multiple of 64, not 0, <= 2^25     */

@@ -269,3 +269,33 @@ def test_append_to_tables_of_few_pages(ac, stride):
     assert int(n) == 1
     c.append(0, 0, x[:count], x[:count])
     same_pages(c, arena)
+
+
+# ---- evict: weights and positions in place ------------------------------------
+
+@pytest.mark.parametrize("n", [300, 17000])
+def test_evict_in_place(ac, n):
+    """Weights and positions replaced where they are equal those written elsewhere; lengths may not be."""
+    lens = [n, 100, 128, n - 77]
+    gen = torch.Generator().manual_seed(98)
+    c = Cache([-(-x // PAGE) for x in lens], 2, 64, INT8)
+    for off in c.pages[c.pages >= 0].tolist():
+        for h in range(2):
+            k, v, sc = c.head(off, h)
+            for x in (k, v):
+                x.copy_(torch.randint(-127, 128, x.shape, generator=gen).to(torch.int8))
+            sc.copy_(2.0 ** torch.randint(-3, 3, (2,), generator=gen))
+    w = torch.rand(4, 2, n + 3, generator=gen).cuda()
+    pos = torch.rand(4, 2, n + 3, generator=gen).argsort(-1).int().cuda()
+    kw = dict(sink=4, recent=32)
+    results = []
+    for in_place in (False, True):
+        arena, wi, pi = c.arena.cuda(), w.clone(), pos.clone()
+        wo, po = (wi, pi) if in_place else (torch.zeros_like(wi), torch.zeros_like(pi))
+        lo, held = ints([-1] * 4), ints(lens)
+        ac.defrag_kv_evict(arena, c.pages.cuda(), held, 128, wi, pi, wo, po, lo, 64, INT8, **kw)
+        results.append([arena, lo, wo[:, :, :100], po[:, :, :100], wo[0, :, :128], po[0, :, :128], wo[3, :, :128], po[3, :, :128]])
+        with pytest.raises(ac.DefragError):
+            ac.defrag_kv_evict(arena, c.pages.cuda(), held, 128, wi, pi, wo, po, held, 64, INT8, **kw)
+    assert results[0][1].tolist() == [128, 100, 128, 128]
+    assert all(torch.equal(a, b) for a, b in zip(*results))

@@ -67,3 +67,24 @@ def test_append_refuses_a_grid_of_two_to_the_32_lanes():
     """2^23 pages of 512 lanes each; one page fewer, or tokens for one page fewer, would fit."""
     a = _args(ac.defrag_kv_append_args, dim=256, page_stride=1 << 23, tokens=1 << 29, max_new=1 << 29, starts_dev=0x1000)
     assert ac.lib.defrag_kv_append(ctypes.byref(a), None) == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("change", [
+    dict(lens_out_dev=0x30000), dict(lens_out_dev=0x3000C), dict(lens_out_dev=0x40000),      # lens, next_pos
+    dict(next_pos_dev=0x9000C), dict(lens_out_dev=0x20010), dict(lens_out_dev=0x50000),      # pages, weight
+    dict(weight_out_dev=0x50004), dict(weight_out_dev=0x50000), dict(pos_out_dev=0x67FFC),   # shifted, another stride
+    dict(pos_out_dev=0x70800), dict(weight_out_dev=0x60000, weight_out_stride=1024),
+    dict(weight_out_dev=0x50000, weight_out_stride=1024, pos_out_dev=0x50000)])
+def test_evict_refuses_outputs_over_inputs(change):
+    a = _args(ac.defrag_kv_evict_args, **change)
+    assert ac.lib.defrag_kv_evict_workspace_bytes(ctypes.byref(a)) == 0
+    assert ac.lib.defrag_kv_evict(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("change", [
+    dict(weight_out_dev=0x50000, weight_out_stride=1024), dict(pos_out_dev=0x60000, weight_out_stride=1024),
+    dict(lens_out_dev=0x30010), dict(weight_out_dev=0x58000), dict(next_pos_dev=0x30000)])
+def test_evict_takes_planes_in_place_and_neighbours(change):
+    a = _args(ac.defrag_kv_evict_args, **change)
+    assert ac.lib.defrag_kv_evict_workspace_bytes(ctypes.byref(a)) > 1
+    assert ac.lib.defrag_kv_evict(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EWORKSPACE
