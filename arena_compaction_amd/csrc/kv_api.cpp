@@ -32,6 +32,14 @@ bool overlap(const Span &a, const Span &b) {
     return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
 
+// From the first to the last of tokens x heads x dim numbers of 2 bytes.
+Span strided(const void *p, uint64_t tokens, int64_t row, uint64_t heads, int64_t head, uint32_t dim) {
+    if (!p || !tokens || !heads) return Span{nullptr, 0};
+    const __int128 r = (__int128)(tokens - 1) * row, h = (__int128)(heads - 1) * head;
+    const __int128 lo = (r < 0 ? r : 0) + (h < 0 ? h : 0), hi = (r > 0 ? r : 0) + (h > 0 ? h : 0) + dim;
+    return Span{reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(p) + (intptr_t)(lo * 2)), (unsigned __int128)(hi - lo) * 2};
+}
+
 // Whether outputs overlap one another or an input.
 template <size_t OUT, size_t IN>
 bool any_overlap(const Span (&out)[OUT], const Span (&in)[IN]) {
@@ -103,6 +111,13 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
         return DEFRAG_EINVAL;
     if (a->tokens && (!a->q_dev || !a->out_dev)) return DEFRAG_EINVAL;
     if (a->weight_dev && a->weight_stride < a->max_len) return DEFRAG_EINVAL;
+    const uint64_t q_heads = (uint64_t)c->heads * a->group, rows = a->tokens * q_heads;
+    const Span out[] = {plane(a->out_dev, 1, 0, rows * c->dim / 2), plane(a->lse_dev, 1, 0, rows),
+                        plane(a->weight_dev, (uint64_t)c->batch * c->heads, a->weight_stride, a->max_len)};
+    const Span in[] = {strided(a->q_dev, a->tokens, a->q_row, q_heads, a->q_head, c->dim),
+                       plane(a->starts_dev, 1, 0, c->batch + 1ull), plane(c->lens_dev, 1, 0, c->batch),
+                       plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
+    if (any_overlap(out, in)) return DEFRAG_EINVAL;
     *p = KvAttendPlan{};
     if (!a->tokens) return DEFRAG_OK;
     *p = plan_of(a);

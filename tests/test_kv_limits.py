@@ -11,7 +11,8 @@ from test_kv import _args
 
 def attend_says(**change):
     """(bytes the query asks for, what the call says without a workspace)."""
-    a = _args(ac.defrag_kv_attend_args, **{"weight_dev": 0x1000, "weight_stride": 1 << 30, **change})
+    apart = {"q_dev": 1 << 46, "out_dev": 1 << 47, "weight_dev": 1 << 55, "weight_stride": 1 << 30}
+    a = _args(ac.defrag_kv_attend_args, **{**apart, **change})
     need = ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a))
     assert need != 1, "would be launched"
     return need, ac.lib.defrag_kv_attend(ctypes.byref(a), None, 0, None)
@@ -88,3 +89,26 @@ def test_evict_takes_planes_in_place_and_neighbours(change):
     a = _args(ac.defrag_kv_evict_args, **change)
     assert ac.lib.defrag_kv_evict_workspace_bytes(ctypes.byref(a)) > 1
     assert ac.lib.defrag_kv_evict(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EWORKSPACE
+
+
+@pytest.mark.parametrize("change", [
+    dict(out_dev=0x40000), dict(out_dev=0x40FF0), dict(out_dev=0x3F810), dict(out_dev=0x40000, q_row=-512, q_dev=0x40C00),  # q
+    dict(lse_dev=0x40010), dict(lse_dev=0x507F0), dict(lse_dev=0x30004), dict(out_dev=0x30000), dict(out_dev=0x20000),
+    dict(lse_dev=0x10FC), dict(weight_dev=0x50000), dict(weight_dev=0x48000 - 4 * 4 * 2 * 1024 + 16, q_dev=0x48000),
+    dict(starts_dev=0x50010)])
+def test_attend_refuses_outputs_over_inputs(change):
+    """q holds 4 x 8 x 64 numbers from 0x40000 on, out as many from 0x50000, the weights 4 x 2 x 1024 from 0x1000."""
+    sizes = dict(group=4, weight_dev=0x1000, weight_stride=1024, **{k: v for k, v in change.items() if k != "weight_dev"})
+    sizes["weight_dev"] = change.get("weight_dev", 0x1000)
+    a = _args(ac.defrag_kv_attend_args, **sizes)
+    assert ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a)) == 0
+    assert ac.lib.defrag_kv_attend(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("change", [
+    dict(out_dev=0x41000), dict(out_dev=0x3F000), dict(lse_dev=0x51000), dict(lse_dev=0x50000 - 128),
+    dict(out_dev=0x41000, q_row=-512, q_dev=0x40C00), dict(out_dev=0x40400, tokens=1, batch=1, max_new=1)])
+def test_attend_takes_outputs_beside_inputs(change):
+    a = _args(ac.defrag_kv_attend_args, **{**dict(group=4, weight_dev=0x1000, weight_stride=1024), **change})
+    assert ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a)) > 1
+    assert ac.lib.defrag_kv_attend(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EWORKSPACE
