@@ -520,9 +520,17 @@ def defrag_monitor(stats: defrag_stats_t, warning_ratio: float = 0.85,
     return out
 
 
+def _kv_int(x: int, what: str, least: int = 0, most: int = 0xFFFFFFFF) -> int:
+    """x where it fits its field, to which ctypes would cut it (heads, a length
+    or a budget of 2^32 + n would be n); refused as the library refuses sizes."""
+    if not least <= x <= most:
+        raise DefragError(DEFRAG_EINVAL, f"{what} = {x}")
+    return x
+
+
 def defrag_kv_page_bytes(heads: int, dim: int) -> int:
     """Bytes of a cache page (64 tokens of every head), a multiple of 32."""
-    nb = int(lib.defrag_kv_page_bytes(heads, dim))
+    nb = int(lib.defrag_kv_page_bytes(_kv_int(heads, "heads"), _kv_int(dim, "dim")))
     if nb == 0:
         raise DefragError(DEFRAG_EINVAL, "defrag_kv_page_bytes")
     return nb
@@ -555,7 +563,8 @@ def _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid) -> defrag_kv_cac
         raise ValueError("lens: int32 [batch] expected, as many as pages has rows")
     return defrag_kv_cache(_kv_ptr(arena, torch.uint8, 0, dev, "arena"), arena.numel(),
                            _kv_ptr(pages, torch.int64, 0, dev, "pages"), stride,
-                           _kv_ptr(lens, torch.int32, 0, dev, "lens"), batch, heads, dim, kind,
+                           _kv_ptr(lens, torch.int32, 0, dev, "lens"), batch, _kv_int(heads, "heads"),
+                           _kv_int(dim, "dim"), kind,
                            None if n_invalid is None else
                            _kv_ptr(n_invalid, torch.int64, 1, dev, "n_invalid"))
 
@@ -589,7 +598,7 @@ def _kv_new(starts, max_new, tokens: int, batch: int, arena) -> int:
             raise ValueError(f"starts: {tokens} tokens of {batch} sequences need it")
         return min(1, tokens)
     _kv_ptr(starts, torch.int32, batch + 1, arena.get_device(), "starts")
-    return tokens if max_new is None else min(int(max_new), tokens)
+    return _kv_int(tokens if max_new is None else min(int(max_new), tokens), "max_new")
 
 
 def _kv_stream(stream, dev: int) -> int:
@@ -685,8 +694,8 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
         _kv_ptr(lse, torch.float32, tokens * q_heads, dev, "lse")
     cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
     a = defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
-                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
-                              max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
+                              KV_DTYPES[q.dtype], _kv_int(q_heads // heads, "group"), tokens, _opt(starts),
+                              most, _kv_int(max_len, "max_len"), dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
                               _opt(lse), _opt(weight), cap)
     need = lib.defrag_kv_attend_workspace_bytes(a)
     ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_attend")
@@ -726,7 +735,9 @@ def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, po
         next_pos = lens
     if max_len is None:
         max_len = min(pages.shape[1] * KV_PAGE_TOKENS, cap)
-    a = defrag_kv_evict_args(ctypes.pointer(c), budget, max_len, sink, recent,
+    a = defrag_kv_evict_args(ctypes.pointer(c), _kv_int(budget, "budget"), _kv_int(max_len, "max_len"),
+                             _kv_int(sink, "sink", -(1 << 31), 0x7FFFFFFF),
+                             _kv_int(recent, "recent", -(1 << 31), 0x7FFFFFFF),
                              _kv_ptr(next_pos, torch.int32, batch, dev, "next_pos"),
                              weight.data_ptr(), pos.data_ptr(), cap, weight_out.data_ptr(),
                              pos_out.data_ptr(), cap_out,

@@ -299,3 +299,22 @@ def test_evict_in_place(ac, n):
             ac.defrag_kv_evict(arena, c.pages.cuda(), held, 128, wi, pi, wo, po, held, 64, INT8, **kw)
     assert results[0][1].tolist() == [128, 100, 128, 128]
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_numbers_past_their_fields(ac):
+    """What ctypes would cut to 32 bits is refused: max_len 2^32 would make every sequence one that holds nothing."""
+    c = Cache([2], 1, 64, INT8)
+    c.fill_random([100], 99)
+    q = queries(1, 2, 64, torch.float16, 100).cuda()
+    arena, pages, lens = c.arena.cuda(), c.pages.cuda(), ints([100])
+    w, pos = torch.zeros(1, 1, 128, device="cuda"), torch.zeros(1, 1, 128, dtype=torch.int32, device="cuda")
+    wo, po, lo = torch.zeros_like(w), torch.zeros_like(pos), ints([0])
+    for bad in (1 << 32, -1):
+        with pytest.raises(ac.DefragError, match="max_len = "):
+            ac.defrag_kv_attend(arena, pages, lens, q, 1, INT8, max_len=bad)
+    with pytest.raises(ac.DefragError, match="max_new = "):
+        ac.defrag_kv_attend(arena, pages, lens, q, 1, INT8, starts=ints([0, 1]), max_new=-1)
+    for what, bad in (("budget", (1 << 32) + 64), ("max_len", 1 << 32), ("sink", 1 << 31), ("recent", 1 << 32)):
+        kw = {"budget": 64, what: bad}
+        with pytest.raises(ac.DefragError, match=what + " = "):
+            ac.defrag_kv_evict(arena, pages, lens, kw.pop("budget"), w, pos, wo, po, lo, 64, INT8, **kw)

@@ -112,3 +112,14 @@ def test_attend_takes_outputs_beside_inputs(change):
     a = _args(ac.defrag_kv_attend_args, **{**dict(group=4, weight_dev=0x1000, weight_stride=1024), **change})
     assert ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(a)) > 1
     assert ac.lib.defrag_kv_attend(ctypes.byref(a), None, 0, None) == ac.DEFRAG_EWORKSPACE
+
+
+def test_binding_refuses_numbers_that_do_not_fit():
+    """ctypes cuts a number to its field: 2^32 + 1 heads would be one."""
+    for heads, dim in (((1 << 32) + 1, 64), (1, (1 << 32) + 64), (-1, 64)):
+        with pytest.raises(ac.DefragError):
+            ac.defrag_kv_page_bytes(heads, dim)
+    assert ac._kv_int(0xFFFFFFFF, "x") == 0xFFFFFFFF and ac._kv_int(-5, "x", -5, 5) == -5
+    for bad in (-1, 1 << 32):
+        with pytest.raises(ac.DefragError, match="x = "):
+            ac._kv_int(bad, "x")
