@@ -22,7 +22,6 @@ namespace ac {
 
 constexpr int kKvPage = 64;       // tokens of a page
 constexpr int kKvExpMin = -64;    // least exponent of a scale
-constexpr uint32_t kKvMaxDim = 256;
 constexpr uint32_t kKvPromptRows = 128;  // query rows of a workgroup over a prompt
 
 // An axis of a grid holds fewer than 2^32 lanes, 2^22 workgroups of 1024.

@@ -11,13 +11,11 @@ constexpr int kE4m3 = 0, kInt8 = 1;
 constexpr int kBf16 = 0, kFp16 = 1;
 
 using half8 = __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16;
-using half4 = __attribute__((__vector_size__(4 * sizeof(_Float16)))) _Float16;
 using half2v = __attribute__((__vector_size__(2 * sizeof(_Float16)))) _Float16;
 using bf8 = __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16;
 using bf2 = __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16;
 using f32x4 = __attribute__((__vector_size__(16))) float;
 using f32x2 = __attribute__((__vector_size__(8))) float;
-using f32x16 = __attribute__((__vector_size__(64))) float;
 using u32x4 = __attribute__((__vector_size__(16))) uint32_t;
 using u32x2 = __attribute__((__vector_size__(8))) uint32_t;
 
@@ -59,12 +57,6 @@ __device__ inline int scale_exp(float amax) {
     const uint32_t top = CODES == kE4m3 ? 0x600000u : 0x7E0000u;
     const int e = (int)(b >> 23) - 127 - k + ((b & 0x7FFFFFu) > top ? 1 : 0);
     return e < kKvExpMin ? kKvExpMin : e;
-}
-
-// |x|, 0 for what is not finite (it takes no part in choosing a scale).
-__device__ inline float finite_abs(float x) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? __builtin_bit_cast(float, b) : 0.0f;
 }
 
 // A code's value.

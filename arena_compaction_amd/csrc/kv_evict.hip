@@ -50,7 +50,7 @@ struct Row {
     const float *w;
     const int32_t *pos;
     int64_t sink, border;
-    __device__ bool safe(int i) const { return pos[i] < sink || pos[i] >= border; }
+    __device__ bool safe(int32_t at) const { return at < sink || at >= border; }
 };
 
 __device__ inline Row row_of(const KvEvict &a, uint32_t h, uint32_t b) {
@@ -228,7 +228,7 @@ __device__ inline uint32_t load_keys_of(const Row &r, int base, int end, uint32_
 #pragma unroll
     for (int k = 0; k < KPT; ++k) {
         key[k] = weight_key(w[k]);
-        safe |= (uint32_t)(p[k] < r.sink || p[k] >= r.border) << k;
+        safe |= (uint32_t)r.safe(p[k]) << k;
     }
     return safe;
 }
