@@ -496,6 +496,9 @@ int defrag_monitor(const defrag_stats_t *stats, const defrag_monitor_cfg *cfg,
  * An entry that is negative, not a multiple of 32, or whose page would end
  * behind the arena is no page: its tokens are passed over (append and attend)
  * or its sequence is left alone (evict), and it is counted in *n_invalid_dev.
+ * Only entries that a call reads are looked at: append's of pages that get
+ * tokens, attend's of sequences with new tokens, evict's of sequences that
+ * hold more than the budget.
  * A sequence whose length, or whose range in starts_dev, is out of range
  * counts as one, and holds (or brings) no tokens; evict leaves it alone.
  *

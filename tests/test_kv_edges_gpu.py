@@ -318,3 +318,27 @@ def test_numbers_past_their_fields(ac):
         kw = {"budget": 64, what: bad}
         with pytest.raises(ac.DefragError, match=what + " = "):
             ac.defrag_kv_evict(arena, pages, lens, kw.pop("budget"), w, pos, wo, po, lo, 64, INT8, **kw)
+
+
+def test_entries_that_no_call_reads_are_not_counted(ac):
+    """A bad entry counts where its page would be read: behind the last token, of a sequence that brings nothing,
+    or of one that evict leaves as it is, it does not."""
+    c = Cache([3, 3], 1, 64, INT8)
+    c.fill_random([100, 100], 101)
+    c.pages[0, 2] = -1                  # behind the tokens
+    c.pages[1, 0] = 7                   # a sequence of no new tokens, within its budget
+    arena, pages, lens, n = c.arena.cuda(), c.pages.cuda(), ints([100, 100]), torch.full((1,), 5, dtype=torch.int64, device="cuda")
+    x = queries(3, 1, 64, torch.float16, 102).cuda()
+    ac.defrag_kv_append(arena, pages, ints([97, 100]), x, x, INT8, starts=ints([0, 3, 3]), n_invalid=n)
+    assert int(n) == 0
+    w, pos = torch.rand(2, 1, 192, device="cuda"), torch.arange(192, dtype=torch.int32, device="cuda").expand(2, 1, 192).contiguous()
+    before = w.clone()
+    ac.defrag_kv_attend(arena, pages, lens, x, 1, INT8, starts=ints([0, 3, 3]), weight=w, n_invalid=n)
+    assert int(n) == 0 and torch.equal(w[1], before[1])
+    wo, po, lo = torch.zeros(2, 1, 128, device="cuda"), torch.zeros(2, 1, 128, dtype=torch.int32, device="cuda"), ints([0, 0])
+    ac.defrag_kv_evict(arena, pages, lens, 128, w, pos, wo, po, lo, 64, INT8, n_invalid=n)
+    assert int(n) == 0 and lo.tolist() == [100, 100] and torch.equal(wo[:, :, :100], w[:, :, :100])
+    ac.defrag_kv_evict(arena, pages, lens, 64, w, pos, wo, po, lo, 64, INT8, n_invalid=n)
+    assert int(n) == 1 and lo.tolist() == [64, 100]
+    ac.defrag_kv_attend(arena, pages, lens, x, 1, INT8, starts=ints([0, 1, 3]), n_invalid=n)
+    assert int(n) == 1
