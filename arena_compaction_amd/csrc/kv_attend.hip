@@ -323,14 +323,25 @@ constexpr uint64_t kFewRows = 32;
 
 namespace {
 
-// Pieces of the cache for few rows.  Workgroups in flight are 3 a compute unit
-// with 16 rows, 2 with more.  The lengths differ, so few heads are cut into a
-// third more pieces than that, which even out; where the heads alone nearly
-// fill the unit, a cut leaves a few pieces over and costs more than it evens
-// out (64 sequences x 8 heads: whole 62 us, in halves 73).
-uint64_t few_splits(uint64_t units, uint32_t rows) {
-    const uint64_t target = rows == 16 ? 1024 : 512;
-    return units == 0 || units >= 512 ? 1 : (target + units - 1) / units;
+// Pieces of the cache for few rows.  Fewer (sequence, head)s than compute units
+// are cut into 1024 workgroups with 16 rows, 512 with more, so that lengths
+// that differ even out.  From a workgroup a unit on, a cut costs more than it
+// evens out, unless the caches are long, which 3 pieces fit best (3 workgroups
+// share a unit).  128 dimensions, 8 heads, lengths down to a tenth of:
+//             4096 tokens                     16,000 tokens
+//   units   whole   3   4 pieces            whole   3   4 pieces
+//    256     33    39    44 us               123   135   131 us
+//    384     52    48    55                  210   177   195
+//    504     57    60    76                  223   222   255
+//    512     60    61    77                  235   227   255
+//    520     66    61    81
+//    768     93    92   119                  342   319   383
+// and of 1000 tokens, 504 units, whole 20 us, in 3 pieces 28; with 32 rows, 504
+// units of 4096, 63 and 79; of 9000 whole and 3 pieces lie within a tenth.
+uint64_t few_splits(uint64_t units, uint64_t pages, uint32_t rows) {
+    if (units == 0) return 1;
+    if (units >= 256) return pages <= 192 ? 1 : 3;
+    return ((rows == 16 ? 1024 : 512) + units - 1) / units;
 }
 
 // Pieces for many rows: those that should end first.  A step is a page; beside
@@ -368,7 +379,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, p.rows);
+    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows);
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave

@@ -56,10 +56,11 @@ def test_attend_more_than_256_parts(ac, group, dim, codes, dtype, count, last):
     (2, 64, E4M3, torch.bfloat16, 1, True, None), (3, 128, INT8, torch.float16, 4, False, None),
     (4, 64, INT8, torch.float16, 6, True, None), (1, 64, E4M3, torch.bfloat16, 40, True, None),
     (2, 64, E4M3, torch.bfloat16, 1, False, 40), (1, 64, INT8, torch.bfloat16, 40, False, 40)])
-def test_attend_256_pages_a_part(ac, group, dim, codes, dtype, count, weight, far):
-    """So many sequences that a cache is cut only at 256 pages, the most that a wave's lanes hold (or, of many
-    rows, not at all)."""
-    B, heads, n = 260, 2, 260 * PAGE + 17
+@pytest.mark.parametrize("pages", [260, 800])
+def test_attend_256_pages_a_part(ac, pages, group, dim, codes, dtype, count, weight, far):
+    """So many sequences that a long cache is cut in few pieces, at 256 pages the latest, the most that a wave's
+    lanes hold (or, of many rows, not at all)."""
+    B, heads, n = 260, 2, pages * PAGE + 17
     c = repeated(heads, dim, codes, n, 2.0, far)
     q = queries(count, heads * group, dim, dtype, 114)
     w = torch.zeros(B, heads, c.pages.shape[1] * PAGE, device="cuda") if weight else None
