@@ -104,13 +104,12 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
     }
     arrived(scales[0]);
     arrived(scales[1]);
-    const int exp_here = off == kNoPage ? kNoExp : value_exp(scales[1]);
     auto next_band = [&]() __attribute__((always_inline)) {
-        const int left = (later >> lane) & 1 ? exp_here : kNoExp;
+        const int left = (later >> lane) & 1 ? value_exp(scales[1]) : kNoExp;
         todo = later & __builtin_amdgcn_ballot_w64(left <= least_of(left) + kBand);
         later &= ~todo;
     };
-    const int near = exp_here - __builtin_amdgcn_readlane(exp_here, good ? __builtin_ctzll(good) : 0) + kBand / 2;
+    const int near = value_exp(scales[1]) - value_exp(lane_f32(scales[1], good ? __builtin_ctzll(good) : 0)) + kBand / 2;
     if (good & __builtin_amdgcn_ballot_w64(near < 0 || near > kBand)) {
         next_band();
         get_keys(__builtin_ctzll(todo));
@@ -122,6 +121,7 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
     while (todo) {
         const int i = __builtin_ctzll(todo);
         todo &= todo - 1;
+        if (!todo && later) next_band();
         // the last page is loaded once more: loads under a condition would be
         // waited for as if they had not been issued, all of them at once
         const int next = todo ? __builtin_ctzll(todo) : i;
@@ -203,11 +203,6 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP>)) void k_
             }
         }
         get_values(next);
-        if (!todo && later) {
-            next_band();
-            get_keys(__builtin_ctzll(todo));
-            get_values(__builtin_ctzll(todo));
-        }
     }
     if constexpr (CODES == kE4m3) {
         if (__builtin_amdgcn_ballot_w64(no_numbers != 0)) {
