@@ -561,10 +561,11 @@ def _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid) -> defrag_kv_cac
     if not isinstance(lens, torch.Tensor) or lens.dtype is not torch.int32 or lens.dim() != 1 \
             or lens.shape[0] != batch:
         raise ValueError("lens: int32 [batch] expected, as many as pages has rows")
+    if (heads | dim) >> 32:
+        _kv_int(heads, "heads"), _kv_int(dim, "dim")
     return defrag_kv_cache(_kv_ptr(arena, torch.uint8, 0, dev, "arena"), arena.numel(),
                            _kv_ptr(pages, torch.int64, 0, dev, "pages"), stride,
-                           _kv_ptr(lens, torch.int32, 0, dev, "lens"), batch, _kv_int(heads, "heads"),
-                           _kv_int(dim, "dim"), kind,
+                           _kv_ptr(lens, torch.int32, 0, dev, "lens"), batch, heads, dim, kind,
                            None if n_invalid is None else
                            _kv_ptr(n_invalid, torch.int64, 1, dev, "n_invalid"))
 
@@ -598,7 +599,7 @@ def _kv_new(starts, max_new, tokens: int, batch: int, arena) -> int:
             raise ValueError(f"starts: {tokens} tokens of {batch} sequences need it")
         return min(1, tokens)
     _kv_ptr(starts, torch.int32, batch + 1, arena.get_device(), "starts")
-    return _kv_int(tokens if max_new is None else min(int(max_new), tokens), "max_new")
+    return tokens if max_new is None else _kv_int(min(int(max_new), tokens), "max_new")
 
 
 def _kv_stream(stream, dev: int) -> int:
@@ -693,9 +694,11 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
     if lse is not None:
         _kv_ptr(lse, torch.float32, tokens * q_heads, dev, "lse")
     cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
+    if (max_len | q_heads) >> 32:
+        _kv_int(max_len, "max_len"), _kv_int(q_heads, "query heads")
     a = defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
-                              KV_DTYPES[q.dtype], _kv_int(q_heads // heads, "group"), tokens, _opt(starts),
-                              most, _kv_int(max_len, "max_len"), dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
+                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
+                              max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
                               _opt(lse), _opt(weight), cap)
     need = lib.defrag_kv_attend_workspace_bytes(a)
     ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_attend")
@@ -735,9 +738,10 @@ def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, po
         next_pos = lens
     if max_len is None:
         max_len = min(pages.shape[1] * KV_PAGE_TOKENS, cap)
-    a = defrag_kv_evict_args(ctypes.pointer(c), _kv_int(budget, "budget"), _kv_int(max_len, "max_len"),
-                             _kv_int(sink, "sink", -(1 << 31), 0x7FFFFFFF),
-                             _kv_int(recent, "recent", -(1 << 31), 0x7FFFFFFF),
+    if (budget | max_len | (sink + 0x80000000) | (recent + 0x80000000)) >> 32:
+        _kv_int(budget, "budget"), _kv_int(max_len, "max_len")
+        _kv_int(sink, "sink", -(1 << 31), 0x7FFFFFFF), _kv_int(recent, "recent", -(1 << 31), 0x7FFFFFFF)
+    a = defrag_kv_evict_args(ctypes.pointer(c), budget, max_len, sink, recent,
                              _kv_ptr(next_pos, torch.int32, batch, dev, "next_pos"),
                              weight.data_ptr(), pos.data_ptr(), cap, weight_out.data_ptr(),
                              pos_out.data_ptr(), cap_out,
