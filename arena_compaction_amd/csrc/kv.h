@@ -1,6 +1,7 @@
 // kv.h -- the 8-bit key/value cache: the layout of a page, its number
 // formats and the launches of its operators (kv_api.cpp checks arguments;
-// kv_append.hip, kv_attend.hip and kv_evict.hip hold the kernels).
+// kv_append.hip, kv_attend.hip, kv_prompt.hip, kv_finish.hip and kv_evict.hip
+// hold the kernels).
 //
 // A page is one block of the arena with 64 tokens of every head.  For head h
 // a strip of 2 * 64 * D bytes: 64 x D key codes, token by token, and then

@@ -26,8 +26,8 @@
 // workgroups split a long cache and k_kv_finish joins their parts.
 //
 // It is bound by the cache's bytes: two documents of 131,000 tokens x 8 heads
-// of 128 (510 MB) take 95 us, 5.4 TB/s, where a reduction over 4 GiB reads 6.0;
-// a ragged batch of 64 x 4096 x 8 heads (296 MB) 62 us, 4.8 TB/s.
+// of 128 (510 MB) take 96 us, 5.3 TB/s, where a reduction over 4 GiB reads 5.9;
+// a ragged batch of 64 x 4096 x 8 heads (296 MB) 61 us, 4.9 TB/s.
 #include "kv_rows.h"
 
 namespace ac {

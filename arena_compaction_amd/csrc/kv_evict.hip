@@ -22,9 +22,9 @@
 //                finds the new scale and writes new codes.  Pages without a
 //                hole are left alone.
 // The fold is what an eviction costs: 32 sequences of up to 8190 tokens x 8
-// heads of 128 cut to 4096 take 18 us to choose and 111 to fold (408 MB through
+// heads of 128 cut to 4096 take 20 us to choose and 115 to fold (408 MB through
 // L2: every page with a hole is read for its largest code), two of 131,000 cut
-// to 32,768 take 46 and 109.  What bounds it is the latency of the strips that
+// to 32,768 take 47 and 108.  What bounds it is the latency of the strips that
 // follow one another through LDS, and of the lists before them.
 //
 // Tokens that move lie behind the budget, and a workgroup writes its own
@@ -537,7 +537,7 @@ __device__ inline float scale_quotient(float was, float inv) { return fminf(was 
 
 // A value code stands alone in its 64 bytes: a token's are D such rows apart.
 // Read byte by byte from memory, every lane would cost L1 an access of its
-// own (163 us for 32 x 8190 tokens cut to 4096, where this takes 111), so
+// own (163 us for 32 x 8190 tokens cut to 4096, where this takes 115), so
 // the strips that hold the page's tokens pass through LDS whole, one after the
 // other -- few, since moved tokens lie in order -- and bytes are picked there.
 // Keys and values of a page are two workgroups: each waits for little, and

@@ -11,7 +11,7 @@
 //                head) holds the page's keys and goes over all the rows that
 //                see it, or a piece of them, whose sums k_kv_add adds up.
 // The second is bound by the vector pipe (74% of the cycles) with an exponent
-// and two fused products a score: 250 us for 8200 tokens x 32 heads of 64.  The
+// and two fused products a score: 241 us for 8200 tokens x 32 heads of 64.  The
 // first moves 36 MB for 48 x 8000 tokens x 4 heads, 28 of them scores, in 14 us.
 //
 // A token belongs to one workgroup, and its rows are added in one order,

@@ -13,10 +13,10 @@
 // What bounds it: the vector pipe (an exponent, a fused product, an addition
 // and half a conversion a score) and the matrix pipe, which two waves a SIMD
 // overlap only in part.  Chunks of 2000 tokens x 32 heads of 128 behind 2048
-// (169 GFLOP) take 205 us, 0.82 PFLOP/s, where a product of 8192 cubed reaches
-// 1.26: the matrix pipe is busy for 31% of the cycles, the vector pipe for 37%,
+// (169 GFLOP) take 223 us, 0.76 PFLOP/s, where a product of 8192 cubed reaches
+// 1.18: the matrix pipe is busy for 31% of the cycles, the vector pipe for 37%,
 // and 22% are lost to the last rows, which see most.  With 64 dimensions the
-// vector pipe is busy for 83% (8200 tokens x 32 heads, float16: 420 us).
+// vector pipe is busy for 83% (8200 tokens x 32 heads, float16: 380 us).
 //
 // Workgroups of one key/value head run on one XCD where the heads are a
 // multiple of 8, so that its pages stay in that XCD's L2; the last rows,
