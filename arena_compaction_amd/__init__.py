@@ -138,6 +138,32 @@ class defrag_kv_evict_args(ctypes.Structure):
                 ("weight_out_stride", ctypes.c_uint64), ("lens_out_dev", ctypes.c_void_p)]
 
 
+class defrag_kv_rotary_args(ctypes.Structure):
+    _fields_ = [("append", ctypes.POINTER(defrag_kv_append_args)), ("freq_dev", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_uint32), ("interleaved", ctypes.c_int32),
+                ("token_pos_dev", ctypes.c_void_p), ("q_dev", ctypes.c_void_p),
+                ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("out_dev", ctypes.c_void_p), ("out_row", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("q_heads", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class defrag_kv_terms(ctypes.Structure):
+    _fields_ = [("mask_dev", ctypes.c_void_p), ("mask_words", ctypes.c_uint64),
+                ("cap", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("slopes_dev", ctypes.c_void_p), ("pos_dev", ctypes.c_void_p),
+                ("pos_stride", ctypes.c_uint64)]
+
+
+class defrag_kv_accept_args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(defrag_kv_cache)), ("tokens", ctypes.c_uint64),
+                ("starts_dev", ctypes.c_void_p), ("max_new", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("path_dev", ctypes.c_void_p),
+                ("path_stride", ctypes.c_uint64), ("kept_dev", ctypes.c_void_p),
+                ("weight_dev", ctypes.c_void_p), ("pos_dev", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_uint64), ("lens_out_dev", ctypes.c_void_p)]
+
+
 KV_PAGE_TOKENS = 64                # DEFRAG_KV_PAGE_TOKENS
 KV_CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}     # DEFRAG_KV_E4M3, DEFRAG_KV_INT8
 KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1}      # DEFRAG_KV_BF16, DEFRAG_KV_FP16
@@ -216,8 +242,14 @@ def _load() -> ctypes.CDLL:
     L.defrag_kv_attend.argtypes = [ctypes.POINTER(defrag_kv_attend_args), P, S, P]
     L.defrag_kv_evict_workspace_bytes.argtypes = [ctypes.POINTER(defrag_kv_evict_args)]
     L.defrag_kv_evict.argtypes = [ctypes.POINTER(defrag_kv_evict_args), P, S, P]
+    L.defrag_kv_append_rotary.argtypes = [ctypes.POINTER(defrag_kv_rotary_args), P]
+    L.defrag_kv_attend_terms_workspace_bytes.argtypes = [ctypes.POINTER(defrag_kv_attend_args),
+                                                         ctypes.POINTER(defrag_kv_terms)]
+    L.defrag_kv_attend_terms.argtypes = [ctypes.POINTER(defrag_kv_attend_args),
+                                         ctypes.POINTER(defrag_kv_terms), P, S, P]
+    L.defrag_kv_accept.argtypes = [ctypes.POINTER(defrag_kv_accept_args), P]
     for f in ("defrag_kv_page_bytes", "defrag_kv_attend_workspace_bytes",
-              "defrag_kv_evict_workspace_bytes"):
+              "defrag_kv_attend_terms_workspace_bytes", "defrag_kv_evict_workspace_bytes"):
         getattr(L, f).restype = S
     L.defrag_strerror.argtypes = [ctypes.c_int]
     L.defrag_strerror.restype = ctypes.c_char_p
@@ -225,7 +257,8 @@ def _load() -> ctypes.CDLL:
               "defrag_move", "defrag_monitor", "defrag_compact", "defrag_compact_static",
               "defrag_move_status", "defrag_move_report", "defrag_plan_tiles",
               "defrag_remap", "defrag_commit", "defrag_kv_append", "defrag_kv_attend",
-              "defrag_kv_evict"):
+              "defrag_kv_evict", "defrag_kv_append_rotary", "defrag_kv_attend_terms",
+              "defrag_kv_accept"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -240,7 +273,8 @@ EXPORTS = ("defrag_workspace_bytes", "defrag_stats", "defrag_first_fit", "defrag
            "defrag_compact", "defrag_compact_static", "defrag_monitor",
            "defrag_kv_page_bytes", "defrag_kv_append", "defrag_kv_attend_workspace_bytes",
            "defrag_kv_attend", "defrag_kv_evict_workspace_bytes", "defrag_kv_evict",
-           "defrag_strerror")
+           "defrag_kv_append_rotary", "defrag_kv_attend_terms_workspace_bytes",
+           "defrag_kv_attend_terms", "defrag_kv_accept", "defrag_strerror")
 
 
 def strerror(code: int) -> str:
@@ -632,15 +666,8 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
-def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Optional[int] = None,
-                     weight=None, pos=None, first_pos=None, n_invalid=None, stream=None) -> None:
-    """Quantise new tokens' keys and values [tokens, heads, dim] into the
-    pages of the cache.  arena: uint8; pages: int64 [batch, pages] byte offsets
-    in it; lens: int32 [batch], the lengths before the call (not changed);
-    codes: torch.float8_e4m3fn or torch.int8; starts: int32 [batch + 1], the
-    first new token of each sequence (None: one a sequence), at most max_new
-    each.  weight (float32) and pos (int32), [batch, heads, places], get 0 and
-    first_pos[b] + the token's number (default: its place)."""
+def _kv_append_args(arena, pages, lens, k, v, codes, starts, max_new, weight, pos, first_pos, n_invalid):
+    """The checked arguments of an append."""
     _kv_rows(k, arena, "k")
     tokens, heads, dim = k.shape
     _kv_rows(v, arena, "v", dim, heads)
@@ -653,28 +680,72 @@ def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Opti
     cap2 = _kv_plane(pos, arena, torch.int32, (batch, heads), "pos")
     if weight is not None and pos is not None and cap != cap2:
         raise ValueError("pos: another number of places than weight")
-    dev = arena.get_device()
     if first_pos is not None:
-        _kv_ptr(first_pos, torch.int32, batch, dev, "first_pos")
-    a = defrag_kv_append_args(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                              v.stride(0), v.stride(1), KV_DTYPES[k.dtype], most, tokens,
-                              _opt(starts), _opt(weight), _opt(pos), _opt(first_pos), cap or cap2)
-    rc = lib.defrag_kv_append(a, _kv_stream(stream, dev))
+        _kv_ptr(first_pos, torch.int32, batch, arena.get_device(), "first_pos")
+    return defrag_kv_append_args(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                                 v.stride(0), v.stride(1), KV_DTYPES[k.dtype], most, tokens,
+                                 _opt(starts), _opt(weight), _opt(pos), _opt(first_pos), cap or cap2)
+
+
+def defrag_kv_append(arena, pages, lens, k, v, codes, starts=None, max_new: Optional[int] = None,
+                     weight=None, pos=None, first_pos=None, n_invalid=None, stream=None) -> None:
+    """Quantise new tokens' keys and values [tokens, heads, dim] into the
+    pages of the cache.  arena: uint8; pages: int64 [batch, pages] byte offsets
+    in it; lens: int32 [batch], the lengths before the call (not changed);
+    codes: torch.float8_e4m3fn or torch.int8; starts: int32 [batch + 1], the
+    first new token of each sequence (None: one a sequence), at most max_new
+    each.  weight (float32) and pos (int32), [batch, heads, places], get 0 and
+    first_pos[b] + the token's number (default: its place)."""
+    a = _kv_append_args(arena, pages, lens, k, v, codes, starts, max_new, weight, pos, first_pos, n_invalid)
+    rc = lib.defrag_kv_append(a, _kv_stream(stream, arena.get_device()))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_append")
 
 
-def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
-                     max_new: Optional[int] = None, max_len: Optional[int] = None,
-                     scale: Optional[float] = None, out=None, lse=None, weight=None,
-                     n_invalid=None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Attention of the newest tokens' queries [tokens, query heads, dim] over
-    the cache; returns out, of q's type.  lens counts the new tokens too (call
-    defrag_kv_append first).  `heads` key/value heads, each read by an equal
-    share of the query heads.  max_len: no length exceeds it (default: what
-    the page table holds); scale: default dim ** -0.5.  lse: float32 [tokens,
-    query heads]; weight: float32 [batch, heads, places], increased by the
-    weight each cached token receives.  ws: workspace, allocated if None."""
+def defrag_kv_append_rotary(arena, pages, lens, k, v, codes, freq, q=None, q_out=None, interleaved: bool = False,
+                            starts=None, max_new: Optional[int] = None, token_pos=None, weight=None, pos=None,
+                            first_pos=None, n_invalid=None, stream=None):
+    """defrag_kv_append with keys that are rotated by their positions on the
+    way.  freq: float64 [pairs], the radians a position that each pair turns
+    by; pairs are (i, i + pairs), or with interleaved (2 i, 2 i + 1), of the
+    first 2 * pairs dimensions.  token_pos: int32 [tokens], positions (default:
+    first_pos[b] + the token's number), which pos gets.  q [tokens, query
+    heads, dim], of k's type, is rotated likewise into q_out, which is returned
+    (default: new memory; q itself: in place); tokens that belong to no
+    sequence are left out."""
+    a = _kv_append_args(arena, pages, lens, k, v, codes, starts, max_new, weight, pos, first_pos, n_invalid)
+    dev, (tokens, _, dim) = arena.get_device(), k.shape
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq: float64 [pairs] expected")
+    if token_pos is not None:
+        _kv_ptr(token_pos, torch.int32, tokens, dev, "token_pos")
+    heads = 0
+    if q is not None:
+        _kv_rows(q, arena, "q", dim)
+        if q.shape[0] != tokens or q.dtype != k.dtype:
+            raise ValueError("q: other tokens or another dtype than k")
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = _kv_new_empty(q, q.shape, stream)
+        else:
+            _kv_rows(q_out, arena, "q_out", dim, heads)
+            if q_out.shape[0] != tokens or q_out.dtype != q.dtype:
+                raise ValueError("q_out: another shape or dtype than q")
+    elif q_out is not None:
+        raise ValueError("q_out: nothing to rotate without q")
+    r = defrag_kv_rotary_args(ctypes.pointer(a), _kv_ptr(freq, torch.float64, 0, dev, "freq"),
+                              _kv_int(2 * freq.shape[0], "rotated dimensions"), 1 if interleaved else 0,
+                              _opt(token_pos), _opt(q), q.stride(0) if heads else 0, q.stride(1) if heads else 0,
+                              _opt(q_out), q_out.stride(0) if heads else 0, q_out.stride(1) if heads else 0, heads, 0)
+    rc = lib.defrag_kv_append_rotary(r, _kv_stream(stream, dev))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_append_rotary")
+    return q_out
+
+
+def _kv_attend_args(arena, pages, lens, q, heads, codes, starts, max_new, max_len, scale, out, lse, weight, n_invalid,
+                    stream):
+    """(the checked arguments of an attention, its output)."""
     _kv_rows(q, arena, "q")
     tokens, q_heads, dim = q.shape
     if heads < 1 or q_heads % heads:
@@ -696,16 +767,93 @@ def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
     cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
     if (max_len | q_heads) >> 32:
         _kv_int(max_len, "max_len"), _kv_int(q_heads, "query heads")
-    a = defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
-                              KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
-                              max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
-                              _opt(lse), _opt(weight), cap)
+    return defrag_kv_attend_args(ctypes.pointer(c), q.data_ptr(), q.stride(0), q.stride(1),
+                                 KV_DTYPES[q.dtype], q_heads // heads, tokens, _opt(starts), most,
+                                 max_len, dim ** -0.5 if scale is None else scale, 0, out.data_ptr(),
+                                 _opt(lse), _opt(weight), cap), out
+
+
+def defrag_kv_attend(arena, pages, lens, q, heads: int, codes, starts=None,
+                     max_new: Optional[int] = None, max_len: Optional[int] = None,
+                     scale: Optional[float] = None, out=None, lse=None, weight=None,
+                     n_invalid=None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the newest tokens' queries [tokens, query heads, dim] over
+    the cache; returns out, of q's type.  lens counts the new tokens too (call
+    defrag_kv_append first).  `heads` key/value heads, each read by an equal
+    share of the query heads.  max_len: no length exceeds it (default: what
+    the page table holds); scale: default dim ** -0.5.  lse: float32 [tokens,
+    query heads]; weight: float32 [batch, heads, places], increased by the
+    weight each cached token receives.  ws: workspace, allocated if None."""
+    a, out = _kv_attend_args(arena, pages, lens, q, heads, codes, starts, max_new, max_len, scale, out, lse, weight,
+                             n_invalid, stream)
     need = lib.defrag_kv_attend_workspace_bytes(a)
     ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_attend")
-    rc = lib.defrag_kv_attend(a, at, size, _kv_stream(stream, dev))
+    rc = lib.defrag_kv_attend(a, at, size, _kv_stream(stream, arena.get_device()))
     if rc != DEFRAG_OK:
         raise DefragError(rc, "defrag_kv_attend")
     return out
+
+
+def defrag_kv_attend_terms(arena, pages, lens, q, heads: int, codes, mask=None, cap: Optional[float] = None,
+                           slopes=None, pos=None, starts=None, max_new: Optional[int] = None,
+                           max_len: Optional[int] = None, scale: Optional[float] = None, out=None, lse=None,
+                           weight=None, n_invalid=None, ws: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """defrag_kv_attend with terms beside causal softmax.  mask: int64 [tokens,
+    words], bit j % 64 of word j / 64 says that the token sees new token j of
+    its sequence (it sees all older ones); cap: scores become cap * tanh(score
+    / cap); slopes: float32 [query heads], times the cached token's position
+    less the query's, is added to a score; pos: int32 [batch, heads, places],
+    the positions (default: the places), a multiple of 64 of them and at least
+    max_len."""
+    a, out = _kv_attend_args(arena, pages, lens, q, heads, codes, starts, max_new, max_len, scale, out, lse, weight,
+                             n_invalid, stream)
+    dev, (tokens, q_heads, _) = arena.get_device(), q.shape
+    words = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2 or mask.shape[0] != tokens:
+            raise ValueError("mask: int64 [tokens, words] expected")
+        _kv_ptr(mask, torch.int64, 0, dev, "mask")
+        words = mask.shape[1]
+    if slopes is not None:
+        _kv_ptr(slopes, torch.float32, q_heads, dev, "slopes")
+    c = a.cache.contents
+    places = _kv_plane(pos, arena, torch.int32, (c.batch, c.heads), "pos")
+    t = defrag_kv_terms(_opt(mask), words, 0.0 if cap is None else cap, 0, _opt(slopes), _opt(pos), places)
+    need = lib.defrag_kv_attend_terms_workspace_bytes(a, t)
+    ws, at, size = _kv_scratch(need, ws, arena, stream, "defrag_kv_attend_terms")
+    rc = lib.defrag_kv_attend_terms(a, t, at, size, _kv_stream(stream, dev))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_attend_terms")
+    return out
+
+
+def defrag_kv_accept(arena, pages, lens, path, kept, lens_out, heads: int, dim: int, codes, starts=None,
+                     max_new: Optional[int] = None, weight=None, pos=None, n_invalid=None, stream=None) -> None:
+    """Keep the accepted path of each sequence's drafted tokens, its last ones
+    (lens counts them; starts: int32 [batch + 1], as in append, None: one
+    each).  path: int32 [batch, most], ascending numbers of drafted tokens, of
+    which kept (int32 [batch]) count; they move to the places behind the
+    sequence's other tokens, with their weight (float32) and pos (int32),
+    [batch, heads, places].  lens_out: int32 [batch], the new lengths, memory
+    of its own."""
+    c = _kv_cache(arena, pages, lens, heads, dim, codes, n_invalid)
+    dev, batch = arena.get_device(), c.batch
+    tokens = batch if starts is None else 1 << 29   # (none of them is read: starts may begin anywhere)
+    most = _kv_new(starts, max_new, tokens, batch, arena)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != batch:
+        raise ValueError("path: int32 [batch, most] expected")
+    cap = _kv_plane(weight, arena, torch.float32, (batch, heads), "weight")
+    cap2 = _kv_plane(pos, arena, torch.int32, (batch, heads), "pos")
+    if weight is not None and pos is not None and cap != cap2:
+        raise ValueError("pos: another number of places than weight")
+    a = defrag_kv_accept_args(ctypes.pointer(c), tokens, _opt(starts), most, 0,
+                              _kv_ptr(path, torch.int32, 0, dev, "path"), path.shape[1],
+                              _kv_ptr(kept, torch.int32, batch, dev, "kept"), _opt(weight), _opt(pos), cap or cap2,
+                              _kv_ptr(lens_out, torch.int32, batch, dev, "lens_out"))
+    rc = lib.defrag_kv_accept(a, _kv_stream(stream, dev))
+    if rc != DEFRAG_OK:
+        raise DefragError(rc, "defrag_kv_accept")
 
 
 def defrag_kv_evict(arena, pages, lens, budget: int, weight, pos, weight_out, pos_out, lens_out,

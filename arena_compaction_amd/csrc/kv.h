@@ -1,7 +1,7 @@
 // kv.h -- the 8-bit key/value cache: the layout of a page, its number
 // formats and the launches of its operators (kv_api.cpp checks arguments;
-// kv_append.hip, kv_attend.hip, kv_prompt.hip, kv_finish.hip and kv_evict.hip
-// hold the kernels).
+// kv_store.h, kv_turn.h, kv_few.h, kv_prompt.h, kv_weigh.h, kv_finish.hip,
+// kv_evict.hip and kv_accept.hip hold the kernels).
 //
 // A page is one block of the arena with 64 tokens of every head.  For head h
 // a strip of 2 * 64 * D bytes: 64 x D key codes, token by token, and then
@@ -65,6 +65,20 @@ struct KvAppend {
     uint64_t cap;
 };
 
+// Appending with rotated keys, and queries rotated beside them.
+struct KvRotary : KvAppend {
+    const double *freq;        // radians a position of each pair
+    uint32_t rotary;           // dimensions that are rotated, two a pair
+    int32_t next;              // pairs of neighbours, else of the two halves
+    const int32_t *token_pos;  // tokens, or null: first_pos and the number
+    const uint16_t *q;
+    int64_t q_row, q_head;
+    uint16_t *q_out;
+    int64_t o_row, o_head;
+    uint32_t q_heads;
+};
+constexpr uint32_t kRotaryHeads = 8;  // query heads of a workgroup
+
 struct KvAttend {
     KvCache c;
     const uint16_t *q;
@@ -89,6 +103,31 @@ struct KvAttend {
     // in each, and what each piece adds to a token (where there is more than one)
     uint32_t weigh_pieces, weigh_tiles;
     float *weigh_part;  // [pieces][batch][heads][score_pages][64]
+    // terms beside causal softmax (null and 0 where there are none)
+    const uint64_t *mask;  // [tokens][mask_words] bits
+    uint64_t mask_words;
+    float score_cap;       // natural units
+    const float *slopes;   // [heads * group]
+    const int32_t *pos;    // [batch][heads][pos_cap]
+    uint64_t pos_cap;
+};
+
+// Which terms a kernel knows: none, the mask, or all of them.
+constexpr int kPlain = 0, kMasked = 1, kTerms = 2;
+inline int kv_mode(const KvAttend &a) { return a.score_cap != 0.0f || a.slopes ? kTerms : a.mask ? kMasked : kPlain; }
+
+struct KvAccept {
+    KvCache c;
+    const int32_t *starts;  // batch + 1, or null: one token a sequence
+    uint64_t tokens;
+    uint32_t max_new;
+    const int32_t *path;    // [batch][path_stride]
+    uint64_t path_stride;
+    const int32_t *kept;
+    float *weight;          // [batch][heads][cap], or null
+    int32_t *pos;
+    uint64_t cap;
+    int32_t *lens_out;
 };
 
 struct KvEvict {
@@ -145,9 +184,16 @@ inline uint32_t kv_append_pages(uint32_t max_new, uint64_t stride) {
 
 // codes: 0 e4m3, 1 int8; dtype: 0 bfloat16, 1 float16
 hipError_t launch_kv_append(const KvAppend &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_append_rotary(const KvRotary &a, int codes, int dtype, hipStream_t s);
+hipError_t launch_kv_accept(const KvAccept &a, int codes, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s);
-hipError_t launch_kv_prompt(const KvAttend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_finish(const KvAttend &a, int dtype, hipStream_t s);
+// (instantiated for each mode where its kernels are compiled)
+template <int MODE>
+hipError_t launch_kv_few(const KvAttend &a, int codes, int dtype, hipStream_t s);
+template <int MODE>
+hipError_t launch_kv_prompt(const KvAttend &a, int codes, int dtype, hipStream_t s);
+template <int MODE>
 hipError_t launch_kv_weigh(const KvAttend &a, int codes, int dtype, hipStream_t s);
 hipError_t launch_kv_evict(const KvEvict &a, int codes, hipStream_t s);
 hipError_t launch_kv_zero(uint64_t *p, hipStream_t s);

@@ -12,6 +12,9 @@ constexpr uint64_t kMaxGrid = (1u << 24) - 1;  // workgroups of 256 along one ax
 constexpr uint64_t kMaxHeadRows = 0x7FFFFC00u;  // query rows of a (sequence, head): the kernels hold them in an int
 constexpr uint64_t kMaxRows = 1ull << 36;       // query rows of a call: sizes in bytes stay below 2^64
 constexpr uint64_t kMaxEvict = 1u << 25;  // tokens of an evicted sequence
+constexpr uint64_t kMaxMaskWords = kMaxTokens / 64;
+constexpr float kLeastCap = 0x1p-64f, kMostCap = 0x1p64f;  // so that its inverse is a number
+constexpr uint64_t kMaxPath = 1ull << 32;  // entries of a row: sizes in bytes stay below 2^64
 constexpr uint64_t kLeastWs = 1;  // none is needed: 0 means "refused"
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -38,6 +41,42 @@ Span strided(const void *p, uint64_t tokens, int64_t row, uint64_t heads, int64_
     const __int128 r = (__int128)(tokens - 1) * row, h = (__int128)(heads - 1) * head;
     const __int128 lo = (r < 0 ? r : 0) + (h < 0 ? h : 0), hi = (r > 0 ? r : 0) + (h > 0 ? h : 0) + dim;
     return Span{reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(p) + (intptr_t)(lo * 2)), (unsigned __int128)(hi - lo) * 2};
+}
+
+// Whether no two rows of tokens x heads x dim numbers share memory: one stride
+// steps over all that the other reaches.
+bool rows_apart(uint64_t tokens, int64_t row, uint64_t heads, int64_t head, uint32_t dim) {
+    const __int128 r = row < 0 ? -(__int128)row : row, h = head < 0 ? -(__int128)head : head;
+    const __int128 of_heads = (__int128)(heads - 1) * h + dim, of_tokens = (__int128)(tokens - 1) * r + dim;
+    const bool token_by_token = (heads == 1 || h >= dim) && (tokens == 1 || r >= of_heads);
+    const bool head_by_head = (tokens == 1 || r >= dim) && (heads == 1 || h >= of_tokens);
+    return token_by_token || head_by_head;
+}
+
+// tokens x heads x dim numbers of 2 bytes.
+struct Rows {
+    const void *p;
+    uint64_t tokens;
+    int64_t row;
+    uint64_t heads;
+    int64_t head;
+    uint32_t dim;
+    Span span() const { return strided(p, tokens, row, heads, head, dim); }
+};
+
+// Whether two sets of rows share memory, or cannot be seen not to: slices of
+// one fused projection lie between one another's rows, the same stride apart.
+bool rows_overlap(const Rows &a, const Rows &b) {
+    const Span x = a.span(), y = b.span();
+    if (!overlap(x, y)) return false;
+    const __int128 step = a.row < 0 ? -(__int128)a.row : a.row;
+    if (a.tokens < 2 || b.tokens < 2 || (b.row != a.row && b.row != -a.row)) return true;
+    const Span one = Rows{a.p, 1, 0, a.heads, a.head, a.dim}.span(), two = Rows{b.p, 1, 0, b.heads, b.head, b.dim}.span();
+    const __int128 wide = (__int128)one.bytes / 2, broad = (__int128)two.bytes / 2;
+    __int128 at = ((__int128)reinterpret_cast<uintptr_t>(two.p) - (__int128)reinterpret_cast<uintptr_t>(one.p)) / 2;
+    if (step == 0) return true;
+    at = (at % step + step) % step;
+    return at < wide || at + broad > step;
 }
 
 // Whether outputs overlap one another or an input.
@@ -83,6 +122,78 @@ int check_new(const defrag_kv_cache *c, const int32_t *starts, uint64_t tokens, 
     if (tokens && (c->batch == 0 || max_new == 0)) return DEFRAG_EINVAL;
     if (max_new > tokens) return DEFRAG_EINVAL;
     return DEFRAG_OK;
+}
+
+int check_append(const defrag_kv_append_args *a) {
+    if (!a) return DEFRAG_EINVAL;
+    int rc = check_cache(a->cache);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = check_new(c, a->starts_dev, a->tokens, a->max_new);
+    if (rc) return rc;
+    if (!dtype_ok(a->dtype) || !aligned(a->k_dev, 2) || !aligned(a->v_dev, 2) ||
+        !aligned(a->weight_dev, 4) || !aligned(a->pos_dev, 4) || !aligned(a->first_pos_dev, 4))
+        return DEFRAG_EINVAL;
+    if (a->tokens && (!a->k_dev || !a->v_dev)) return DEFRAG_EINVAL;
+    if ((uint64_t)kv_append_pages(a->max_new, c->page_stride) * 2 * c->dim > 0xFFFFFFFFu) return DEFRAG_EINVAL;
+    return DEFRAG_OK;
+}
+
+KvAppend append_of(const defrag_kv_append_args *a) {
+    return KvAppend{cache_of(a->cache),
+                    static_cast<const uint16_t *>(a->k_dev), static_cast<const uint16_t *>(a->v_dev),
+                    a->k_row, a->k_head, a->v_row, a->v_head, a->tokens, a->starts_dev, a->max_new,
+                    a->weight_dev, a->pos_dev, a->first_pos_dev, a->weight_stride};
+}
+
+int check_rotary(const defrag_kv_rotary_args *r) {
+    if (!r) return DEFRAG_EINVAL;
+    const defrag_kv_append_args *a = r->append;
+    const int rc = check_append(a);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    if (r->rotary_dim < 8 || r->rotary_dim % 8 || r->rotary_dim > c->dim || (r->interleaved != 0 && r->interleaved != 1))
+        return DEFRAG_EINVAL;
+    if (!aligned(r->freq_dev, 8) || !aligned(r->token_pos_dev, 4) || !aligned(r->q_dev, 2) || !aligned(r->out_dev, 2))
+        return DEFRAG_EINVAL;
+    if (a->tokens && (!r->freq_dev || (r->q_heads && (!r->q_dev || !r->out_dev)))) return DEFRAG_EINVAL;
+    if (c->heads + ((uint64_t)r->q_heads + kRotaryHeads - 1) / kRotaryHeads > 65535 || a->tokens * r->q_heads > kMaxRows)
+        return DEFRAG_EINVAL;
+    if (!a->tokens || !r->q_heads) return DEFRAG_OK;
+    if (!rows_apart(a->tokens, r->out_row, r->q_heads, r->out_head, c->dim)) return DEFRAG_EINVAL;
+    const Rows to{r->out_dev, a->tokens, r->out_row, r->q_heads, r->out_head, c->dim};
+    const Rows q{r->q_dev, a->tokens, r->q_row, r->q_heads, r->q_head, c->dim};
+    const Rows k{a->k_dev, a->tokens, a->k_row, c->heads, a->k_head, c->dim}, v{a->v_dev, a->tokens, a->v_row, c->heads, a->v_head, c->dim};
+    const bool same = r->out_dev == r->q_dev && (a->tokens == 1 || r->out_row == r->q_row) && (r->q_heads == 1 || r->out_head == r->q_head);
+    const uint64_t rows = (uint64_t)c->batch * c->heads;
+    if ((!same && rows_overlap(to, q)) || rows_overlap(to, k) || rows_overlap(to, v)) return DEFRAG_EINVAL;
+    const Span out[] = {to.span()};
+    const Span in[] = {Span{c->arena_dev, c->arena_bytes}, plane(a->weight_dev, rows, a->weight_stride, a->weight_stride),
+                       plane(a->pos_dev, rows, a->weight_stride, a->weight_stride), plane(r->freq_dev, 1, 0, r->rotary_dim),
+                       plane(r->token_pos_dev, 1, 0, a->tokens), plane(a->first_pos_dev, 1, 0, c->batch),
+                       plane(a->starts_dev, 1, 0, c->batch + 1ull), plane(c->lens_dev, 1, 0, c->batch),
+                       plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
+    return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
+}
+
+int check_accept(const defrag_kv_accept_args *a) {
+    if (!a) return DEFRAG_EINVAL;
+    int rc = check_cache(a->cache);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = check_new(c, a->starts_dev, a->tokens, a->max_new);
+    if (rc) return rc;
+    if (a->path_stride > kMaxPath || !aligned(a->path_dev, 4) || !aligned(a->kept_dev, 4) || !aligned(a->weight_dev, 4) ||
+        !aligned(a->pos_dev, 4) || !aligned(a->lens_out_dev, 4))
+        return DEFRAG_EINVAL;
+    if (c->batch && (!a->kept_dev || !a->lens_out_dev || (a->path_stride && !a->path_dev))) return DEFRAG_EINVAL;
+    const uint64_t rows = (uint64_t)c->batch * c->heads;
+    const Span out[] = {plane(a->lens_out_dev, 1, 0, c->batch), plane(a->weight_dev, rows, a->weight_stride, a->weight_stride),
+                        plane(a->pos_dev, rows, a->weight_stride, a->weight_stride), Span{c->arena_dev, c->arena_bytes}};
+    const Span in[] = {plane(c->lens_dev, 1, 0, c->batch), plane(a->starts_dev, 1, 0, c->batch + 1ull),
+                       plane(a->path_dev, c->batch, a->path_stride, a->path_stride), plane(a->kept_dev, 1, 0, c->batch),
+                       plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
+    return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
 }
 
 KvAttendPlan plan_of(const defrag_kv_attend_args *a) {
@@ -131,6 +242,25 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
     return DEFRAG_OK;
 }
 
+// The same with terms; a call without any is defrag_kv_attend's.
+int check_terms(const defrag_kv_attend_args *a, const defrag_kv_terms *t, KvAttendPlan *p) {
+    const int rc = check_attend(a, p);
+    if (rc) return rc;
+    if (!t) return DEFRAG_EINVAL;
+    const defrag_kv_cache *c = a->cache;
+    if (t->cap != 0.0f && !(t->cap >= kLeastCap && t->cap <= kMostCap)) return DEFRAG_EINVAL;
+    if (!aligned(t->mask_dev, 8) || !aligned(t->slopes_dev, 4) || !aligned(t->pos_dev, 4)) return DEFRAG_EINVAL;
+    if (t->mask_dev && (t->mask_words > kMaxMaskWords || t->mask_words * 64 < a->max_new)) return DEFRAG_EINVAL;
+    const uint64_t places = (a->max_len + (uint64_t)kKvPage - 1) / kKvPage * kKvPage;
+    if (t->pos_dev && (t->pos_stride < places || t->pos_stride > kMaxTokens)) return DEFRAG_EINVAL;
+    const uint64_t q_heads = (uint64_t)c->heads * a->group, rows = a->tokens * q_heads, units = (uint64_t)c->batch * c->heads;
+    const Span out[] = {plane(a->out_dev, 1, 0, rows * c->dim / 2), plane(a->lse_dev, 1, 0, rows),
+                        plane(a->weight_dev, units, a->weight_stride, a->max_len)};
+    const Span in[] = {plane(t->mask_dev, 1, 0, 2 * a->tokens * t->mask_words), plane(t->slopes_dev, 1, 0, q_heads),
+                       plane(t->pos_dev, units, t->pos_stride, places)};
+    return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
+}
+
 int check_evict(const defrag_kv_evict_args *a) {
     if (!a) return DEFRAG_EINVAL;
     const int rc = check_cache(a->cache);
@@ -174,49 +304,11 @@ int check_ws(const void *ws, size_t have, uint64_t need) {
     return DEFRAG_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t defrag_kv_page_bytes(uint32_t heads, uint32_t dim) {
-    if (heads < 1 || heads > 65535 || !dim_ok(dim)) return 0;
-    return (kv_page_bytes(heads, dim) + 31) / 32 * 32;
-}
-
-int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
-    if (!a) return DEFRAG_EINVAL;
-    int rc = check_cache(a->cache);
-    if (rc) return rc;
+// The launches of an attention whose arguments have been checked.
+int attend(const defrag_kv_attend_args *a, const defrag_kv_terms *t, const KvAttendPlan &p, void *ws_dev, size_t ws_bytes,
+           hipStream_t stream) {
     const defrag_kv_cache *c = a->cache;
-    rc = check_new(c, a->starts_dev, a->tokens, a->max_new);
-    if (rc) return rc;
-    if (!dtype_ok(a->dtype) || !aligned(a->k_dev, 2) || !aligned(a->v_dev, 2) ||
-        !aligned(a->weight_dev, 4) || !aligned(a->pos_dev, 4) || !aligned(a->first_pos_dev, 4))
-        return DEFRAG_EINVAL;
-    if (a->tokens && (!a->k_dev || !a->v_dev)) return DEFRAG_EINVAL;
-    if ((uint64_t)kv_append_pages(a->max_new, c->page_stride) * 2 * c->dim > 0xFFFFFFFFu) return DEFRAG_EINVAL;
-    rc = clear_count(c, stream);
-    if (rc || !a->tokens) return rc;
-    const KvAppend k{cache_of(c),
-                     static_cast<const uint16_t *>(a->k_dev), static_cast<const uint16_t *>(a->v_dev),
-                     a->k_row, a->k_head, a->v_row, a->v_head, a->tokens, a->starts_dev, a->max_new,
-                     a->weight_dev, a->pos_dev, a->first_pos_dev, a->weight_stride};
-    return launch_kv_append(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
-}
-
-size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *a) {
-    KvAttendPlan p;
-    if (check_attend(a, &p)) return 0;
-    return p.total > kLeastWs ? p.total : kLeastWs;
-}
-
-int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_bytes,
-                     hipStream_t stream) {
-    KvAttendPlan p;
-    int rc = check_attend(a, &p);
-    if (rc) return rc;
-    const defrag_kv_cache *c = a->cache;
-    rc = check_ws(ws_dev, ws_bytes, p.total);
+    int rc = check_ws(ws_dev, ws_bytes, p.total);
     if (rc) return rc;
     rc = clear_count(c, stream);
     if (rc || !a->tokens) return rc;
@@ -248,7 +340,93 @@ int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_byt
     k.weigh_pieces = p.weigh_pieces;
     k.weigh_tiles = p.weigh_tiles;
     k.weigh_part = p.weigh_bytes ? reinterpret_cast<float *>(ws + p.part_bytes + p.score_bytes + p.sum_bytes) : nullptr;
+    if (t) {
+        k.mask = t->mask_dev;
+        k.mask_words = t->mask_words;
+        k.score_cap = t->cap;
+        k.slopes = t->slopes_dev;
+        k.pos = t->pos_dev;
+        k.pos_cap = t->pos_stride;
+    }
     return launch_kv_attend(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t defrag_kv_page_bytes(uint32_t heads, uint32_t dim) {
+    if (heads < 1 || heads > 65535 || !dim_ok(dim)) return 0;
+    return (kv_page_bytes(heads, dim) + 31) / 32 * 32;
+}
+
+int defrag_kv_append(const defrag_kv_append_args *a, hipStream_t stream) {
+    int rc = check_append(a);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = clear_count(c, stream);
+    if (rc || !a->tokens) return rc;
+    return launch_kv_append(append_of(a), c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+int defrag_kv_append_rotary(const defrag_kv_rotary_args *r, hipStream_t stream) {
+    int rc = check_rotary(r);
+    if (rc) return rc;
+    const defrag_kv_append_args *a = r->append;
+    const defrag_kv_cache *c = a->cache;
+    rc = clear_count(c, stream);
+    if (rc || !a->tokens) return rc;
+    KvRotary k{};
+    static_cast<KvAppend &>(k) = append_of(a);
+    k.freq = r->freq_dev;
+    k.rotary = r->rotary_dim;
+    k.next = r->interleaved;
+    k.token_pos = r->token_pos_dev;
+    k.q = static_cast<const uint16_t *>(r->q_dev);
+    k.q_row = r->q_row;
+    k.q_head = r->q_head;
+    k.q_out = static_cast<uint16_t *>(r->out_dev);
+    k.o_row = r->out_row;
+    k.o_head = r->out_head;
+    k.q_heads = r->q_heads;
+    return launch_kv_append_rotary(k, c->codes, a->dtype, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+int defrag_kv_accept(const defrag_kv_accept_args *a, hipStream_t stream) {
+    int rc = check_accept(a);
+    if (rc) return rc;
+    const defrag_kv_cache *c = a->cache;
+    rc = clear_count(c, stream);
+    if (rc || !c->batch) return rc;
+    const KvAccept k{cache_of(c), a->starts_dev, a->tokens, a->max_new, a->path_dev, a->path_stride, a->kept_dev,
+                     a->weight_dev, a->pos_dev, a->weight_stride, a->lens_out_dev};
+    return launch_kv_accept(k, c->codes, stream) == hipSuccess ? DEFRAG_OK : DEFRAG_EHIP;
+}
+
+size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *a) {
+    KvAttendPlan p;
+    if (check_attend(a, &p)) return 0;
+    return p.total > kLeastWs ? p.total : kLeastWs;
+}
+
+int defrag_kv_attend(const defrag_kv_attend_args *a, void *ws_dev, size_t ws_bytes,
+                     hipStream_t stream) {
+    KvAttendPlan p;
+    const int rc = check_attend(a, &p);
+    return rc ? rc : attend(a, nullptr, p, ws_dev, ws_bytes, stream);
+}
+
+size_t defrag_kv_attend_terms_workspace_bytes(const defrag_kv_attend_args *a, const defrag_kv_terms *t) {
+    KvAttendPlan p;
+    if (check_terms(a, t, &p)) return 0;
+    return p.total > kLeastWs ? p.total : kLeastWs;
+}
+
+int defrag_kv_attend_terms(const defrag_kv_attend_args *a, const defrag_kv_terms *t, void *ws_dev, size_t ws_bytes,
+                           hipStream_t stream) {
+    KvAttendPlan p;
+    const int rc = check_terms(a, t, &p);
+    return rc ? rc : attend(a, t, p, ws_dev, ws_bytes, stream);
 }
 
 size_t defrag_kv_evict_workspace_bytes(const defrag_kv_evict_args *a) {

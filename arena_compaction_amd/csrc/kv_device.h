@@ -49,13 +49,14 @@ __device__ inline int exp_of_pow2(float s) {
 }
 
 // Least e with amax <= largest code * 2^e (448 = 1.75 * 2^8, 127 =
-// 1.984375 * 2^6), at least kKvExpMin; amax is finite and not negative.
+// 1.984375 * 2^6), at least kKvExpMin; amax is finite and not negative,
+// and stands for amax * 2^shift.
 template <int CODES>
-__device__ inline int scale_exp(float amax) {
+__device__ inline int scale_exp(float amax, int shift = 0) {
     const uint32_t b = __builtin_bit_cast(uint32_t, amax);
     const int k = CODES == kE4m3 ? 8 : 6;
     const uint32_t top = CODES == kE4m3 ? 0x600000u : 0x7E0000u;
-    const int e = (int)(b >> 23) - 127 - k + ((b & 0x7FFFFFu) > top ? 1 : 0);
+    const int e = (int)(b >> 23) - 127 - k + ((b & 0x7FFFFFu) > top ? 1 : 0) + shift;
     return e < kKvExpMin ? kKvExpMin : e;
 }
 

@@ -1,0 +1,41 @@
+// kv_rotary.hip -- new tokens into the pages of the 8-bit cache, their keys
+// rotated by their positions on the way (kv_turn.h), and their queries beside
+// them: the kernel is kv_store.h's, whose grid has workgroups for the queries
+// behind those of the heads.
+#include "kv_store.h"
+
+namespace ac {
+namespace {
+
+template <int D, int CODES>
+void rotary_go(const KvRotary &a, int dtype, dim3 grid, hipStream_t s) {
+    if (dtype == kBf16)
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kBf16, true>), grid, dim3(2 * D), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kFp16, true>), grid, dim3(2 * D), 0, s, a);
+}
+
+template <int D>
+void rotary_codes(const KvRotary &a, int codes, int dtype, dim3 grid, hipStream_t s) {
+    if (codes == kE4m3)
+        rotary_go<D, kE4m3>(a, dtype, grid, s);
+    else
+        rotary_go<D, kInt8>(a, dtype, grid, s);
+}
+
+}  // namespace
+
+hipError_t launch_kv_append_rotary(const KvRotary &a, int codes, int dtype, hipStream_t s) {
+    const dim3 grid(kv_append_pages(a.max_new, a.c.stride), a.c.heads + (a.q_heads + kRotaryHeads - 1) / kRotaryHeads, a.c.batch);
+    switch (a.c.dim) {
+        case 64: rotary_codes<64>(a, codes, dtype, grid, s); break;
+        case 96: rotary_codes<96>(a, codes, dtype, grid, s); break;
+        case 128: rotary_codes<128>(a, codes, dtype, grid, s); break;
+        case 192: rotary_codes<192>(a, codes, dtype, grid, s); break;
+        case 256: rotary_codes<256>(a, codes, dtype, grid, s); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ac

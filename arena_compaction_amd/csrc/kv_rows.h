@@ -33,8 +33,10 @@ __device__ inline Seq sequence(const KvAttend &a, uint32_t b, bool *bad) {
     return s;
 }
 
-// Pages that the rows of block rb may see (its last row sees most).
-__device__ inline int block_pages(const KvAttend &a, const Seq &s, int rb) {
+// Pages that the rows of block rb may see (its last row sees most; under a
+// mask any of them may see all).
+__device__ inline int block_pages(const KvAttend &a, const Seq &s, int rb, bool masked) {
+    if (masked) return (s.len + kKvPage - 1) / kKvPage;
     const int rows = s.count * (int)a.group;
     int last = (rb + 1) * (int)a.rows;
     last = (last < rows ? last : rows) - 1;
@@ -49,11 +51,93 @@ struct Soft {
     float m, l;
 };
 
+// The first n of a lane's 16 tokens as bits.
+__device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// What a row sees of the sequence's new tokens: words of its mask.
+struct Words {
+    uint64_t lo, hi;
+};
+// Words that hold the bits of the 16 places from `at` on; token: the row's, of
+// the call.  (Words behind the row's last one hold no new token's bit.)
+__device__ inline Words mask_words(const KvAttend &a, const Seq &s, uint64_t token, int at) {
+    const int w = at > s.had ? (at - s.had) / 64 : 0, last = (int)a.mask_words - 1;
+    const uint64_t *row = a.mask + token * a.mask_words;
+    return Words{row[w < last ? w : last], row[w + 1 < last ? w + 1 : last]};
+}
+// Bits of these places that the row sees (all before the new tokens).
+__device__ inline uint32_t mask_bits(const Words &x, const Seq &s, int at) {
+    const int off = at - s.had;
+    uint64_t bits = 0xFFFFu;
+    if (off >= 0) {
+        bits = x.lo >> (off & 63);
+        if (off & 63) bits |= x.hi << (64 - (off & 63));
+    } else if (off > -16) {
+        bits = x.lo << -off | ((1u << -off) - 1u);
+    }
+    return (uint32_t)bits & first_bits(s.len - at);
+}
+
+// Scores (in powers of two) that the row does not see.
+__device__ inline void hide(f32x4 (&w)[4], uint32_t bits) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (!((bits >> i) & 1)) w[i / 4][i % 4] = KV_NEG_INF;
+}
+
+// Sums over codes to scores in powers of two, with the terms: f scales them,
+// slope is that of the row's head times log2(e) and far the position of the
+// lane's i-th token less that of the row's.
+//   c tanh(v / c) = v (1 - x^2/3 + 2 x^4/15 - 17 x^6/315 + 62 x^8/2835 - ...),
+// x = v / c, is used below 1/4, where what is left out is 2^-26 of it; above,
+// c - 2 c / (2^(2 v log2(e) / c) + 1), whose error is some 2^-23 of c.  Most
+// pages' scores are all below: the exponents are only made where one is not.
+template <typename Far>
+__device__ inline void term_scores(const KvAttend &a, f32x4 (&w)[4], float f, float slope, Far far) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i / 4][i % 4] *= f;
+    if (a.score_cap != 0.0f) {
+        const float c = a.score_cap * kLog2e, inv = 1.0f / c;
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(w[i / 4][i % 4]));
+        const bool high = __builtin_amdgcn_ballot_w64(most * inv >= 0.25f) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = w[i / 4][i % 4], x = v * inv, y = x * x;
+            float z = __builtin_fmaf(y, 62.0f / 2835, -17.0f / 315);
+            z = __builtin_fmaf(z, y, 2.0f / 15);
+            z = __builtin_fmaf(z, y, -1.0f / 3);
+            z = __builtin_fmaf(z * y, v, v);
+            if (high) {
+                const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
+                const float t = __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(e + 1.0f), c);
+                z = fabsf(x) < 0.25f ? z : t;
+            }
+            w[i / 4][i % 4] = z;
+        }
+    }
+    if (a.slopes) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(slope, far(i), w[i / 4][i % 4]);
+    }
+}
+
+// A row's slope, in powers of two, and its position, where there are slopes.
+__device__ inline void row_terms(const KvAttend &a, const Seq &s, uint32_t b, uint32_t h, int t, int hg, float &slope, int &pos) {
+    slope = 0.0f;
+    pos = s.had + t;
+    if (!a.slopes) return;
+    slope = a.slopes[h * a.group + hg] * kLog2e;
+    if (a.pos && pos >= 0) pos = a.pos[((uint64_t)b * a.c.heads + h) * a.pos_cap + pos];
+}
+
 // Scores of a page (sums over codes, in w) to exponents f * score + ev - m,
 // at most kRoom, which replace them.  `see`: how many of the lane's 16 tokens
-// the row sees, looked at where `edge` says that some row misses some.
-// Returns what the row's earlier sums are to be multiplied by (1 almost
+// the row sees, or with BITS which, looked at where `edge` says that some row
+// misses some.  Returns what the row's earlier sums are to be multiplied by (1 almost
 // always: the maximum moves only when an exponent would pass kRoom).
+template <bool BITS = false>
 __device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, bool edge, int see) {
     const bool first = s.m == KV_NEG_INF;
     const float c = (float)ei - (first ? 0.0f : s.m);
@@ -63,11 +147,15 @@ __device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, boo
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[tt][i] = __builtin_fmaf(w[tt][i], f, c);
     if (__builtin_expect(edge, 0)) {
+        if constexpr (BITS) {
+            hide(w, (uint32_t)see);
+        } else {
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+            for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (tt * 4 + i >= see) w[tt][i] = KV_NEG_INF;
+                for (int i = 0; i < 4; ++i)
+                    if (tt * 4 + i >= see) w[tt][i] = KV_NEG_INF;
+        }
     }
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
@@ -176,15 +264,15 @@ __device__ inline uint32_t only_there(uint32_t codes, int there) {
 // Puts a NaN into the sums of the rows that see a token whose value is NaN:
 // sums over a page's tokens of (the row sees it) x (its value is NaN).
 // values: the lane's first value code of the page; see: for each row tile,
-// how many of the lane's 16 tokens its row sees.
+// which of the lane's 16 tokens its row sees.
 template <int D, int R>
-__device__ inline void put_nan(const uint8_t *values, const int (&see)[R], f32x4 (&o)[R][D / 16]) {
+__device__ inline void put_nan(const uint8_t *values, const uint32_t (&see)[R], f32x4 (&o)[R][D / 16]) {
     u32x4 sees[R][2];
 #pragma unroll
     for (int rt = 0; rt < R; ++rt)
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            sees[rt][x / 4][x % 4] = (2 * x < see[rt] ? 0x3C00u : 0u) | (2 * x + 1 < see[rt] ? 0x3C000000u : 0u);
+            sees[rt][x / 4][x % 4] = (see[rt] >> (2 * x) & 1u) * 0x3C00u | (see[rt] >> (2 * x + 1) & 1u) * 0x3C000000u;
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
         const u32x4 v = *reinterpret_cast<const u32x4 *>(values + dt * 16 * kKvPage);

@@ -1,0 +1,14 @@
+// kv_terms.hip -- attention over the 8-bit cache with capped scores or a distance
+// bias, and a mask or none (the kernels are
+// in kv_few.h, kv_prompt.h and kv_weigh.h).
+#include "kv_few.h"
+#include "kv_prompt.h"
+#include "kv_weigh.h"
+
+namespace ac {
+
+template hipError_t launch_kv_few<kTerms>(const KvAttend &a, int codes, int dtype, hipStream_t s);
+template hipError_t launch_kv_prompt<kTerms>(const KvAttend &a, int codes, int dtype, hipStream_t s);
+template hipError_t launch_kv_weigh<kTerms>(const KvAttend &a, int codes, int dtype, hipStream_t s);
+
+}  // namespace ac

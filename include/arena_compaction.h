@@ -495,16 +495,18 @@ int defrag_monitor(const defrag_stats_t *stats, const defrag_monitor_cfg *cfg,
  *            of the page with tokens 64 j .. 64 j + 63 of sequence b.
  * An entry that is negative, not a multiple of 32, or whose page would end
  * behind the arena is no page: its tokens are passed over (append and attend)
- * or its sequence is left alone (evict), and it is counted in *n_invalid_dev.
- * Only entries that a call reads are looked at: append's of pages that get
- * tokens, attend's of sequences with new tokens, evict's of sequences that
- * hold more than the budget.
+ * or its sequence is left alone (evict and accept), and it is counted in
+ * *n_invalid_dev.  Only entries that a call reads are looked at: append's of
+ * pages that get tokens, attend's of sequences with new tokens, evict's of
+ * sequences that hold more than the budget, accept's from the first place that
+ * changes to that of the last token kept.
  * A sequence whose length, or whose range in starts_dev, is out of range
- * counts as one, and holds (or brings) no tokens; evict leaves it alone.
+ * counts as one, and holds (or brings) no tokens; evict and accept leave it
+ * alone.
  *
- * All three calls run on the caller's stream and return at once; they
+ * All calls run on the caller's stream and return at once; they
  * allocate nothing, create no stream and may be captured into a graph.  A
- * page that append or evict writes belongs to one sequence; pages that are
+ * page that append, evict or accept writes belongs to one sequence; pages that are
  * only read may be shared.  Outputs may not overlap inputs or one another
  * (but see evict's weights and positions).  Every argument is checked on the
  * host before the first launch (DEFRAG_EINVAL, DEFRAG_EWORKSPACE).
@@ -560,6 +562,36 @@ typedef struct defrag_kv_append_args {
 
 int defrag_kv_append(const defrag_kv_append_args *args, hipStream_t stream);
 
+/* defrag_kv_append with keys that are rotated by their positions on the way,
+ * and the same tokens' queries rotated beside them.  Pair i of a token at
+ * position p turns by p * freq_dev[i] radians: (x, y) becomes (x cos - y sin,
+ * x sin + y cos).  The first rotary_dim dimensions are pairs, of (i, i +
+ * rotary_dim / 2), or with interleaved 1 of (2 i, 2 i + 1); the others stay
+ * as they are.  The rotation is computed in 64 bits, and a number is rounded
+ * once, to its code or to the queries' type; an infinity or a NaN goes by the
+ * formula, that is, reaches both numbers of its pair.  A token's position is
+ * token_pos_dev[token], or where that is NULL first_pos_dev[b] + its number
+ * (first_pos_dev NULL: its place); pos_dev gets it.  out_dev gets the queries,
+ * but not those of tokens that belong to no sequence or to one that counts as
+ * invalid; it may be q_dev where the strides are the same, else it overlaps
+ * nothing.  Its rows may not overlap one another.
+ * Limits: heads + ceil(q_heads / 8) <= 65535, tokens * q_heads <= 2^36. */
+typedef struct defrag_kv_rotary_args {
+    const defrag_kv_append_args *append;
+    const double *freq_dev;          /* rotary_dim / 2                       */
+    uint32_t rotary_dim;             /* a multiple of 8, at most dim         */
+    int32_t interleaved;             /* 0 or 1                               */
+    const int32_t *token_pos_dev;    /* tokens, or NULL                      */
+    const void *q_dev;               /* tokens x q_heads x dim, keys' type   */
+    int64_t q_row, q_head;           /* strides in elements; the last is 1   */
+    void *out_dev;                   /* the same                             */
+    int64_t out_row, out_head;
+    uint32_t q_heads;                /* 0: no queries                        */
+    uint32_t reserved;
+} defrag_kv_rotary_args;
+
+int defrag_kv_append_rotary(const defrag_kv_rotary_args *args, hipStream_t stream);
+
 /* Softmax attention of the newest tokens' queries over the cache.  lens_dev
  * counts the new tokens too (append first).  New token t of a sequence with n
  * of them sees the places 0 .. len - n + t.  Query head i reads key/value
@@ -596,6 +628,66 @@ typedef struct defrag_kv_attend_args {
 size_t defrag_kv_attend_workspace_bytes(const defrag_kv_attend_args *args);
 int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_bytes,
                      hipStream_t stream);
+
+/* defrag_kv_attend with terms beside causal softmax; each may be left out.
+ * With s = scale * q.k, in this order:
+ *   cap    : s becomes cap * tanh(s / cap)                    (0: none)
+ *   slopes : s becomes s + slopes_dev[query head] * (position of the cached
+ *            token - position of the query's); positions are pos_dev's at the
+ *            tokens' places (which append, evict and accept keep), or where
+ *            that is NULL the places themselves; they are not negative
+ *   mask   : new token t of a sequence sees every place before the new ones,
+ *            and of these the new token j where bit j % 64 of word j / 64 of
+ *            its row is set, whatever the order (NULL: 0 .. t).
+ * What a row does not see does not count, whatever it holds.  lse_dev,
+ * weight_dev and a row that sees nothing are as in defrag_kv_attend, and so
+ * are the limits; mask_words is at most 2^23. */
+typedef struct defrag_kv_terms {
+    const uint64_t *mask_dev;        /* tokens x mask_words, or NULL         */
+    uint64_t mask_words;             /* 64 * mask_words >= max_new           */
+    float cap;                       /* not negative                         */
+    uint32_t reserved;
+    const float *slopes_dev;         /* heads * group, or NULL               */
+    const int32_t *pos_dev;          /* batch x heads x pos_stride, or NULL  */
+    uint64_t pos_stride;             /* at least max_len, rounded up to 64   */
+} defrag_kv_terms;
+
+size_t defrag_kv_attend_terms_workspace_bytes(const defrag_kv_attend_args *args,
+                                              const defrag_kv_terms *terms);
+int defrag_kv_attend_terms(const defrag_kv_attend_args *args, const defrag_kv_terms *terms,
+                           void *ws_dev, size_t ws_bytes, hipStream_t stream);
+
+/* Keeps the accepted path of each sequence's drafted tokens, which are its
+ * last ones (lens_dev counts them, starts_dev tells them apart as in append):
+ * of n drafted tokens behind had others, those numbered path_dev[b *
+ * path_stride + k], k < kept_dev[b], ascending in 0 .. n - 1, move to the
+ * places had + k, and lens_out_dev[b] = had + kept_dev[b].  Weights and
+ * positions, where given, move along, from places below weight_stride.  A
+ * token that stays in its page keeps its codes.  For the keys and the values
+ * of each (page, head) that takes tokens from other pages, e is the least
+ * exponent that holds their finite numbers, and at least the page's own where
+ * it keeps a token of its own; codes of another exponent are brought to it,
+ * to the nearest, ties to even.  Places behind lens_out_dev are not written,
+ * and pages behind them are free afterwards.  A sequence whose path is not of
+ * that form counts as invalid; it is left alone, and so is one with an entry
+ * that is no page: lens_out_dev[b] is its length then.  lens_out_dev has to be
+ * memory of its own. */
+typedef struct defrag_kv_accept_args {
+    const defrag_kv_cache *cache;
+    uint64_t tokens;                 /* drafted, of all sequences            */
+    const int32_t *starts_dev;       /* batch + 1, or NULL: one a sequence   */
+    uint32_t max_new;                /* at most tokens                       */
+    uint32_t reserved;
+    const int32_t *path_dev;         /* batch x path_stride                  */
+    uint64_t path_stride;
+    const int32_t *kept_dev;         /* batch, at most path_stride           */
+    float *weight_dev;               /* batch x heads x weight_stride        */
+    int32_t *pos_dev;                /* (either may be NULL)                 */
+    uint64_t weight_stride;
+    int32_t *lens_out_dev;           /* batch                                */
+} defrag_kv_accept_args;
+
+int defrag_kv_accept(const defrag_kv_accept_args *args, hipStream_t stream);
 
 /* Keeps `budget` tokens of every (sequence, head) that holds more: first the
  * safe ones, whose position is below sink or at least next_pos - recent, then
