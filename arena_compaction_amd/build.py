@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libarena_compaction.so")
 SOURCES = ["api.cpp", "monitor.cpp", "readback.cpp", "plan.hip", "move.hip", "remap.hip",
            "publish.hip", "static.hip", "kv_api.cpp", "kv_append.hip", "kv_rotary.hip", "kv_accept.hip", "kv_attend.hip",
-           "kv_prompt.hip", "kv_finish.hip", "kv_masked.hip", "kv_terms.hip", "kv_evict.hip"]
+           "kv_prompt.hip", "kv_finish.hip", "kv_masked.hip", "kv_capped.hip", "kv_terms.hip", "kv_evict.hip"]
 ARCH = "gfx950"  # MI355X (CDNA4) only
 
 # No packed-FP32 instructions anywhere in the device code.  hipcc hands the

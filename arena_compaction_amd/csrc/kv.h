@@ -112,9 +112,12 @@ struct KvAttend {
     uint64_t pos_cap;
 };
 
-// Which terms a kernel knows: none, the mask, or all of them.
-constexpr int kPlain = 0, kMasked = 1, kTerms = 2;
-inline int kv_mode(const KvAttend &a) { return a.score_cap != 0.0f || a.slopes ? kTerms : a.mask ? kMasked : kPlain; }
+// Which terms a kernel knows: none, the mask, the mask and the cap (prompts
+// alone: few rows do not gain by it), or all of them.
+constexpr int kPlain = 0, kMasked = 1, kCapped = 2, kTerms = 3;
+inline int kv_mode(const KvAttend &a) {
+    return a.slopes ? kTerms : a.score_cap != 0.0f ? kCapped : a.mask ? kMasked : kPlain;
+}
 
 struct KvAccept {
     KvCache c;

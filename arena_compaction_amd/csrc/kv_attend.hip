@@ -62,9 +62,10 @@ namespace {
 
 template <int MODE>
 hipError_t launch_mode(const KvAttend &a, int codes, int dtype, hipStream_t s) {
-    hipError_t e = a.rows == kKvPromptRows ? launch_kv_prompt<MODE>(a, codes, dtype, s) : launch_kv_few<MODE>(a, codes, dtype, s);
+    constexpr int kOther = MODE == kCapped ? kTerms : MODE;
+    hipError_t e = a.rows == kKvPromptRows ? launch_kv_prompt<MODE>(a, codes, dtype, s) : launch_kv_few<kOther>(a, codes, dtype, s);
     if (e == hipSuccess) e = launch_kv_finish(a, dtype, s);
-    if (e == hipSuccess && a.weight && !a.scores) e = launch_kv_weigh<MODE>(a, codes, dtype, s);
+    if (e == hipSuccess && a.weight && !a.scores) e = launch_kv_weigh<kOther>(a, codes, dtype, s);
     return e;
 }
 
@@ -122,6 +123,7 @@ hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t
     switch (kv_mode(a)) {
         case kPlain: return launch_mode<kPlain>(a, codes, dtype, s);
         case kMasked: return launch_mode<kMasked>(a, codes, dtype, s);
+        case kCapped: return launch_mode<kCapped>(a, codes, dtype, s);
         default: return launch_mode<kTerms>(a, codes, dtype, s);
     }
 }

@@ -183,24 +183,27 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP, MODE>)) v
                 for (int rt = 0; rt < R; ++rt) bits[rt] = seen(rt, base);
             }
         }
-        if constexpr (MODE == kTerms) {
-#pragma unroll
-            for (int rt = 0; rt < R; ++rt) {
-                if (a.pos) {
-                    term_scores(a, w[rt], f, slope[rt],
-                                [&](int x) { return (float)((int)key_pos[x / 4][x % 4] - row_pos[rt]); });
-                } else {
-                    const float first = (float)(base + g * 16 - row_pos[rt]);
-                    term_scores(a, w[rt], f, slope[rt], [&](int x) { return first + (float)x; });
-                }
-                if (edge) hide(w[rt], bits[rt]);
-            }
-        } else if constexpr (MODE == kMasked && KEEP) {
+        // sums to scores + c
+        [[maybe_unused]] auto terms = [&](int rt, float c) __attribute__((always_inline)) {
+            term_scores(a, w[rt], f, slope[rt], row_pos[rt], base + g * 16, [&](int x) { return (int)key_pos[x / 4][x % 4]; }, c);
+            if (edge) hide(w[rt], bits[rt]);
+        };
+        constexpr bool kDone = MODE != kPlain && KEEP;  // w holds scores of what is seen
+        if constexpr (kDone && MODE == kTerms) {
+            terms(0, 0.0f);
+        } else if constexpr (kDone) {
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) w[0][tt] = w[0][tt] * f;
             if (edge) hide(w[0], bits[0]);
         }
-        constexpr bool kDone = MODE == kTerms || (MODE == kMasked && KEEP);  // w holds scores of what is seen
+        // (the terms that are not kept are made below; the next page's
+        // positions would overwrite this one's)
+        [[maybe_unused]] float fades[R];
+        if constexpr (MODE == kTerms && !KEEP) {
+#pragma unroll
+            for (int rt = 0; rt < R; ++rt)
+                fades[rt] = soft_step(soft[rt], w[rt], ei, [&](float c) __attribute__((always_inline)) { terms(rt, c); });
+        }
         get_keys(next);
         if constexpr (KEEP) {
             float *to = a.scores + ((uint64_t)b * a.c.heads + h) * a.score_pages * a.score_rows * kKvPage;
@@ -215,7 +218,9 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP, MODE>)) v
 #pragma unroll
         for (int rt = 0; rt < R; ++rt) {
             float fade;
-            if constexpr (kDone)
+            if constexpr (MODE == kTerms && !KEEP)
+                fade = fades[rt];
+            else if constexpr (kDone)
                 fade = soft_scores(soft[rt], w[rt], 1.0f, ei, false, 0);
             else if constexpr (MODE == kMasked)
                 fade = soft_scores<true>(soft[rt], w[rt], f, ei, edge, (int)bits[rt]);

@@ -34,7 +34,7 @@ template <int D>
 constexpr int kPromptWaves = D <= 128 ? 4 : 8;
 
 template <int D, int CODES, int DTYPE, int MODE>
-__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && DTYPE == kBf16 && MODE == kPlain ? 3 : 2) void k_kv_prompt(
+__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && ((CODES == kE4m3 && DTYPE == kBf16 && MODE == kPlain) || MODE == kMasked) ? 3 : 2) void k_kv_prompt(
     KvAttend a) {
     constexpr int kN = kPromptWaves<D>, kRows = (int)kKvPromptRows, R = kRows / 16 / kN;
     constexpr int kSteps = D / 32, kTiles = D / 16;
@@ -44,6 +44,8 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
     constexpr int kChunks = (D + 63) / 64, kKeyJobs = (4 * kChunks + kN - 1) / kN, kValueJobs = (kTiles + kN - 1) / kN;
     __shared__ u32x4 sm_k[2][4 * kSteps * 64], sm_v[2][kTiles * 2 * 64];
     __shared__ int sm_nan;
+    __shared__ uint64_t sm_vis[MODE != kPlain ? kN : 1];
+    __shared__ int sm_seen[2][MODE != kPlain ? kN : 1];
     __shared__ int sm_pos[MODE == kTerms ? 2 : 1][MODE == kTerms ? kKvPage : 1];  // positions of the pages' tokens
     const uint32_t units = a.c.batch * a.c.heads, block = block_number();
     if (block >= units * a.row_blocks * a.splits) return;
@@ -62,8 +64,55 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
     const int per = (int)a.per_split;
     const int active = pages > per ? (pages + per - 1) / per : 1;
     if (split >= active) return;
-    const int p_lo = split * per, p_hi = p_lo + per < pages ? p_lo + per : pages;
-    const bool counts = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows && tid == 0;  // once a page
+    int p_lo = split * per, p_hi = p_lo + per < pages ? p_lo + per : pages;
+    const bool speaks = a.c.n_invalid && h == 0 && (rb + 1) * kRows >= rows;  // once a page
+    const bool counts = speaks && !masked && tid == 0;
+    if constexpr (MODE != kPlain) {
+        if (masked && speaks) {
+            for (int p = p_lo + tid; p < p_hi; p += kN * 64)
+                if (page_offset(a.c, b, p) == kNoPage) atomicAdd(a.c.n_invalid, 1ull);
+        }
+        // With few places before the new tokens, the pages from the first to
+        // the last that a row of the workgroup sees: of documents packed into
+        // a prompt that is one's (8200 tokens, five documents: 230 us without).
+        if (masked && s.had < kKvPage) {
+            const int words = (s.count + 63) / 64, t_first = rb * kRows / G;
+            const int t_last = ((rb + 1) * kRows < rows ? (rb + 1) * kRows - 1 : rows - 1) / G;
+            int low = 0x7FFFFFFF, high = -1;
+            for (int w = lane; w < words; w += 64) {
+                uint64_t x = 0;
+                for (int t0 = t_first + wave; t0 <= t_last; t0 += 8 * kN) {  // 8 rows at a time, the last one again
+                    uint64_t y[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int t = t0 + u * kN;
+                        y[u] = a.mask[(s.first + (t <= t_last ? t : t_last)) * a.mask_words + w];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) x |= y[u];
+                }
+                if (w == words - 1 && s.count % 64) x &= (1ull << s.count % 64) - 1;
+                low = x && w < low ? w : low;
+                high = x && w > high ? w : high;
+            }
+            low = least_of(low);
+            high = most_of(high);
+            if (lane == 0) {
+                sm_seen[0][wave] = low;
+                sm_seen[1][wave] = high;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                low = sm_seen[0][k] < low ? sm_seen[0][k] : low;
+                high = sm_seen[1][k] > high ? sm_seen[1][k] : high;
+            }
+            const int64_t from = high < 0 || s.had > 0 ? 0 : s.had + low * 64ll, to = high < 0 ? s.had : s.had + high * 64ll + 64;
+            const int first_page = from > 0 ? (int)(from / kKvPage) : 0, end_page = to > 0 ? (int)((to + kKvPage - 1) / kKvPage) : 0;
+            p_lo = first_page > p_lo ? first_page : p_lo;
+            p_hi = end_page < p_hi ? end_page : p_hi;
+        }
+    }
 
     const int first = rb * kRows + wave * 16 * R;  // the wave's rows
     u32x4 q[R][kSteps];
@@ -231,7 +280,40 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
                 highest = most_of(off == kNoPage ? -kNoExp : exp_here);
             }
         }
-        const uint64_t good = there & __builtin_amdgcn_ballot_w64(exp_here >= from && exp_here <= from + kBand);
+        uint64_t good = there & __builtin_amdgcn_ballot_w64(exp_here >= from && exp_here <= from + kBand);
+        if constexpr (MODE != kPlain) {
+            // pages that no row of the workgroup sees are left out: a page a
+            // lane, the tokens of the workgroup's rows over the waves
+            if (masked && (p0 + 64) * kKvPage > s.had) {
+                const int at = (p0 + lane) * kKvPage, off = at - s.had, words = (int)a.mask_words;
+                const int t_last = ((rb + 1) * kRows < rows ? (rb + 1) * kRows - 1 : rows - 1) / G;
+                uint64_t any = off < 0 ? 1u : 0u;
+                if (off >= 0 && off / 64 < words && lane < np) {
+                    const uint64_t *word = a.mask + off / 64;
+                    const int more = off / 64 + 1 < words ? 1 : 0, sh = off % 64;
+                    for (int t0 = rb * kRows / G + wave; t0 <= t_last; t0 += 4 * kN) {
+                        uint64_t x[4], y[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = t0 + u * kN;
+                            const uint64_t *row = word + (s.first + (t <= t_last ? t : t_last)) * (uint64_t)words;
+                            x[u] = row[0];
+                            y[u] = row[more];
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) any |= x[u] >> sh | (sh ? y[u] << (64 - sh) : 0);
+                    }
+                }
+                const uint64_t vis = __builtin_amdgcn_ballot_w64(any != 0);
+                if (lane == 0) sm_vis[wave] = vis;
+                __syncthreads();
+                uint64_t all = 0;
+#pragma unroll
+                for (int k = 0; k < kN; ++k) all |= sm_vis[k];
+                good &= all;
+                __syncthreads();
+            }
+        }
         // page i is summed from LDS while the next one's codes, loaded two
         // pages before, are brought to 16 bits, and a third page's are loaded
         uint64_t todo = good;
@@ -241,6 +323,20 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
             return i;
         };
         int i = take(), next = take(), after = -1;
+        // what the wave's rows see of a page under a mask, 64 tokens a row:
+        // words that hold the first and the last of them, one a lane, loaded
+        // a page ahead
+        [[maybe_unused]] uint64_t word_ahead = 0;
+        auto load_word = [&](int page) __attribute__((always_inline)) -> uint64_t {
+            const int off = (p0 + page) * kKvPage - s.had;
+            if (off <= -kKvPage) return 0;
+            const int r = first + lane % (16 * R), last_word = (int)a.mask_words - 1;
+            const int w = (off < 0 ? 0 : off / 64) + (lane / (16 * R) == 1 ? 1 : 0);
+            return a.mask[(s.first + (r < rows ? r / G : 0)) * a.mask_words + (w < last_word ? w : last_word)];
+        };
+        if constexpr (MODE != kPlain) {
+            if (masked && i >= 0) word_ahead = load_word(i);
+        }
         if (i >= 0) {
             load(i, ra);
             load(next >= 0 ? next : i, rz);
@@ -255,7 +351,30 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
             after = take();
             load(after >= 0 ? after : i, then);
             if (next >= 0) clean(next, now);
-            if (base < most) {
+            [[maybe_unused]] uint64_t mine = ~0ull;  // of row lane % (16 R)
+            bool any = base < most, edge = base + kKvPage > least;
+            if constexpr (MODE != kPlain) {
+                if (masked && edge) {
+                    const int off = base - s.had, left = s.len - base;
+                    const uint64_t lo = word_ahead;
+                    const uint64_t hi = (uint64_t)__builtin_amdgcn_ds_bpermute((lane % (16 * R) + 16 * R) * 4, (int)(uint32_t)lo) & 0xFFFFFFFFu;
+                    const uint64_t hi2 = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute((lane % (16 * R) + 16 * R) * 4, (int)(lo >> 32));
+                    const uint64_t second = hi | hi2 << 32;
+                    if (off >= 0) {
+                        mine = lo >> (off & 63);
+                        if (off & 63) mine |= second << (64 - (off & 63));
+                    } else if (off > -64) {
+                        mine = lo << -off | ((1ull << -off) - 1);
+                    }
+                    if (left < 64) mine &= (1ull << left) - 1;
+                    if (first + lane % (16 * R) >= rows) mine = 0;
+                    const uint64_t of_rows = 16 * R == 64 ? ~0ull : (1ull << (16 * R % 64)) - 1;
+                    any = any && (__builtin_amdgcn_ballot_w64(mine != 0) & of_rows);
+                    edge = (__builtin_amdgcn_ballot_w64(mine != ~0ull) & of_rows) != 0;
+                }
+                if (masked && next >= 0) word_ahead = load_word(next);
+            }
+            if (any) {
                 const float f = a.scale * kLog2e * lane_f32(scales[0], i);
                 const int ei = value_exp(lane_f32(scales[1], i));
                 // Operands are read a stage ahead of their products; nothing
@@ -298,25 +417,33 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && CODES == kE4m3 && 
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 float fade[R];
-                const bool edge = base + kKvPage > least;
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
                     if constexpr (MODE == kPlain) {
                         fade[rt] = soft_scores(soft[rt], w[rt], f, ei, edge, lim[rt] - base - g * 16);
                     } else {
                         uint32_t bits = 0xFFFFu;
-                        if (edge) bits = seen(rt, base);
+                        if (edge) {
+                            if (masked) {
+                                const int from = (rt * 16 + n) * 4;
+                                const uint32_t lo = __builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)mine);
+                                const uint32_t hi = __builtin_amdgcn_ds_bpermute(from, (int)(mine >> 32));
+                                bits = ((g & 2 ? hi : lo) >> (g & 1 ? 16 : 0)) & 0xFFFFu;
+                            } else {
+                                bits = first_bits(lim[rt] - base - g * 16);
+                            }
+                        }
                         if constexpr (MODE == kMasked) {
                             fade[rt] = soft_scores<true>(soft[rt], w[rt], f, ei, edge, (int)bits);
                         } else {
-                            if (a.pos) {
-                                const int *from = &sm_pos[cur][g * 16];
-                                term_scores(a, w[rt], f, slope[rt], [&](int x) { return (float)(from[x] - row_pos[rt]); });
-                            } else {
-                                const float far = (float)(base + g * 16 - row_pos[rt]);
-                                term_scores(a, w[rt], f, slope[rt], [&](int x) { return far + (float)x; });
-                            }
-                            fade[rt] = soft_scores<true>(soft[rt], w[rt], 1.0f, ei, edge, (int)bits);
+                            fade[rt] = soft_step(soft[rt], w[rt], ei, [&](float c) __attribute__((always_inline)) {
+                                if constexpr (MODE == kTerms)
+                                    term_scores(a, w[rt], f, slope[rt], row_pos[rt], base + g * 16,
+                                                [&](int x) { return sm_pos[cur][g * 16 + x]; }, c);
+                                else
+                                    cap_scores(a, w[rt], f, c);
+                                if (edge) hide(w[rt], bits);
+                            });
                         }
                     }
                 }

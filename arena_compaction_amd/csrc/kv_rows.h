@@ -85,41 +85,54 @@ __device__ inline void hide(f32x4 (&w)[4], uint32_t bits) {
         if (!((bits >> i) & 1)) w[i / 4][i % 4] = KV_NEG_INF;
 }
 
-// Sums over codes to scores in powers of two, with the terms: f scales them,
-// slope is that of the row's head times log2(e) and far the position of the
-// lane's i-th token less that of the row's.
-//   c tanh(v / c) = v (1 - x^2/3 + 2 x^4/15 - 17 x^6/315 + 62 x^8/2835 - ...),
-// x = v / c, is used below 1/4, where what is left out is 2^-26 of it; above,
-// c - 2 c / (2^(2 v log2(e) / c) + 1), whose error is some 2^-23 of c.  Most
-// pages' scores are all below: the exponents are only made where one is not.
-template <typename Far>
-__device__ inline void term_scores(const KvAttend &a, f32x4 (&w)[4], float f, float slope, Far far) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i / 4][i % 4] *= f;
+// Sums over codes w to w * f, capped, + add, in powers of two.
+//   c tanh(x) = c - 2 c / (2^(2 x log2(e)) + 1)
+// is off by up to 2^-22 of c, no more than 2^-19 of a score from c / 8 on: pages
+// without any go by c x + c x^3 (a1 + a2 x^2), with the a that leave least,
+// 2^-27 of it.  (The first costs a prompt an eighth of its time: chunks of 2000
+// tokens x 32 heads of 128 279 us for 246.  A series that reaches to 9/16, so
+// that few pages need exponents, took 307.)
+__device__ inline void cap_scores(const KvAttend &a, f32x4 (&w)[4], float f, float add) {
     if (a.score_cap != 0.0f) {
-        const float c = a.score_cap * kLog2e, inv = 1.0f / c;
+        const float c = a.score_cap * kLog2e, by = f * (1.0f / c);
         float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(w[i / 4][i % 4]));
-        const bool high = __builtin_amdgcn_ballot_w64(most * inv >= 0.25f) != 0;
+        if (__builtin_amdgcn_ballot_w64(!(most * fabsf(by) < 0.125f))) {
+            const float by2 = by * (2.0f * kLog2e), top = c + add;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float v = w[i / 4][i % 4], x = v * inv, y = x * x;
-            float z = __builtin_fmaf(y, 62.0f / 2835, -17.0f / 315);
-            z = __builtin_fmaf(z, y, 2.0f / 15);
-            z = __builtin_fmaf(z, y, -1.0f / 3);
-            z = __builtin_fmaf(z * y, v, v);
-            if (high) {
-                const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
-                const float t = __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(e + 1.0f), c);
-                z = fabsf(x) < 0.25f ? z : t;
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(w[i / 4][i % 4] * by2);
+                w[i / 4][i % 4] = __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(e + 1.0f), top);
             }
-            w[i / 4][i % 4] = z;
-        }
-    }
-    if (a.slopes) {
+        } else {
+            const float a1 = c * -0.333327708f, a2 = c * 0.132167363f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(slope, far(i), w[i / 4][i % 4]);
+            for (int i = 0; i < 16; ++i) {
+                const float v = w[i / 4][i % 4], x = v * by, y = x * x;
+                w[i / 4][i % 4] = __builtin_fmaf(__builtin_fmaf(a2, y, a1), y * x, __builtin_fmaf(v, f, add));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(w[i / 4][i % 4], f, add);
+    }
+}
+
+// The same plus slope * (position of the lane's i-th token - the row's): slope
+// is that of the row's head times log2(e); positions are key_pos(i), or where
+// there are none the places, from `place` on.
+template <typename Pos>
+__device__ inline void term_scores(const KvAttend &a, f32x4 (&w)[4], float f, float slope, int row_pos, int place, Pos key_pos,
+                                   float add) {
+    cap_scores(a, w, f, a.pos ? add : __builtin_fmaf(slope, (float)(place - row_pos), add));
+    if (!a.slopes) return;
+    if (a.pos) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(slope, (float)(key_pos(i) - row_pos), w[i / 4][i % 4]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(slope, (float)i, w[i / 4][i % 4]);
     }
 }
 
@@ -132,31 +145,15 @@ __device__ inline void row_terms(const KvAttend &a, const Seq &s, uint32_t b, ui
     if (a.pos && pos >= 0) pos = a.pos[((uint64_t)b * a.c.heads + h) * a.pos_cap + pos];
 }
 
-// Scores of a page (sums over codes, in w) to exponents f * score + ev - m,
-// at most kRoom, which replace them.  `see`: how many of the lane's 16 tokens
-// the row sees, or with BITS which, looked at where `edge` says that some row
-// misses some.  Returns what the row's earlier sums are to be multiplied by (1 almost
+// Scores of a page (in w) to exponents, at most kRoom, which replace them:
+// make(c) turns them to score + c, c = ev - m, and hides what is not seen.
+// Returns what the row's earlier sums are to be multiplied by (1 almost
 // always: the maximum moves only when an exponent would pass kRoom).
-template <bool BITS = false>
-__device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, bool edge, int see) {
+template <typename Make>
+__device__ inline float soft_step(Soft &s, f32x4 (&w)[4], int ei, Make make) {
     const bool first = s.m == KV_NEG_INF;
-    const float c = (float)ei - (first ? 0.0f : s.m);
     float top = KV_NEG_INF;
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[tt][i] = __builtin_fmaf(w[tt][i], f, c);
-    if (__builtin_expect(edge, 0)) {
-        if constexpr (BITS) {
-            hide(w, (uint32_t)see);
-        } else {
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (tt * 4 + i >= see) w[tt][i] = KV_NEG_INF;
-        }
-    }
+    make((float)ei - (first ? 0.0f : s.m));
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -176,6 +173,30 @@ __device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, boo
         }
     }
     return fade;
+}
+
+// The same for sums over codes, which f scales.  `see`: how many of the lane's
+// 16 tokens the row sees, or with BITS which, looked at where `edge` says that
+// some row misses some.
+template <bool BITS = false>
+__device__ inline float soft_scores(Soft &s, f32x4 (&w)[4], float f, int ei, bool edge, int see) {
+    return soft_step(s, w, ei, [&](float c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[tt][i] = __builtin_fmaf(w[tt][i], f, c);
+        if (__builtin_expect(edge, 0)) {
+            if constexpr (BITS) {
+                hide(w, (uint32_t)see);
+            } else {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (tt * 4 + i >= see) w[tt][i] = KV_NEG_INF;
+            }
+        }
+    });
 }
 
 // Weights of 8 of the lane's tokens as the operand of a product over 32

@@ -18,12 +18,17 @@ __device__ inline bool piece_tiles(const KvAttend &a, const Seq &s, int base, in
     return *first < *end;
 }
 
+// Waves of a workgroup: with terms never 16, whose 128 registers would spill.
+template <int D, int MODE>
+constexpr int kWeighWaves = MODE == kPlain ? (int)kv_weigh_waves(D) : 8;
+
 template <int D, int CODES, int DTYPE, int MODE>
-__global__ __launch_bounds__(kv_weigh_waves(D) * 64) void k_kv_weigh(KvAttend a) {
-    constexpr int kSteps = D / 32, kN = (int)kv_weigh_waves(D);
+__global__ __launch_bounds__((kWeighWaves<D, MODE>)*64) void k_kv_weigh(KvAttend a) {
+    constexpr int kSteps = D / 32, kN = kWeighWaves<D, MODE>;
     constexpr int kPieces = D / 8, kPitch = kPieces + 1;  // of 16 bytes; odd, so that rows start in other banks
     __shared__ float sm[kN][kKvPage];
     __shared__ u32x4 sm_q[kN][16 * kPitch];
+    __shared__ int sm_pos[MODE == kTerms ? kKvPage : 1];  // positions of the page's tokens
     // the last rows first: every page's rows end there, so that workgroups
     // that start together read the same queries
     const uint32_t units = a.c.heads * a.c.batch, block = block_number();
@@ -53,17 +58,11 @@ __global__ __launch_bounds__(kv_weigh_waves(D) * 64) void k_kv_weigh(KvAttend a)
                 kk[tt][st] = widen8<CODES, DTYPE>(x[0], x[1]);
             }
     }
-    // positions of the lane's 16 tokens, and which words of a row's mask it takes
-    [[maybe_unused]] int key_pos[MODE == kTerms ? 16 : 1];
     const bool masked = MODE != kPlain && a.mask != nullptr, page_edge = base + kKvPage > s.had;
     if constexpr (MODE == kTerms) {
         if (a.slopes && a.pos) {
-            const int32_t *from = a.pos + ((uint64_t)b * a.c.heads + h) * a.pos_cap + base + g * 16;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) key_pos[i] = from[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) key_pos[i] = base + g * 16 + i;
+            if (tid < kKvPage) sm_pos[tid] = a.pos[((uint64_t)b * a.c.heads + h) * a.pos_cap + base + tid];
+            __syncthreads();
         }
     }
     float acc[16] = {};
@@ -161,9 +160,7 @@ __global__ __launch_bounds__(kv_weigh_waves(D) * 64) void k_kv_weigh(KvAttend a)
             for (int st = 0; st < kSteps; ++st) w[tt] = mfma16<DTYPE>(kk[tt][st], qq[st], w[tt]);
         }
         if constexpr (MODE == kTerms) {
-            term_scores(a, w, f, slope_now, [&](int i) { return (float)(key_pos[i] - pos_now); });
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i / 4][i % 4] -= now.x;
+            term_scores(a, w, f, slope_now, pos_now, base + g * 16, [&](int i) { return sm_pos[g * 16 + i]; }, -now.x);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __builtin_fmaf(w[i / 4][i % 4], f, -now.x);
@@ -223,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_add(KvAttend a) {
 
 template <int MODE, int D, int CODES>
 void weigh_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid = grid_of(kv_weigh_blocks(a.score_pages, a.weigh_pieces, a.c.heads, a.c.batch)), block(kv_weigh_waves(D) * 64);
+    const dim3 grid = grid_of(kv_weigh_blocks(a.score_pages, a.weigh_pieces, a.c.heads, a.c.batch)), block(kWeighWaves<D, MODE> * 64);
     if (dtype == kBf16)
         hipLaunchKernelGGL((k_kv_weigh<D, CODES, kBf16, MODE>), grid, block, 0, s, a);
     else

@@ -36,8 +36,10 @@ def attend(cache, lens, q, group, counts, scale, mask=None, cap=0.0, slopes=None
 
     The bounds, beyond those of kv_plain.attend for a score s and its products'
     magnitudes: the cap changes no error for the worse (its slope is at most 1)
-    and adds 2^-19 of its result (2^-21 of the cap where that is below four
-    times the result, else a series with 2^-21 of it); the bias has a slope
+    and adds 2^-21 of its result where that comes from a series, and some 2^-22
+    of the cap where it comes from exponents (a power of at most 2^-23, of an
+    exponent rounded by 2^-23 of itself, a sum and a quotient by 2^-23, times at
+    most one cap), with the shift by the running maximum 2^-21 of it; the bias has a slope
     rounded twice and a product, 2^-21 of it; the sum and the running maximum's
     subtraction round by 2^-22 of the score and of the largest.  With d_j the
     error of s_j, that of a weight p_j is d_j + sum_k p_k d_k, to first order;
@@ -54,6 +56,9 @@ def attend(cache, lens, q, group, counts, scale, mask=None, cap=0.0, slopes=None
         had = n - t
         for h in range(H):
             k, v, ok = cache.numbers(b, n, h)
+            # whether any score of these rows is high; all others may then go by exponents too
+            raw = torch.einsum("tgd,nd->tgn", q[at: at + t, h * group: (h + 1) * group].double(), k) * scale
+            high = bool(cap) and bool((raw.abs() >= 0.12 * cap).any())
             for g in range(group):
                 hg = h * group + g
                 if n == 0 or t == 0:
@@ -73,7 +78,7 @@ def attend(cache, lens, q, group, counts, scale, mask=None, cap=0.0, slopes=None
                 d = mag * ((D + 4) * 2.0 ** -24) + mag * 2.0 ** -22 + 2.0 ** -22
                 if cap:
                     s = cap * torch.tanh(s / cap)
-                    d = d + s.abs() * 2.0 ** -19
+                    d = d + s.abs() * 2.0 ** -21 + cap * 2.0 ** -21 * high
                 if slopes is not None:
                     where = pos[b, h, :n].double() if pos is not None else torch.arange(n).double()
                     mine = had + torch.arange(t)
