@@ -76,6 +76,7 @@ struct KvRotary : KvAppend {
     uint16_t *q_out;
     int64_t o_row, o_head;
     uint32_t q_heads;
+    uint32_t lanes;            // of a workgroup
 };
 constexpr uint32_t kRotaryHeads = 8;  // query heads of a workgroup
 

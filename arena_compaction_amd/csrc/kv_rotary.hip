@@ -10,9 +10,9 @@ namespace {
 template <int D, int CODES>
 void rotary_go(const KvRotary &a, int dtype, dim3 grid, hipStream_t s) {
     if (dtype == kBf16)
-        hipLaunchKernelGGL((k_kv_append<D, CODES, kBf16, true>), grid, dim3(2 * D), 0, s, a);
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kBf16, true>), grid, dim3(a.lanes), 0, s, a);
     else
-        hipLaunchKernelGGL((k_kv_append<D, CODES, kFp16, true>), grid, dim3(2 * D), 0, s, a);
+        hipLaunchKernelGGL((k_kv_append<D, CODES, kFp16, true>), grid, dim3(a.lanes), 0, s, a);
 }
 
 template <int D>
@@ -25,7 +25,11 @@ void rotary_codes(const KvRotary &a, int codes, int dtype, dim3 grid, hipStream_
 
 }  // namespace
 
-hipError_t launch_kv_append_rotary(const KvRotary &a, int codes, int dtype, hipStream_t s) {
+hipError_t launch_kv_append_rotary(const KvRotary &call, int codes, int dtype, hipStream_t s) {
+    KvRotary a = call;
+    // A wave takes up to 4 tokens (of 256 dimensions 2 quads and so 5, where
+    // they begin in a quad's last place).
+    a.lanes = a.max_new <= 4 ? 64 : 2 * a.c.dim;
     const dim3 grid(kv_append_pages(a.max_new, a.c.stride), a.c.heads + (a.q_heads + kRotaryHeads - 1) / kRotaryHeads, a.c.batch);
     switch (a.c.dim) {
         case 64: rotary_codes<64>(a, codes, dtype, grid, s); break;

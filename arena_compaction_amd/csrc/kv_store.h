@@ -75,8 +75,10 @@ constexpr int kPitch = 20;  // dwords of a value row in LDS: 16 and a gap, so th
 // (blockIdx.y) rotate queries (kv_turn.h).
 template <int D, int CODES, int DTYPE, bool ROTARY>
 __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, KvRotary, KvAppend> a) {
-    constexpr int kN = 2 * D, kPer = D / 8;  // lanes; pieces of 8 dimensions
-    __shared__ float red[2][kN / 64];
+    constexpr int kPer = D / 8, kWavesMost = 2 * D / 64;  // pieces of 8 dimensions
+    int lanes = 2 * D;
+    if constexpr (ROTARY) lanes = (int)a.lanes;
+    __shared__ float red[2][kWavesMost];
     __shared__ __align__(16) uint32_t turn[D * kPitch];
     const uint32_t h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x;
@@ -85,6 +87,8 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     bool bad;
     new_tokens(a.starts, a.tokens, a.max_new, b, &first, &count, &bad);
     const int64_t len = a.c.lens[b];
+    [[maybe_unused]] int first_pos = 0;
+    if constexpr (ROTARY) first_pos = a.first_pos ? a.first_pos[b] : (int)len;
     const bool fits = len >= 0 && len + count <= (int64_t)(a.c.stride * kKvPage);
     if (bad || !fits) {  // nothing of this sequence is written
         if (a.c.n_invalid && blockIdx.x == 0 && h == 0 && tid == 0) atomicAdd(a.c.n_invalid, 1ull);
@@ -97,7 +101,7 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     if (hi <= lo) return;
     if constexpr (ROTARY) {
         if (h >= a.c.heads) {
-            turn_queries<D, DTYPE>(a, (h - a.c.heads) * kRotaryHeads, b, (int64_t)first + base + lo - len, hi - lo,
+            turn_queries<D, DTYPE>(a, lanes, (h - a.c.heads) * kRotaryHeads, first_pos, (int64_t)first + base + lo - len, hi - lo,
                                    base + lo - len);
             return;
         }
@@ -119,15 +123,28 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     [[maybe_unused]] Lane8 at{};
     u32x4 k[4], v[4];
     float km = 0.0f, vm = 0.0f;
-    if constexpr (ROTARY) at = lane8(a, tid % kPer);
+    [[maybe_unused]] int position[4];
+    // Rotated keys are taken a token and 8 dimensions a lane, up to four tokens
+    // one after the other, lanes / kPer apart, so that few tokens leave the
+    // other turns out: a turn makes four sines and cosines.
+    [[maybe_unused]] const int slots = lanes / kPer, slot = tid / kPer;
+    if constexpr (ROTARY) {
+        at = lane8(a, tid % kPer);
+        if (slot < slots) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = lo + slot + e * slots;
+                if (t >= hi) continue;
+                position[e] = token_position(a, first_pos, src + t, base + t - len);
+                k[e] = load_pairs(a.k + (src + t) * a.k_row + h * a.k_head, at);
+            }
+        }
+    }
     if (mine) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // for places without a new token the nearest one that has
             const int t = t0 + e < lo ? lo : t0 + e < hi ? t0 + e : hi - 1;
-            if constexpr (ROTARY)
-                k[e] = load_pairs(a.k + (src + t) * a.k_row + h * a.k_head, at);
-            else
-                k[e] = load8(a.k + (src + t) * a.k_row + h * a.k_head + d);
+            if constexpr (!ROTARY) k[e] = load8(a.k + (src + t) * a.k_row + h * a.k_head + d);
             v[e] = load8(a.v + (src + t) * a.v_row + h * a.v_head + d);
         }
     }
@@ -142,23 +159,23 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
                 if constexpr (!ROTARY) max_bits<DTYPE>(k[e][i], kb, odd_bits);
                 max_bits<DTYPE>(v[e][i], vb, odd_bits);
             }
-        if constexpr (ROTARY) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = t0 + e < lo ? lo : t0 + e < hi ? t0 + e : hi - 1;
-                turn_lane<DTYPE>(k[e], a, at, token_position(a, b, src + t, base + t - len), turned[e]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t x = __builtin_bit_cast(uint32_t, turned[e][i]) & 0x7FFFFFFFu;
-                    const bool finite = x < 0x7F800000u;
-                    km = fmaxf(km, finite ? __builtin_bit_cast(float, x) : 0.0f);
-                    odd_bits |= finite ? 0u : 1u;
-                }
-            }
-        } else {
-            km = fmaxf(to_float<DTYPE>((uint16_t)kb), to_float<DTYPE>((uint16_t)(kb >> 16)));
-        }
+        if constexpr (!ROTARY) km = fmaxf(to_float<DTYPE>((uint16_t)kb), to_float<DTYPE>((uint16_t)(kb >> 16)));
         vm = fmaxf(to_float<DTYPE>((uint16_t)vb), to_float<DTYPE>((uint16_t)(vb >> 16)));
+    }
+    if constexpr (ROTARY) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            __builtin_amdgcn_sched_barrier(0);  // one turn's registers after the other's
+            if (slot >= slots || lo + slot + e * slots >= hi) continue;
+            turn_lane<DTYPE>(k[e], a, at, position[e], turned[e]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = __builtin_bit_cast(uint32_t, turned[e][i]) & 0x7FFFFFFFu;
+                const bool finite = x < 0x7F800000u;
+                km = fmaxf(km, finite ? __builtin_bit_cast(float, x) : 0.0f);
+                odd_bits |= finite ? 0u : 1u;
+            }
+        }
     }
     const bool odd = __builtin_amdgcn_ballot_w64(odd_bits != 0) != 0;
     km = wave_max0(km);
@@ -169,7 +186,8 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kN / 64; ++w) {
+    for (int w = 0; w < kWavesMost; ++w) {
+        if (ROTARY && w * 64 >= lanes) break;
         km = fmaxf(km, red[0][w]);
         vm = fmaxf(vm, red[1][w]);
     }
@@ -187,7 +205,7 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     // 16 bytes a lane: 4 bytes a lane, as codes are made, would reach L2 in
     // pieces of 16 (four quads of tokens a wave), 22 us for a prompt's pages
     // where this takes 19.
-    const bool whole = lo == 0 && hi == kKvPage;
+    const bool whole = lo == 0 && hi == kKvPage && lanes == 2 * D;
     if (mine) {
         // dwords that also hold places outside [lo, hi) are read first: older
         // tokens in them are brought to the new scale, places behind the last
@@ -213,17 +231,11 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
             }
             *p = w;
         }
+        if constexpr (!ROTARY) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (t0 + e >= lo && t0 + e < hi) {
-                u32x2 w;
-                if constexpr (ROTARY) {
-                    const float(&y)[8] = turned[e];
-                    w[0] = codes4<CODES>(y[0], y[1], y[2], y[3], ki, odd);
-                    w[1] = codes4<CODES>(y[4], y[5], y[6], y[7], ki, odd);
-                    *reinterpret_cast<uint32_t *>(kc + (t0 + e) * D + at.d0) = w[0];
-                    *reinterpret_cast<uint32_t *>(kc + (t0 + e) * D + at.d1) = w[1];
-                } else {
+            for (int e = 0; e < 4; ++e) {
+                if (t0 + e >= lo && t0 + e < hi) {
+                    u32x2 w;
                     w[0] = codes4<CODES>(nth<DTYPE>(k[e], 0), nth<DTYPE>(k[e], 1), nth<DTYPE>(k[e], 2), nth<DTYPE>(k[e], 3),
                                          ki, odd);
                     w[1] = codes4<CODES>(nth<DTYPE>(k[e], 4), nth<DTYPE>(k[e], 5), nth<DTYPE>(k[e], 6), nth<DTYPE>(k[e], 7),
@@ -233,17 +245,27 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
             }
         }
     }
+    if constexpr (ROTARY) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = lo + slot + e * slots;
+            if (slot >= slots || t >= hi) continue;
+            const float(&y)[8] = turned[e];
+            *reinterpret_cast<uint32_t *>(kc + t * D + at.d0) = codes4<CODES>(y[0], y[1], y[2], y[3], ki, odd);
+            *reinterpret_cast<uint32_t *>(kc + t * D + at.d1) = codes4<CODES>(y[4], y[5], y[6], y[7], ki, odd);
+        }
+    }
     if (whole) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int row = (tid + i * kN) / 4, c = tid % 4;
+            const int row = (tid + i * lanes) / 4, c = tid % 4;
             *reinterpret_cast<u32x4 *>(vc + row * kKvPage + c * 16) =
                 *reinterpret_cast<const u32x4 *>(turn + row * kPitch + (c ^ (row / 16 % 4)) * 4);
         }
     }
     if (lo > 0 && kf != 1.0f) {
-        for (int i = tid; i < lo * kPer; i += kN) {
+        for (int i = tid; i < lo * kPer; i += lanes) {
             u32x2 *p = reinterpret_cast<u32x2 *>(kc) + i;
             u32x2 w = *p;
             w[0] = requant4<CODES>(w[0], kf);
@@ -253,7 +275,7 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
     }
     if (lo >= 4 && vf != 1.0f) {  // dwords of older tokens alone
         const int nq = lo / 4;
-        for (int i = tid; i < nq * D; i += kN) {
+        for (int i = tid; i < nq * D; i += lanes) {
             uint32_t *p = reinterpret_cast<uint32_t *>(vc + i / nq * kKvPage) + i % nq;
             *p = requant4<CODES>(*p, vf);
         }
@@ -262,17 +284,18 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(std::conditional_t<ROTARY, 
         sc[0] = pow2(ke);
         sc[1] = pow2(ve);
     }
-    if (tid >= lo && tid < hi) {
-        const uint64_t at = (uint64_t)base + tid;
+    for (int t = tid; t < kKvPage; t += lanes) {
+        if (t < lo || t >= hi) continue;
+        const uint64_t at = (uint64_t)base + t;
         if (at < a.cap) {
             const uint64_t i = ((uint64_t)b * a.c.heads + h) * a.cap + at;
             if (a.weight) a.weight[i] = 0.0f;
             if (a.pos) {
                 if constexpr (ROTARY)
-                    a.pos[i] = token_position(a, b, src + tid, base + tid - len);
+                    a.pos[i] = token_position(a, first_pos, src + t, base + t - len);
                 else
                     a.pos[i] = (a.first_pos ? a.first_pos[b] : (int32_t)len) +
-                               (int32_t)(base + tid - len);
+                               (int32_t)(base + t - len);
             }
         }
     }

@@ -2,10 +2,12 @@
 //
 // Pair i of a token at position p turns by the angle a = p * f_i:
 //   x' = x cos a - y sin a        y' = x sin a + y cos a
-// in 64 bits, whose result is rounded once, to a code or to the queries' type.
-// 32 bits would not do: an angle of position 100,000 has an error of 2^-8 there,
-// and a key beside the border between two codes, or a page's largest beside
-// that between two scales, would fall on either side.
+// The angle, its sine and its cosine are made in 64 bits: in 32 an angle of
+// position 100,000 would be off by 2^-8.  Keys stay in 64 bits and are rounded
+// once, to their code: beside the border between two codes, or a page's largest
+// beside that between two scales, 32 bits would fall on either side.  Queries
+// are products in 32 bits, whose rounding, 2^-23 of the pair's larger number,
+// is lost beside the one to 16 bits (2^-11 at least of the result).
 //
 // The angle is taken in turns, p * (f / 2 pi), of which only the fraction
 // counts; a quarter turn more or less swaps sine and cosine, so that their
@@ -92,26 +94,38 @@ __device__ inline u32x4 load_pairs(const uint16_t *row, const Lane8 &at) {
     return u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// The lane's 8 numbers x turned by the 4 angles, each divided by 4 (so that
-// what two numbers of the type's range add up to is still a float32), in the
-// order of x.
-template <int DTYPE>
-__device__ inline void turn8(const u32x4 &x, bool next, const double (&s)[4], const double (&c)[4], float (&y)[8]) {
-    float first[4], second[4];
+// The lane's 8 numbers x as 4 pairs, first in the low half.
+__device__ inline void pairs_of(const u32x4 &x, bool next, uint32_t (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t lo = x[i / 2], hi = x[2 + i / 2];
         const uint32_t halves = i % 2 ? lo >> 16 | (hi & 0xFFFF0000u) : (lo & 0xFFFFu) | hi << 16;
-        const uint32_t w = next ? x[i] : halves;
-        const double a = (double)to_float<DTYPE>((uint16_t)w), b = (double)to_float<DTYPE>((uint16_t)(w >> 16));
-        first[i] = to_odd(__builtin_fma(a, c[i], -(b * s[i])));
-        second[i] = to_odd(__builtin_fma(a, s[i], b * c[i]));
+        w[i] = next ? x[i] : halves;
     }
+}
+// Two results a pair in the order of x.
+__device__ inline void unpair(const float (&first)[4], const float (&second)[4], bool next, float (&y)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         y[i] = next ? (i % 2 ? second[i / 2] : first[i / 2]) : first[i];
         y[4 + i] = next ? (i % 2 ? second[2 + i / 2] : first[2 + i / 2]) : second[i];
     }
+}
+
+// The lane's 8 numbers turned by the 4 angles, each divided by 4 (so that what
+// two numbers of the type's range add up to is still a float32).
+template <int DTYPE>
+__device__ inline void turn8(const u32x4 &x, bool next, const double (&s)[4], const double (&c)[4], float (&y)[8]) {
+    uint32_t w[4];
+    float first[4], second[4];
+    pairs_of(x, next, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double a = (double)to_float<DTYPE>((uint16_t)w[i]), b = (double)to_float<DTYPE>((uint16_t)(w[i] >> 16));
+        first[i] = to_odd(__builtin_fma(a, c[i], -(b * s[i])));
+        second[i] = to_odd(__builtin_fma(a, s[i], b * c[i]));
+    }
+    unpair(first, second, next, y);
 }
 
 template <int DTYPE>
@@ -127,11 +141,10 @@ __device__ inline void turn_lane(const u32x4 &x, const KvRotary &a, const Lane8 
     }
 }
 
-// Position of the number-th new token of sequence b.
-__device__ inline int token_position(const KvRotary &a, uint32_t b, int64_t token, int64_t number) {
-    if (a.token_pos) return a.token_pos[token];
-    const uint32_t first = (uint32_t)(a.first_pos ? a.first_pos[b] : a.c.lens[b]);
-    return (int)(first + (uint32_t)number);
+// Position of a sequence's number-th new token, whose first one's is `first`
+// where they are not given one by one.
+__device__ inline int token_position(const KvRotary &a, int first, int64_t token, int64_t number) {
+    return a.token_pos ? a.token_pos[token] : (int)((uint32_t)first + (uint32_t)number);
 }
 
 // Turns the queries of count tokens, from `token` on (the number-th new one of
@@ -139,20 +152,25 @@ __device__ inline int token_position(const KvRotary &a, uint32_t b, int64_t toke
 // token in every head; where there are fewer tokens than the lanes could take,
 // the heads are dealt out too.
 template <int D, int DTYPE>
-__device__ inline void turn_queries(const KvRotary &a, uint32_t head, uint32_t b, int64_t token, int count, int64_t number) {
-    constexpr int kPer = D / 8, kSlots = 2 * D / kPer, kAhead = 4;
-    const int slot = threadIdx.x / kPer, tokens = count < kSlots ? count : kSlots, deal = kSlots / tokens;
+__device__ inline void turn_queries(const KvRotary &a, int lanes, uint32_t head, int first, int64_t token, int count, int64_t number) {
+    constexpr int kPer = D / 8, kAhead = 4;
+    const int slots = lanes / kPer, slot = threadIdx.x / kPer, tokens = count < slots ? count : slots, deal = slots / tokens;
     const int left = (int)(a.q_heads - head), heads = left < (int)kRotaryHeads ? left : (int)kRotaryHeads;
     const int mine = slot / tokens;
     if (mine >= deal) return;
     const Lane8 at = lane8(a, threadIdx.x % kPer);
     for (int t = slot % tokens; t < count; t += tokens) {
-        const int p = token_position(a, b, token + t, number + t);
+        const int p = token_position(a, first, token + t, number + t);
         const uint16_t *from = a.q + (token + t) * a.q_row + (int64_t)head * a.q_head;
         uint16_t *to = a.q_out + (token + t) * a.o_row + (int64_t)head * a.o_head;
-        double s[4], c[4];
+        float s[4], c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) quarter_sin_cos(at.f[i], p, s[i], c[i]);
+        for (int i = 0; i < 4; ++i) {
+            double ss, cc;
+            quarter_sin_cos(at.f[i], p, ss, cc);
+            s[i] = 4.0f * (float)ss;
+            c[i] = 4.0f * (float)cc;
+        }
         for (int h0 = mine; h0 < heads; h0 += kAhead * deal) {
             u32x4 x[kAhead];
 #pragma unroll
@@ -166,10 +184,18 @@ __device__ inline void turn_queries(const KvRotary &a, uint32_t head, uint32_t b
                 if (h >= heads) continue;
                 u32x2 w0 = {x[u][0], x[u][1]}, w1 = {x[u][2], x[u][3]};
                 if (at.turns) {
-                    float y[8];
-                    turn8<DTYPE>(x[u], a.next, s, c, y);
-                    w0 = u32x2{pack2<DTYPE>(4 * y[0], 4 * y[1]), pack2<DTYPE>(4 * y[2], 4 * y[3])};
-                    w1 = u32x2{pack2<DTYPE>(4 * y[4], 4 * y[5]), pack2<DTYPE>(4 * y[6], 4 * y[7])};
+                    uint32_t w[4];
+                    float one[4], two[4], y[8];
+                    pairs_of(x[u], a.next, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v0 = to_float<DTYPE>((uint16_t)w[i]), v1 = to_float<DTYPE>((uint16_t)(w[i] >> 16));
+                        one[i] = __builtin_fmaf(v0, c[i], -(v1 * s[i]));
+                        two[i] = __builtin_fmaf(v0, s[i], v1 * c[i]);
+                    }
+                    unpair(one, two, a.next, y);
+                    w0 = u32x2{pack2<DTYPE>(y[0], y[1]), pack2<DTYPE>(y[2], y[3])};
+                    w1 = u32x2{pack2<DTYPE>(y[4], y[5]), pack2<DTYPE>(y[6], y[7])};
                 }
                 __builtin_memcpy(to + h * a.o_head + at.d0, &w0, 8);
                 __builtin_memcpy(to + h * a.o_head + at.d1, &w1, 8);

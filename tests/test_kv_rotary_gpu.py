@@ -1,9 +1,11 @@
 """Appending with rotation on the GPU against plain 64-bit arithmetic.
 
 Codes, scales, positions and weights are compared exactly.  Queries are the
-64-bit result rounded once: within half a step of their type (bf16 2^-8, fp16
-2^-11 of the value, 2^-25 below fp16's normal numbers), and where positions are
-far within the 64-bit angle's own rounding, 2^-52 of it."""
+result of 32-bit products with 64-bit angles, rounded once to their type (half
+a step: bf16 2^-8, fp16 2^-11 of the value, 2^-25 below fp16's normal numbers).
+Sine and cosine are rounded to 32 bits, 2^-24, and so are a product and a sum:
+together at most 2^-22 of the pair's larger number; far positions add the
+64-bit angle's own rounding, 2^-52 of it."""
 import itertools
 
 import pytest
@@ -66,7 +68,8 @@ def check_q(got, q, pos, freq, interleaved):
     size = torch.zeros_like(want)
     size[..., :R] = q.double()[..., :R].abs().amax(-1, keepdim=True) * 2
     angle = float(pos.double().abs().max()) * float(freq.abs().max()) if len(pos) else 0.0
-    tol = want.abs() * half * (1 + 2.0 ** -20) + 2.0 ** -25 * (q.dtype == FP16) + size * (angle * 2.0 ** -52 + 2.0 ** -50)
+    near = size * (angle * 2.0 ** -52 + 2.0 ** -23)      # size is twice the larger number
+    tol = (want.abs() + near) * half + near + 2.0 ** -25 * (q.dtype == FP16)
     assert torch.equal(torch.isfinite(got), torch.isfinite(want))
     fine = torch.isfinite(want)
     assert ((got - want).abs()[fine] <= tol[fine]).all()
@@ -124,6 +127,14 @@ def test_one_token(ac, heads, group, dim, rotary, interleaved, codes, dtype):
     run(ac, lens, [1] * len(lens), heads, group, dim, rotary, interleaved, codes, dtype, 1)
 
 
+@pytest.mark.parametrize("most", [2, 3, 4, 5, 17])
+@pytest.mark.parametrize("heads,group,dim,rotary,interleaved,codes,dtype", SHAPES)
+def test_few_tokens(ac, heads, group, dim, rotary, interleaved, codes, dtype, most):
+    """Up to 4 a sequence a wave takes a head, above a workgroup; at every place in four, and over a page's end."""
+    lens = [0, 1, 2, 3, 60, 61, 62, 63, 7, 130]
+    run(ac, lens, [most, most, most, most, most, most, most, most, 1, 2], heads, group, dim, rotary, interleaved, codes, dtype, most)
+
+
 @pytest.mark.parametrize("heads,group,dim,rotary,interleaved,codes,dtype", SHAPES)
 def test_ragged(ac, heads, group, dim, rotary, interleaved, codes, dtype):
     run(ac, [0, 5, 64, 100, 7, 63], [64, 7, 0, 133, 17, 2], heads, group, dim, rotary, interleaved, codes, dtype, 2,
@@ -176,10 +187,12 @@ def test_ends_of_the_types_range(ac, dtype, size, codes):
     top = torch.finfo(dtype).max
     inside = want.abs() <= top
     step = torch.finfo(dtype).eps / 2
-    assert torch.isinf(got[want.abs() > top * (1 + step)]).all()
-    err = (got - want).abs()[inside]
+    pair = torch.maximum(q.double().abs(), torch.cat([q.double()[..., 32:], q.double()[..., :32]], -1).abs()) * 2.0 ** -22
+    assert torch.isinf(got[want.abs() - pair > top * (1 + step)]).all()
+    fine = inside & ~(torch.isinf(got) & (want.abs() + pair >= top))
+    err = (got - want).abs()[fine]
     least = torch.finfo(dtype).smallest_normal * step      # half a step of the numbers below the normal ones
-    assert (err <= want.abs()[inside] * step * (1 + 2.0 ** -20) + least).all()
+    assert (err <= (want.abs() * step + pair * (1 + step) + least)[fine]).all()
 
 
 @pytest.mark.parametrize("codes", [E4M3, INT8])
