@@ -46,6 +46,7 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP, MODE>)) v
     constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 16 * R, kJoin = 4;
     __shared__ f32x4 sm_o[kWaves][R * kJoin * 64];
     __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
+    __shared__ int sm_pos[MODE == kTerms ? kWaves : 1][MODE == kTerms ? kKvPage : 1];
     const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
     const uint32_t h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, wave = wave_uniform(tid / 64), lane = tid % 64;
@@ -109,17 +110,16 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP, MODE>)) v
     const uint8_t *strips = a.c.arena + (uint64_t)h * 2 * kKvPage * D;
     uint32_t kraw[4][D / 16];
     u32x4 vraw[kTiles];
-    // positions of the lane's tokens (where there are none, what is at hand
-    // instead: loads are never under a condition)
-    [[maybe_unused]] u32x4 key_pos[4];
+    // position of the page's token `lane`, dealt out through LDS, each wave's
+    // own (where there are none, what is at hand instead: loads are never under
+    // a condition)
+    [[maybe_unused]] int key_pos = 0;
     auto get_keys = [&](int i) __attribute__((always_inline)) {
         const uint8_t *strip = strips + lane_u64(off, i);
         load_keys<D>(strip, lane, kraw);
         if constexpr (MODE == kTerms) {
             const uint64_t at = ((uint64_t)b * a.c.heads + h) * a.pos_cap + (uint64_t)(p_lo + wave + kWaves * i) * kKvPage;
-            const int32_t *from = a.pos && a.slopes ? a.pos + at : reinterpret_cast<const int32_t *>(strip);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) __builtin_memcpy(&key_pos[x], from + g * 16 + x * 4, 16);
+            key_pos = (a.pos && a.slopes ? a.pos + at : reinterpret_cast<const int32_t *>(strip))[lane];
         }
     };
     auto get_values = [&](int i) {
@@ -185,9 +185,15 @@ __global__ __launch_bounds__(kThreads, (kWavesASimd<D, DTYPE, R, KEEP, MODE>)) v
         }
         // sums to scores + c
         [[maybe_unused]] auto terms = [&](int rt, float c) __attribute__((always_inline)) {
-            term_scores(a, w[rt], f, slope[rt], row_pos[rt], base + g * 16, [&](int x) { return (int)key_pos[x / 4][x % 4]; }, c);
+            term_scores(a, w[rt], f, slope[rt], row_pos[rt], base + g * 16, [&](int x) { return sm_pos[wave][g * 16 + x]; }, c);
             if (edge) hide(w[rt], bits[rt]);
         };
+        if constexpr (MODE == kTerms) {
+            sm_pos[wave][lane] = key_pos;
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
         constexpr bool kDone = MODE != kPlain && KEEP;  // w holds scores of what is seen
         if constexpr (kDone && MODE == kTerms) {
             terms(0, 0.0f);

@@ -79,21 +79,27 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && ((CODES == kE4m3 &
             const int words = (s.count + 63) / 64, t_first = rb * kRows / G;
             const int t_last = ((rb + 1) * kRows < rows ? (rb + 1) * kRows - 1 : rows - 1) / G;
             int low = 0x7FFFFFFF, high = -1;
-            for (int w = lane; w < words; w += 64) {
-                uint64_t x = 0;
-                for (int t0 = t_first + wave; t0 <= t_last; t0 += 8 * kN) {  // 8 rows at a time, the last one again
-                    uint64_t y[8];
+            for (int w0 = lane; w0 < words + lane; w0 += 256) {
+                uint64_t x[4] = {};  // 4 words and 4 rows at a time, the last ones again
+                for (int t0 = t_first + wave; t0 <= t_last; t0 += 4 * kN) {
+                    uint64_t y[4][4];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
+                    for (int u = 0; u < 4; ++u) {
                         const int t = t0 + u * kN;
-                        y[u] = a.mask[(s.first + (t <= t_last ? t : t_last)) * a.mask_words + w];
+                        const uint64_t *row = a.mask + (s.first + (t <= t_last ? t : t_last)) * a.mask_words;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[u][v] = row[w0 + v * 64 < words ? w0 + v * 64 : words - 1];
                     }
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) x |= y[u];
+                    for (int v = 0; v < 4; ++v) x[v] |= (y[0][v] | y[1][v]) | (y[2][v] | y[3][v]);
                 }
-                if (w == words - 1 && s.count % 64) x &= (1ull << s.count % 64) - 1;
-                low = x && w < low ? w : low;
-                high = x && w > high ? w : high;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int w = w0 + v * 64;
+                    if (w == words - 1 && s.count % 64) x[v] &= (1ull << s.count % 64) - 1;
+                    low = w < words && x[v] && w < low ? w : low;
+                    high = w < words && x[v] && w > high ? w : high;
+                }
             }
             low = least_of(low);
             high = most_of(high);
@@ -282,9 +288,11 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && ((CODES == kE4m3 &
         }
         uint64_t good = there & __builtin_amdgcn_ballot_w64(exp_here >= from && exp_here <= from + kBand);
         if constexpr (MODE != kPlain) {
-            // pages that no row of the workgroup sees are left out: a page a
-            // lane, the tokens of the workgroup's rows over the waves
-            if (masked && (p0 + 64) * kKvPage > s.had) {
+            // Behind a cached prefix pages that no row of the workgroup sees
+            // are left out here: a page a lane, the tokens of the workgroup's
+            // rows over the waves.  (Without one the range from the first to
+            // the last is known, which seldom has holes.)
+            if (masked && s.had >= kKvPage && (p0 + 64) * kKvPage > s.had) {
                 const int at = (p0 + lane) * kKvPage, off = at - s.had, words = (int)a.mask_words;
                 const int t_last = ((rb + 1) * kRows < rows ? (rb + 1) * kRows - 1 : rows - 1) / G;
                 uint64_t any = off < 0 ? 1u : 0u;
