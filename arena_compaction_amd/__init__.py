@@ -801,20 +801,26 @@ def defrag_kv_attend_terms(arena, pages, lens, q, heads: int, codes, mask=None, 
                            stream=None) -> torch.Tensor:
     """defrag_kv_attend with terms beside causal softmax.  mask: int64 [tokens,
     words], bit j % 64 of word j / 64 says that the token sees new token j of
-    its sequence (it sees all older ones); cap: scores become cap * tanh(score
+    its sequence (it sees all older ones; max_new is then at most what the words
+    hold, which is its default); cap: scores become cap * tanh(score
     / cap); slopes: float32 [query heads], times the cached token's position
     less the query's, is added to a score; pos: int32 [batch, heads, places],
     the positions (default: the places), a multiple of 64 of them and at least
     max_len."""
+    words = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+            raise ValueError("mask: int64 [tokens, words] expected")
+        words = mask.shape[1]
+        if max_new is None:
+            max_new = 64 * words
     a, out = _kv_attend_args(arena, pages, lens, q, heads, codes, starts, max_new, max_len, scale, out, lse, weight,
                              n_invalid, stream)
     dev, (tokens, q_heads, _) = arena.get_device(), q.shape
-    words = 0
     if mask is not None:
-        if not isinstance(mask, torch.Tensor) or mask.dim() != 2 or mask.shape[0] != tokens:
-            raise ValueError("mask: int64 [tokens, words] expected")
+        if mask.shape[0] != tokens:
+            raise ValueError(f"mask: {mask.shape[0]} rows of {tokens} tokens")
         _kv_ptr(mask, torch.int64, 0, dev, "mask")
-        words = mask.shape[1]
     if slopes is not None:
         _kv_ptr(slopes, torch.float32, q_heads, dev, "slopes")
     c = a.cache.contents

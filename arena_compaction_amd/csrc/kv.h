@@ -167,7 +167,8 @@ struct KvAttendPlan {
 };
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
-                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored);
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored,
+                            bool terms);  // a cap or a bias
 
 // Workgroups of the launches that follow from the plan.
 inline uint64_t kv_prompt_blocks(uint64_t splits, uint64_t row_blocks, uint64_t heads, uint64_t batch) {

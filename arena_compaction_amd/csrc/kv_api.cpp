@@ -64,19 +64,30 @@ struct Rows {
     Span span() const { return strided(p, tokens, row, heads, head, dim); }
 };
 
+// Whether intervals of x and y numbers, `apart` bytes from the one's start to
+// the other's, share any when both are repeated every `step` numbers.
+bool repeated_overlap(__int128 apart, __int128 x, __int128 y, int64_t stride) {
+    const __int128 step = stride < 0 ? -(__int128)stride : stride;
+    if (step == 0 || apart % 2) return true;
+    const __int128 at = (apart / 2 % step + step) % step;
+    return at < x || at + y > step;
+}
+
 // Whether two sets of rows share memory, or cannot be seen not to: slices of
-// one fused projection lie between one another's rows, the same stride apart.
+// one fused projection lie between one another's rows, or heads, the same
+// stride apart.
 bool rows_overlap(const Rows &a, const Rows &b) {
-    const Span x = a.span(), y = b.span();
-    if (!overlap(x, y)) return false;
-    const __int128 step = a.row < 0 ? -(__int128)a.row : a.row;
-    if (a.tokens < 2 || b.tokens < 2 || (b.row != a.row && b.row != -a.row)) return true;
-    const Span one = Rows{a.p, 1, 0, a.heads, a.head, a.dim}.span(), two = Rows{b.p, 1, 0, b.heads, b.head, b.dim}.span();
-    const __int128 wide = (__int128)one.bytes / 2, broad = (__int128)two.bytes / 2;
-    __int128 at = ((__int128)reinterpret_cast<uintptr_t>(two.p) - (__int128)reinterpret_cast<uintptr_t>(one.p)) / 2;
-    if (step == 0) return true;
-    at = (at % step + step) % step;
-    return at < wide || at + broad > step;
+    if (!overlap(a.span(), b.span())) return false;
+    const auto at = [](const Span &s) { return (__int128)reinterpret_cast<uintptr_t>(s.p); };
+    const bool same_row = a.tokens > 1 && b.tokens > 1 && (b.row == a.row || b.row == -a.row);
+    const bool same_head = a.heads > 1 && b.heads > 1 && (b.head == a.head || b.head == -a.head);
+    if (same_row) {
+        const Span x = Rows{a.p, 1, 0, a.heads, a.head, a.dim}.span(), y = Rows{b.p, 1, 0, b.heads, b.head, b.dim}.span();
+        if (!repeated_overlap(at(y) - at(x), (__int128)x.bytes / 2, (__int128)y.bytes / 2, a.row)) return false;
+    }
+    if (same_head && ((a.tokens == 1 && b.tokens == 1) || (same_row && a.head && a.row % a.head == 0)))
+        return repeated_overlap((__int128)reinterpret_cast<uintptr_t>(b.p) - (__int128)reinterpret_cast<uintptr_t>(a.p), a.dim, b.dim, a.head);
+    return true;
 }
 
 // Whether outputs overlap one another or an input.
@@ -196,15 +207,15 @@ int check_accept(const defrag_kv_accept_args *a) {
     return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
 }
 
-KvAttendPlan plan_of(const defrag_kv_attend_args *a) {
+KvAttendPlan plan_of(const defrag_kv_attend_args *a, bool terms) {
     return kv_attend_plan(a->cache->batch, a->cache->heads, a->group, a->cache->dim, a->tokens,
-                          a->max_new, a->max_len, a->weight_dev != nullptr);
+                          a->max_new, a->max_len, a->weight_dev != nullptr, terms);
 }
 
 // The plan of a call, and whether its launches fit their grids.  (Rows are
 // joined by a workgroup each at the most, where the cache is cut: fewer than
 // 2^21 of them, as kv_attend_plan cuts few rows or few workgroups.)
-int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
+int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p, bool terms = false) {
     if (!a) return DEFRAG_EINVAL;
     int rc = check_cache(a->cache);
     if (rc) return rc;
@@ -231,7 +242,7 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
     if (any_overlap(out, in)) return DEFRAG_EINVAL;
     *p = KvAttendPlan{};
     if (!a->tokens) return DEFRAG_OK;
-    *p = plan_of(a);
+    *p = plan_of(a, terms);
     if (p->rows == kKvPromptRows && kv_prompt_blocks(p->splits, p->row_blocks, c->heads, c->batch) > kMaxBlocks)
         return DEFRAG_EINVAL;
     const uint64_t pages = (a->max_len + (uint64_t)kKvPage - 1) / kKvPage;
@@ -244,9 +255,9 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p) {
 
 // The same with terms; a call without any is defrag_kv_attend's.
 int check_terms(const defrag_kv_attend_args *a, const defrag_kv_terms *t, KvAttendPlan *p) {
-    const int rc = check_attend(a, p);
-    if (rc) return rc;
     if (!t) return DEFRAG_EINVAL;
+    const int rc = check_attend(a, p, t->cap != 0.0f || t->slopes_dev);
+    if (rc) return rc;
     const defrag_kv_cache *c = a->cache;
     if (t->cap != 0.0f && !(t->cap >= kLeastCap && t->cap <= kMostCap)) return DEFRAG_EINVAL;
     if (!aligned(t->mask_dev, 8) || !aligned(t->slopes_dev, 4) || !aligned(t->pos_dev, 4)) return DEFRAG_EINVAL;

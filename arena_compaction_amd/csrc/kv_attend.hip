@@ -25,8 +25,16 @@ namespace {
 //    768     93    92   119                  342   319   383
 // and of 1000 tokens, 504 units, whole 20 us, in 3 pieces 28; with 32 rows, 504
 // units of 4096, 63 and 79; of 9000 whole and 3 pieces lie within a tenth.
-uint64_t few_splits(uint64_t units, uint64_t pages, uint32_t rows) {
+// With a cap or a bias 2 workgroups share a unit, so that 2 pieces fill them up
+// where the caches are whole otherwise; 8000 tokens, lengths down to a third,
+// with weights:
+//   units           272   320   384   448   512
+//   whole           139   145   163   173   193 us
+//   in 2 pieces     119   133   147   179   192
+// (of 4000 tokens, 384 units, 73 and 68; of 1000 27 and 30).
+uint64_t few_splits(uint64_t units, uint64_t pages, uint32_t rows, uint32_t dim, bool terms) {
     if (units == 0) return 1;
+    if (terms && dim <= 128 && units >= 256 && units < 416 && pages > 60 && pages <= 192) return 2;
     if (units >= 256) return pages <= 192 ? 1 : 3;
     return ((rows == 16 ? 1024 : 512) + units - 1) / units;
 }
@@ -72,7 +80,7 @@ hipError_t launch_mode(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 }  // namespace
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
-                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored) {
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored, bool terms) {
     KvAttendPlan p{};
     const uint64_t rows = (uint64_t)max_new * group;
     // 32 rows a wave share the codes brought to 16 bits; above 128 dimensions
@@ -81,7 +89,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows);
+    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows, dim, terms);
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave

@@ -567,14 +567,17 @@ int defrag_kv_append(const defrag_kv_append_args *args, hipStream_t stream);
  * position p turns by p * freq_dev[i] radians: (x, y) becomes (x cos - y sin,
  * x sin + y cos).  The first rotary_dim dimensions are pairs, of (i, i +
  * rotary_dim / 2), or with interleaved 1 of (2 i, 2 i + 1); the others stay
- * as they are.  The rotation is computed in 64 bits, and a number is rounded
- * once, to its code or to the queries' type; an infinity or a NaN goes by the
- * formula, that is, reaches both numbers of its pair.  A token's position is
+ * as they are.  Keys are rotated in 64 bits and rounded once, to their code;
+ * queries by products in 32 bits (of 64-bit angles), which are rounded to
+ * their type; an infinity or a NaN goes by the formula, that is, reaches both
+ * numbers of its pair.  A token's position is
  * token_pos_dev[token], or where that is NULL first_pos_dev[b] + its number
  * (first_pos_dev NULL: its place); pos_dev gets it.  out_dev gets the queries,
  * but not those of tokens that belong to no sequence or to one that counts as
  * invalid; it may be q_dev where the strides are the same, else it overlaps
- * nothing.  Its rows may not overlap one another.
+ * nothing.  Its rows may not overlap one another.  (Queries, keys and values
+ * that are slices of one projection lie between one another's rows or heads:
+ * in place queries alone are written.)
  * Limits: heads + ceil(q_heads / 8) <= 65535, tokens * q_heads <= 2^36. */
 typedef struct defrag_kv_rotary_args {
     const defrag_kv_append_args *append;
@@ -635,7 +638,8 @@ int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_
  *   slopes : s becomes s + slopes_dev[query head] * (position of the cached
  *            token - position of the query's); positions are pos_dev's at the
  *            tokens' places (which append, evict and accept keep), or where
- *            that is NULL the places themselves; they are not negative
+ *            that is NULL the places themselves; they are not negative, and
+ *            slopes are finite
  *   mask   : new token t of a sequence sees every place before the new ones,
  *            and of these the new token j where bit j % 64 of word j / 64 of
  *            its row is set, whatever the order (NULL: 0 .. t).
@@ -645,7 +649,7 @@ int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_
 typedef struct defrag_kv_terms {
     const uint64_t *mask_dev;        /* tokens x mask_words, or NULL         */
     uint64_t mask_words;             /* 64 * mask_words >= max_new           */
-    float cap;                       /* not negative                         */
+    float cap;                       /* 0, or 2^-64 to 2^64                  */
     uint32_t reserved;
     const float *slopes_dev;         /* heads * group, or NULL               */
     const int32_t *pos_dev;          /* batch x heads x pos_stride, or NULL  */

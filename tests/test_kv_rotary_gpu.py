@@ -147,6 +147,27 @@ def test_in_place_and_unaligned(ac, codes, dtype, interleaved):
     run(ac, [10, 70], [30, 16], 2, 3, 128, 64, interleaved, codes, dtype, 3, layout="unaligned", inplace=True)
 
 
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_in_place_between_other_heads(ac, tokens):
+    """A projection whose heads hold query, key and value side by side."""
+    heads, dim = 3, 64
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn(tokens, heads, 3, dim, generator=gen).to(BF16)
+    xg = x.cuda()
+    c = Cache([1], heads, dim, E4M3)
+    arena, freq, pos = c.arena.cuda(), freqs(dim), torch.arange(tokens) + 7
+    out = ac.defrag_kv_append_rotary(arena, c.pages.cuda(), ints([0]), xg[:, :, 1], xg[:, :, 2], E4M3, freq.cuda(), q=xg[:, :, 0],
+                                     q_out=xg[:, :, 0], starts=ints([0, tokens]), first_pos=ints([7]))
+    check_q(out, x[:, :, 0], pos, freq, False)
+    assert torch.equal(xg[:, :, 1:].cpu(), x[:, :, 1:])
+    c.append(0, 0, rotate(x[:, :, 1], pos, freq, False), x[:, :, 2].double())
+    assert_same_arena(c, arena)
+    for q, to in ((xg[:, :, 0], xg[:, :, 1]), (xg[:, :2, 0], xg[:, 1:, 0])):   # over the keys, over other queries
+        with pytest.raises(ac.DefragError):
+            ac.defrag_kv_append_rotary(arena, c.pages.cuda(), ints([0]), xg[:, :, 1], xg[:, :, 2], E4M3, freq.cuda(), q=q, q_out=to,
+                                       starts=ints([0, tokens]))
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_positions_by_token(ac, interleaved):
     """Depths of trees, one position for several tokens, far and negative ones."""

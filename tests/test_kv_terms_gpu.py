@@ -279,6 +279,28 @@ def test_what_is_passed_over(ac):
     assert (out == 0).all()
 
 
+def test_max_new_is_what_the_words_hold(ac):
+    """Without max_new; a sequence that brings more than the words hold counts as invalid and brings nothing."""
+    lens, counts = [100, 90], [70, 20]
+    c = Cache([2, 2], 1, 64, E4M3, fill=0x7F)
+    c.fill_random(lens, 1)
+    q = queries(90, 2, 64, BF16, 2).cuda()
+    mask = pack(masks(counts, "tree", 3), counts, 2, 90).cuda()
+    args = (c.arena.cuda(), c.pages.cuda(), ints(lens), q, 1, E4M3)
+    want = ac.defrag_kv_attend_terms(*args, mask=mask, starts=starts_of(counts), max_new=70)
+    assert torch.equal(ac.defrag_kv_attend_terms(*args, mask=mask, starts=starts_of(counts)), want)
+    bad, out = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.full_like(q, 3.0)
+    ac.defrag_kv_attend_terms(*args, mask=mask[:, :1].contiguous(), starts=starts_of(counts), out=out, n_invalid=bad)
+    # the cache may be cut elsewhere: weights rounded to float16 once more (2^-10 of the largest |v|), then a step of bf16
+    most, got = c.numbers(1, 90, 0)[1].abs().max(), out[70:].double()
+    assert int(bad) == 1 and (out[:70] == 3.0).all()
+    assert ((got - want[70:].double()).abs() <= want[70:].double().abs() * 2.0 ** -7 + most * 2.0 ** -10 * 1.01).all()
+    with pytest.raises(ac.DefragError):
+        ac.defrag_kv_attend_terms(*args, mask=mask[:, :1].contiguous(), starts=starts_of(counts), max_new=70)
+    with pytest.raises(ValueError):
+        ac.defrag_kv_attend_terms(*args, mask=mask[:5], starts=starts_of(counts), max_new=70)
+
+
 def test_stream_and_graph(ac):
     """Two calls of different kinds that share a workspace, captured and replayed with other inputs."""
     lens, counts = [1000, 700], [5, 4]
