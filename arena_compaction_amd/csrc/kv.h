@@ -24,6 +24,7 @@ namespace ac {
 constexpr int kKvPage = 64;       // tokens of a page
 constexpr int kKvExpMin = -64;    // least exponent of a scale
 constexpr uint32_t kKvPromptRows = 128;  // query rows of a workgroup over a prompt
+constexpr uint32_t kKvTreeRows = 64;     // and of one over a small tree
 
 // An axis of a grid holds fewer than 2^32 lanes, 2^22 workgroups of 1024.
 // What may need more is numbered through x, row by row of y (block_number in
@@ -116,8 +117,8 @@ struct KvAttend {
 // Which terms a kernel knows: none, the mask, the mask and the cap (prompts
 // alone: few rows do not gain by it), or all of them.
 constexpr int kPlain = 0, kMasked = 1, kCapped = 2, kTerms = 3;
-inline int kv_mode(const KvAttend &a) {
-    return a.slopes ? kTerms : a.score_cap != 0.0f ? kCapped : a.mask ? kMasked : kPlain;
+inline int kv_mode(float cap, const float *slopes, const uint64_t *mask) {
+    return slopes ? kTerms : cap != 0.0f ? kCapped : mask ? kMasked : kPlain;
 }
 
 struct KvAccept {
@@ -167,8 +168,7 @@ struct KvAttendPlan {
 };
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
-                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored,
-                            bool terms);  // a cap or a bias
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored, int mode);
 
 // Workgroups of the launches that follow from the plan.
 inline uint64_t kv_prompt_blocks(uint64_t splits, uint64_t row_blocks, uint64_t heads, uint64_t batch) {

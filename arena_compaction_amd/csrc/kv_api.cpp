@@ -207,15 +207,15 @@ int check_accept(const defrag_kv_accept_args *a) {
     return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
 }
 
-KvAttendPlan plan_of(const defrag_kv_attend_args *a, bool terms) {
+KvAttendPlan plan_of(const defrag_kv_attend_args *a, int mode) {
     return kv_attend_plan(a->cache->batch, a->cache->heads, a->group, a->cache->dim, a->tokens,
-                          a->max_new, a->max_len, a->weight_dev != nullptr, terms);
+                          a->max_new, a->max_len, a->weight_dev != nullptr, mode);
 }
 
 // The plan of a call, and whether its launches fit their grids.  (Rows are
 // joined by a workgroup each at the most, where the cache is cut: fewer than
 // 2^21 of them, as kv_attend_plan cuts few rows or few workgroups.)
-int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p, bool terms = false) {
+int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p, int mode = kPlain) {
     if (!a) return DEFRAG_EINVAL;
     int rc = check_cache(a->cache);
     if (rc) return rc;
@@ -242,8 +242,8 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p, bool terms = f
     if (any_overlap(out, in)) return DEFRAG_EINVAL;
     *p = KvAttendPlan{};
     if (!a->tokens) return DEFRAG_OK;
-    *p = plan_of(a, terms);
-    if (p->rows == kKvPromptRows && kv_prompt_blocks(p->splits, p->row_blocks, c->heads, c->batch) > kMaxBlocks)
+    *p = plan_of(a, mode);
+    if (p->rows >= kKvTreeRows && kv_prompt_blocks(p->splits, p->row_blocks, c->heads, c->batch) > kMaxBlocks)
         return DEFRAG_EINVAL;
     const uint64_t pages = (a->max_len + (uint64_t)kKvPage - 1) / kKvPage;
     if (a->weight_dev && !p->score_bytes && kv_weigh_blocks(pages, p->weigh_pieces, c->heads, c->batch) > kMaxBlocks)
@@ -256,7 +256,7 @@ int check_attend(const defrag_kv_attend_args *a, KvAttendPlan *p, bool terms = f
 // The same with terms; a call without any is defrag_kv_attend's.
 int check_terms(const defrag_kv_attend_args *a, const defrag_kv_terms *t, KvAttendPlan *p) {
     if (!t) return DEFRAG_EINVAL;
-    const int rc = check_attend(a, p, t->cap != 0.0f || t->slopes_dev);
+    const int rc = check_attend(a, p, kv_mode(t->cap, t->slopes_dev, t->mask_dev));
     if (rc) return rc;
     const defrag_kv_cache *c = a->cache;
     if (t->cap != 0.0f && !(t->cap >= kLeastCap && t->cap <= kMostCap)) return DEFRAG_EINVAL;

@@ -71,7 +71,7 @@ namespace {
 template <int MODE>
 hipError_t launch_mode(const KvAttend &a, int codes, int dtype, hipStream_t s) {
     constexpr int kOther = MODE == kCapped ? kTerms : MODE;
-    hipError_t e = a.rows == kKvPromptRows ? launch_kv_prompt<MODE>(a, codes, dtype, s) : launch_kv_few<kOther>(a, codes, dtype, s);
+    hipError_t e = a.rows > kFewRows ? launch_kv_prompt<MODE>(a, codes, dtype, s) : launch_kv_few<kOther>(a, codes, dtype, s);
     if (e == hipSuccess) e = launch_kv_finish(a, dtype, s);
     if (e == hipSuccess && a.weight && !a.scores) e = launch_kv_weigh<kOther>(a, codes, dtype, s);
     return e;
@@ -80,20 +80,26 @@ hipError_t launch_mode(const KvAttend &a, int codes, int dtype, hipStream_t s) {
 }  // namespace
 
 KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint32_t dim,
-                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored, bool terms) {
+                            uint64_t tokens, uint32_t max_new, uint32_t max_len, bool scored, int mode) {
     KvAttendPlan p{};
     const uint64_t rows = (uint64_t)max_new * group;
     // 32 rows a wave share the codes brought to 16 bits; above 128 dimensions
     // their sums would leave no registers to load ahead
     p.rows = rows > kFewRows ? kKvPromptRows : rows <= 16 || dim > 128 ? 16 : 32;
+    // Small trees: half of 128 rows would be none.  8 heads of 128, 4 query
+    // heads each, 16 sequences of 5000-10,000 tokens: 9 drafts 69 us with 64
+    // rows and 93 with 128, 16 drafts 82 and 100; 64 sequences of 1200-4000, 16
+    // drafts 103 and 138.
+    if (mode == kMasked && dim <= 128 && p.rows == kKvPromptRows && rows <= kKvTreeRows) p.rows = kKvTreeRows;
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;
     const uint64_t pages = (max_len + kKvPage - 1) / kKvPage;
-    const uint64_t splits = p.rows == kKvPromptRows ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows, dim, terms);
+    const bool many = p.rows > kFewRows;
+    const uint64_t splits = many ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows, dim, mode >= kCapped);
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave
-    if (p.rows != kKvPromptRows && per > 64 * kWaves) per = 64 * kWaves;
+    if (!many && per > 64 * kWaves) per = 64 * kWaves;
     p.per_split = (uint32_t)per;
     p.splits = (uint32_t)((pages + per - 1) / per);
     if (p.splits < 1) p.splits = 1;
@@ -128,7 +134,7 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
 }
 
 hipError_t launch_kv_attend(const KvAttend &a, int codes, int dtype, hipStream_t s) {
-    switch (kv_mode(a)) {
+    switch (kv_mode(a.score_cap, a.slopes, a.mask)) {
         case kPlain: return launch_mode<kPlain>(a, codes, dtype, s);
         case kMasked: return launch_mode<kMasked>(a, codes, dtype, s);
         case kCapped: return launch_mode<kCapped>(a, codes, dtype, s);

@@ -30,13 +30,13 @@ namespace {
 
 // 32 rows a wave; above 128 dimensions 16, whose sums and queries leave two
 // waves a SIMD their registers.
-template <int D>
-constexpr int kPromptWaves = D <= 128 ? 4 : 8;
+template <int D, int ROWS>
+constexpr int kPromptWaves = D <= 128 ? ROWS / 32 > 4 ? ROWS / 32 : 4 : 8;
 
-template <int D, int CODES, int DTYPE, int MODE>
-__global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && ((CODES == kE4m3 && DTYPE == kBf16 && MODE == kPlain) || MODE == kMasked) ? 3 : 2) void k_kv_prompt(
+template <int D, int CODES, int DTYPE, int MODE, int ROWS>
+__global__ __launch_bounds__((kPromptWaves<D, ROWS>)*64, D == 64 && ((CODES == kE4m3 && DTYPE == kBf16 && MODE == kPlain) || MODE == kMasked) ? 3 : 2) void k_kv_prompt(
     KvAttend a) {
-    constexpr int kN = kPromptWaves<D>, kRows = (int)kKvPromptRows, R = kRows / 16 / kN;
+    constexpr int kN = kPromptWaves<D, ROWS>, kRows = ROWS, R = kRows / 16 / kN;
     constexpr int kSteps = D / 32, kTiles = D / 16;
     constexpr int kBatch = kTiles % 4 ? 3 : 4, kBatches = kTiles / kBatch;  // value tiles read at a time
     // a wave's share of a page: of the keys' 4 tiles x chunks of 64 dimensions
@@ -559,13 +559,21 @@ __global__ __launch_bounds__(kPromptWaves<D> * 64, D == 64 && ((CODES == kE4m3 &
     }
 }
 
+template <int MODE, int D, int CODES, int ROWS>
+void prompt_rows(const KvAttend &a, int dtype, hipStream_t s) {
+    const dim3 grid = grid_of(kv_prompt_blocks(a.splits, a.row_blocks, a.c.heads, a.c.batch)), block(kPromptWaves<D, ROWS> * 64);
+    if (dtype == kBf16)
+        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kBf16, MODE, ROWS>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kFp16, MODE, ROWS>), grid, block, 0, s, a);
+}
+
 template <int MODE, int D, int CODES>
 void prompt_go(const KvAttend &a, int dtype, hipStream_t s) {
-    const dim3 grid = grid_of(kv_prompt_blocks(a.splits, a.row_blocks, a.c.heads, a.c.batch));
-    if (dtype == kBf16)
-        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kBf16, MODE>), grid, dim3(kPromptWaves<D> * 64), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_kv_prompt<D, CODES, kFp16, MODE>), grid, dim3(kPromptWaves<D> * 64), 0, s, a);
+    if constexpr (MODE == kMasked && D <= 128) {
+        if (a.rows == kKvTreeRows) return prompt_rows<MODE, D, CODES, (int)kKvTreeRows>(a, dtype, s);
+    }
+    prompt_rows<MODE, D, CODES, (int)kKvPromptRows>(a, dtype, s);
 }
 
 template <int MODE, int D>

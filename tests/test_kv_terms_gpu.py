@@ -166,6 +166,21 @@ def test_masks_across_words_and_pages(ac, had, group, count):
         assert check(ac, c, lens, q, group, counts, "random", words=words, seed=had + words)[1] == 0
 
 
+@pytest.mark.parametrize("dim,codes,dtype", [(64, E4M3, BF16), (64, INT8, FP16), (96, INT8, BF16), (96, E4M3, FP16), (128, E4M3, BF16),
+                                             (128, INT8, FP16), (192, E4M3, BF16)])
+@pytest.mark.parametrize("group,count", [(4, 16), (8, 5), (1, 64), (3, 11), (2, 33)])
+def test_small_trees(ac, group, count, dim, codes, dtype):
+    """33 to 66 rows a head; prefixes that are cut into pieces, and a sequence of its drafts alone."""
+    counts = [count, count, max(1, count - 3)]
+    lens = [2000 + count, count, 61 + counts[2]]
+    c = Cache([-(-n // PAGE) for n in lens], 2, dim, codes, fill=0x7F)
+    c.fill_random(lens, 6, spread=9)
+    c.pages[0, 3] = -1
+    q = queries(sum(counts) + 1, 2 * group, dim, dtype, 9, "slice")
+    for kind in ("tree", "random"):
+        assert check(ac, c, lens, q, group, counts, kind, seed=count)[1] == 1
+
+
 @pytest.mark.parametrize("count,group", [(6, 2), (50, 3)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_rows_that_see_nothing(ac, count, group, bias):
