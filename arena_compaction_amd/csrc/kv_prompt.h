@@ -18,6 +18,15 @@
 // and 22% are lost to the last rows, which see most.  With 64 dimensions the
 // vector pipe is busy for 83% (8200 tokens x 32 heads, float16: 380 us).
 //
+// Terms (kv_rows.h): a page's mask words are loaded a page ahead, one a lane,
+// and dealt out where some row misses some token; a wave whose rows see nothing
+// of a page only brings the next one to LDS.  A causal mask costs the prompt of
+// 8200 tokens 408 us for 392, five documents in it 140; a cap the chunks above
+// 286 for 244, with the vector pipe busy for 54% of the cycles.  With a distance
+// bias registers leave two waves a SIMD for 64 dimensions, where the plain
+// kernel has three: 560 us for 392, documents 200 (three, with 60 registers in
+// memory: 630 and 250).
+//
 // Workgroups of one key/value head run on one XCD where the heads are a
 // multiple of 8, so that its pages stay in that XCD's L2; the last rows,
 // which see most, start first.
@@ -74,7 +83,8 @@ __global__ __launch_bounds__((kPromptWaves<D, ROWS>)*64, D == 64 && ((CODES == k
         }
         // With few places before the new tokens, the pages from the first to
         // the last that a row of the workgroup sees: of documents packed into
-        // a prompt that is one's (8200 tokens, five documents: 230 us without).
+        // a prompt that is one's (8200 tokens, five documents: 230 us without,
+        // 221 with).
         if (masked && s.had < kKvPage) {
             const int words = (s.count + 63) / 64, t_first = rb * kRows / G;
             const int t_last = ((rb + 1) * kRows < rows ? (rb + 1) * kRows - 1 : rows - 1) / G;

@@ -2,6 +2,13 @@
 // rotated by their positions on the way (kv_turn.h), and their queries beside
 // them: the kernel is kv_store.h's, whose grid has workgroups for the queries
 // behind those of the heads.
+//
+// Prompts of 13,000 tokens, 8 heads of 128 and 32 query heads (295 MB) take 79
+// us, 3.7 TB/s where a copy reaches 4.75: the vector pipe, which makes sines and
+// cosines and turns the keys in 64 bits, is busy for 47% of the cycles, and few
+// waves (2.2 a SIMD) hide part of it.  One token of 128 sequences takes 10.6 us, of
+// which 8.5 are what appending takes (five dependent trips to memory); a
+// workgroup a head, of which one lane in 16 has a token, took 14.
 #include "kv_store.h"
 
 namespace ac {
