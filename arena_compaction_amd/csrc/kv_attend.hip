@@ -97,6 +97,12 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     const bool many = p.rows > kFewRows;
     const uint64_t splits = many ? prompt_splits(units, pages, max_new, dim) : few_splits(units, pages, p.rows, dim, mode >= kCapped);
     uint64_t per = splits ? (pages + splits - 1) / splits : pages;
+    // With terms short caches are whole: the join is a launch, and a call 4 us
+    // longer.  7 drafts, 8 heads of 128, 2 query heads each, a call (and out of a
+    // captured graph) cut and whole: 500 tokens 18.6 (11.2) and 14.3 us (9.4),
+    // 1000 18.2 (12.0) and 14.1 (12.3), 2000 18.5 (12.8) and 17.5 (17.5); of 256
+    // dimensions 760 tokens 18.7 (18.3) and 21.0 (20.9).
+    if (mode != kPlain && !many && dim <= 128 && pages <= 16) per = pages;
     if (per < kWaves) per = kWaves;
     // a lane keeps the offset of each page of its wave
     if (!many && per > 64 * kWaves) per = 64 * kWaves;

@@ -177,13 +177,18 @@ def test_terms_take_all_or_none():
     assert ac.lib.defrag_kv_attend_terms(None, ctypes.byref(_terms()), None, 0, None) == ac.DEFRAG_EINVAL
 
 
-def test_terms_and_attend_agree_on_the_workspace():
-    """Terms change no plan: the bytes that attend asks for."""
-    for sizes in (dict(group=4), dict(group=16, weight_dev=None), dict(group=4, batch=1, tokens=700, max_new=700, starts_dev=0x1000,
-                                                                       q_dev=0x4000000, out_dev=0x5000000, page_stride=64, max_len=4096)):
-        sizes = {**dict(weight_dev=0x8000000, weight_stride=4096), **sizes}
+def test_workspaces_of_attend_and_of_terms():
+    """The bytes that attend asks for, but of short caches, which terms leave whole."""
+    def both(**sizes):
+        sizes = {**dict(weight_dev=0x8000000, weight_stride=4096, page_stride=64, max_len=4096), **sizes}
         need = ac.lib.defrag_kv_attend_workspace_bytes(ctypes.byref(_args(ac.defrag_kv_attend_args, **sizes)))
-        assert need > 1 and terms_say(sizes, mask_words=11, pos_stride=4096, pos_dev=0x20000000)[0] == need
+        return need, terms_say(sizes, mask_words=11, pos_stride=4096, pos_dev=0x20000000)[0]
+    for sizes in (dict(group=4), dict(group=16, weight_dev=None), dict(group=4, max_len=1025), dict(group=4, dim=192, max_len=1024),
+                  dict(group=4, batch=1, tokens=700, max_new=700, starts_dev=0x1000, q_dev=0x4000000, out_dev=0x5000000)):
+        need, terms = both(**sizes)
+        assert need > 1 and terms == need
+    need, terms = both(group=4, max_len=1024)
+    assert 1 < terms < need
 
 
 def _accept(**change):
