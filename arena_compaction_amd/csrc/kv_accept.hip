@@ -26,6 +26,11 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 
 __device__ inline int place_page(int place) { return place / kKvPage; }
 
+// What brings a code of one exponent to another.  Only zeros and NaN come from
+// 2^128 and more above the scale that is chosen (any other code would have
+// raised it), and a zero times infinity would be no number.
+__device__ inline float to_scale(int from, int to) { return ldexpf(1.0f, from - to < 127 ? from - to : 127); }
+
 // A code times f; as it is where f is 1.
 template <int CODES>
 __device__ inline uint8_t again1(uint8_t code, float f) {
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
             const int t = i / kPer, c = i % kPer;
             u32x2 w = sm_k[i];
             if (sm_exp[0][t] != ke) {
-                const float f = ldexpf(1.0f, sm_exp[0][t] - ke);
+                const float f = to_scale(sm_exp[0][t], ke);
                 w[0] = requant4<CODES>(w[0], f);
                 w[1] = requant4<CODES>(w[1], f);
             }
@@ -180,10 +185,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
         }
         for (int i = tid; i < n * D; i += kThreads) {
             const int d = i / n, t = i - d * n;
-            vc[d * kKvPage + lo + t] = again1<CODES>(sm_v[i], ldexpf(1.0f, sm_exp[1][t] - ve));
+            vc[d * kKvPage + lo + t] = again1<CODES>(sm_v[i], to_scale(sm_exp[1][t], ve));
         }
         if (lo > 0 && ke != ke0) {
-            const float f = ldexpf(1.0f, ke0 - ke);
+            const float f = to_scale(ke0, ke);
             for (int i = tid; i < lo * kPer; i += kThreads) {
                 u32x2 *p = reinterpret_cast<u32x2 *>(kc) + i;
                 u32x2 w = *p;
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
             }
         }
         if (lo > 0 && ve != ve0) {
-            const float f = ldexpf(1.0f, ve0 - ve);
+            const float f = to_scale(ve0, ve);
             for (int i = tid; i < lo * D; i += kThreads) {
                 uint8_t *p = vc + i / lo * kKvPage + i % lo;
                 *p = again1<CODES>(*p, f);

@@ -228,3 +228,30 @@ def test_drafting_cycle(ac, codes):
                 assert want.abs().max() < 127 * 2.0 ** -4
                 tol = 2.0 ** -4 if codes == INT8 else want.abs() * 2.0 ** -4 + 2.0 ** -14
                 assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("codes", [E4M3, INT8])
+@pytest.mark.parametrize("e_from", [63, 64, 100, 120])
+def test_zeros_out_of_a_page_of_large_numbers(ac, codes, e_from):
+    """Tokens of zeros stay zeros, whatever their page's scale was: into a page of zeros, alone and beside small numbers
+    out of a third page, and into a page that they fill."""
+    lens, counts = [128 + 40, 128 + 40, 64 + 128], [128 + 20, 128 + 20, 128]
+    paths = [[50, 55, 60], [50, 110, 112, 115], list(range(64, 128))]
+    c = Cache(pages_of(lens), 2, 64, codes, fill=0)
+    c.fill_random(lens, 1)
+    for b in (0, 1, 2):
+        for h in (0, 1):
+            for w in (0, 1):
+                first, second = (c.head(int(c.pages[b, j]), h) for j in (0, 1))
+                if b < 2:                                    # the first page: zeros
+                    first[w].view(torch.uint8)[:] = 0
+                    first[2][w] = 2.0 ** -64
+                second[2][w] = 2.0 ** e_from
+                second[w].view(torch.uint8)[:] = 0
+                second[w].view(torch.uint8)[0] = 0x38        # its large numbers, which go
+                third = c.head(int(c.pages[b, 2]), h)
+                third[2][w] = 2.0 ** (e_from if b == 2 else -10)
+                if b == 2:                                   # its path takes zeros alone
+                    third[w].view(torch.uint8)[:] = 0
+    run(ac, c, lens, counts, paths)
+    assert not any(torch.isnan(x).any() for x in c.numbers(0, 23, 0)[:2])
