@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
     __shared__ int sm_exp[2][kKvPage];       // its page's exponents
     __shared__ uint8_t *sm_from[kKvPage];    // its strip
     __shared__ float sm_top[2][kWaves];
-    __shared__ int sm_same, sm_bad;
+    __shared__ int sm_same, sm_bad, sm_none;  // (a word a phase: a wave may be a phase ahead of another's reading)
     const uint32_t h = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, wave = tid / 64;
     const bool speaks = h == 0;
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
     const int len = a.c.lens[b], kept = a.kept[b];
     bad = bad || len < count || (uint64_t)len > a.c.stride * kKvPage || kept < 0 || kept > count || (uint64_t)kept > a.path_stride;
     const int32_t *path = a.path + (uint64_t)b * a.path_stride;
-    if (tid == 0) sm_same = sm_bad = 0;
+    if (tid == 0) sm_same = sm_bad = sm_none = 0;
     __syncthreads();
     if (!bad) {
         int same = 0, wrong = 0;
@@ -94,13 +94,13 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAccept a) {
         int none = 0;
         for (int j = j_first + tid; j <= j_last; j += kThreads) none += page_offset(a.c, b, j) == kNoPage;
         if (none) {
-            atomicAdd(&sm_bad, none);
+            atomicAdd(&sm_none, none);
             if (speaks && a.c.n_invalid) atomicAdd(a.c.n_invalid, (unsigned long long)none);
         }
     }
     __syncthreads();
-    if (speaks && tid == 0) a.lens_out[b] = sm_bad ? len : had + kept;
-    if (sm_bad) return;
+    if (speaks && tid == 0) a.lens_out[b] = sm_none ? len : had + kept;
+    if (sm_none) return;
     const uint64_t strip = (uint64_t)h * 2 * kKvPage * D;
     for (int j = j_first; j <= place_page(had + kept - 1); ++j) {
         const int base = j * kKvPage;

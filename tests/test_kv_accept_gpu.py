@@ -255,3 +255,15 @@ def test_zeros_out_of_a_page_of_large_numbers(ac, codes, e_from):
                     third[w].view(torch.uint8)[:] = 0
     run(ac, c, lens, counts, paths)
     assert not any(torch.isnan(x).any() for x in c.numbers(0, 23, 0)[:2])
+
+
+def test_missing_pages_are_counted_once_each(ac):
+    """A path over more pages than a wave has lanes, of which some are none: each is counted, by one head."""
+    t = 150 * PAGE
+    lens, counts, paths = [t + 5, 40], [t, 10], [list(range(1, t, 97)) + [t - 1], [4, 7]]
+    c = Cache(pages_of(lens), 3, 64, INT8, fill=0x11)
+    c.fill_random([70, 40], 1)
+    none = [1, 60, 63, 64, 65, 100, 130, 149]
+    for j in none:
+        c.pages[0, j] = -1
+    run(ac, c, lens, counts, paths, bad=len(none), left=(0,))
