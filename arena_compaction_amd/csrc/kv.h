@@ -114,11 +114,12 @@ struct KvAttend {
     uint64_t pos_cap;
 };
 
-// Which terms a kernel knows: none, the mask, the mask and the cap (prompts
-// alone: few rows do not gain by it), or all of them.
+// Which terms a kernel knows: none, the mask, the mask and a cap up to kLowCap
+// (prompts alone: few rows do not gain by it), or all of them.
 constexpr int kPlain = 0, kMasked = 1, kCapped = 2, kTerms = 3;
+constexpr float kLowCap = 128.0f;  // above, small scores go by a form of their own (cap_scores)
 inline int kv_mode(float cap, const float *slopes, const uint64_t *mask) {
-    return slopes ? kTerms : cap != 0.0f ? kCapped : mask ? kMasked : kPlain;
+    return slopes || cap > kLowCap ? kTerms : cap != 0.0f ? kCapped : mask ? kMasked : kPlain;
 }
 
 struct KvAccept {

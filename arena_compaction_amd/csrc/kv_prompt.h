@@ -459,7 +459,7 @@ __global__ __launch_bounds__((kPromptWaves<D, ROWS>)*64, D == 64 && ((CODES == k
                                     term_scores(a, w[rt], f, slope[rt], row_pos[rt], base + g * 16,
                                                 [&](int x) { return sm_pos[cur][g * 16 + x]; }, c);
                                 else
-                                    cap_scores(a, w[rt], f, c);
+                                    cap_scores<MODE>(a, w[rt], f, c);
                                 if (edge) hide(w[rt], bits);
                             });
                         }

@@ -85,33 +85,48 @@ __device__ inline void hide(f32x4 (&w)[4], uint32_t bits) {
         if (!((bits >> i) & 1)) w[i / 4][i % 4] = KV_NEG_INF;
 }
 
-// Sums over codes w to w * f, capped, + add, in powers of two.
+// Sums over codes w to w * f, capped, + add, in powers of two.  A score goes by
+// a form that the cap and its own size choose, so that nothing beside it, seen or
+// not, changes a bit of it.
 //   c tanh(x) = c - 2 c / (2^(2 x log2(e)) + 1)
-// is off by up to 2^-22 of c, no more than 2^-19 of a score from c / 8 on: pages
-// without any go by c x + c x^3 (a1 + a2 x^2), with the a that leave least,
-// 2^-27 of it.  (The first costs a prompt an eighth of its time: chunks of 2000
-// tokens x 32 heads of 128 279 us for 246.  A series that reaches to 9/16, so
-// that few pages need exponents, took 307.)
+// is off by up to 2^-22 of c.  Up to kLowCap that is no more than 2^-15 of a
+// weight, beside the 2^-11 that rounding it to float16 costs, and every score
+// goes by it.  Above, those from c / 8 on do (2^-19 of the score), and smaller
+// ones are c x + c x^3 (a1 + a2 x^2), with the a that leave least, 2^-27 of the
+// score, so that a large cap is none; pages without any from c / 8 on leave the
+// exponents out.  (Choosing so under every cap costs a prompt a third: chunks of
+// 2000 tokens x 32 heads of 128 under a cap of 30 376 us for 285.)
+// (kLowCap is in kv.h: kernels of kCapped know the first form alone.)
+template <int MODE>
 __device__ inline void cap_scores(const KvAttend &a, f32x4 (&w)[4], float f, float add) {
-    if (a.score_cap != 0.0f) {
-        const float c = a.score_cap * kLog2e, by = f * (1.0f / c);
+    if (MODE == kCapped || a.score_cap != 0.0f) {
+        // z = 2 x log2(e), so that x = z ln(2) / 2
+        const float c = a.score_cap * kLog2e, by = f * (1.0f / c) * (2.0f * kLog2e), top = c + add;
+        auto large = [&](float z) __attribute__((always_inline)) {
+            return __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), top);
+        };
+        if (MODE == kCapped || a.score_cap <= kLowCap) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = large(w[i / 4][i % 4] * by);
+            return;
+        }
+        const float limit = 0.25f * kLog2e, a1 = c * (-0.333327708f * 0.0416280815f), a2 = c * (0.132167363f * 0.00500008430f);
+        auto small = [&](float v, float z) __attribute__((always_inline)) {
+            const float y = z * z;
+            return __builtin_fmaf(__builtin_fmaf(a2, y, a1), y * z, __builtin_fmaf(v, f, add));
+        };
         float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(w[i / 4][i % 4]));
-        if (__builtin_amdgcn_ballot_w64(!(most * fabsf(by) < 0.125f))) {
-            const float by2 = by * (2.0f * kLog2e), top = c + add;
+        if (__builtin_amdgcn_ballot_w64(!(most * fabsf(by) < limit))) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(w[i / 4][i % 4] * by2);
-                w[i / 4][i % 4] = __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(e + 1.0f), top);
+                const float v = w[i / 4][i % 4], z = v * by;
+                w[i / 4][i % 4] = fabsf(z) < limit ? small(v, z) : large(z);
             }
         } else {
-            const float a1 = c * -0.333327708f, a2 = c * 0.132167363f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = w[i / 4][i % 4], x = v * by, y = x * x;
-                w[i / 4][i % 4] = __builtin_fmaf(__builtin_fmaf(a2, y, a1), y * x, __builtin_fmaf(v, f, add));
-            }
+            for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = small(w[i / 4][i % 4], w[i / 4][i % 4] * by);
         }
     } else {
 #pragma unroll
@@ -125,7 +140,7 @@ __device__ inline void cap_scores(const KvAttend &a, f32x4 (&w)[4], float f, flo
 template <typename Pos>
 __device__ inline void term_scores(const KvAttend &a, f32x4 (&w)[4], float f, float slope, int row_pos, int place, Pos key_pos,
                                    float add) {
-    cap_scores(a, w, f, a.pos ? add : __builtin_fmaf(slope, (float)(place - row_pos), add));
+    cap_scores<kTerms>(a, w, f, a.pos ? add : __builtin_fmaf(slope, (float)(place - row_pos), add));
     if (!a.slopes) return;
     if (a.pos) {
 #pragma unroll
