@@ -100,8 +100,10 @@ __device__ inline void hide(f32x4 (&w)[4], uint32_t bits) {
 template <int MODE>
 __device__ inline void cap_scores(const KvAttend &a, f32x4 (&w)[4], float f, float add) {
     if (MODE == kCapped || a.score_cap != 0.0f) {
-        // z = 2 x log2(e), so that x = z ln(2) / 2
-        const float c = a.score_cap * kLog2e, by = f * (1.0f / c) * (2.0f * kLog2e), top = c + add;
+        // z = 2 x log2(e), so that x = z ln(2) / 2; its factor stays finite, as
+        // a sum of 0 is 0 under a small cap over large keys too
+        const float c = a.score_cap * kLog2e, top = c + add;
+        const float by = __builtin_amdgcn_fmed3f(f * (1.0f / c) * (2.0f * kLog2e), -__FLT_MAX__, __FLT_MAX__);
         auto large = [&](float z) __attribute__((always_inline)) {
             return __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), top);
         };

@@ -112,3 +112,25 @@ def test_scores_of_many_sizes_in_one_tile(ac, group, bias):
     err = (lse[0].double().cpu() - want).abs()
     assert (err <= want * 2.0 ** -19 + want * 2.0 ** -21 + 15 * 2.0 ** -20).all()
     assert (out == 1.0).all()
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -64, 2.0 ** -30, 2.0 ** 64])
+@pytest.mark.parametrize("count", [1, 50])
+def test_scores_of_zero_under_any_cap(ac, cap, count):
+    """Queries of zeros over keys of the largest scale: every score is 0, and every token counts alike."""
+    n = 90
+    c = Cache([2], 1, 64, INT8, fill=0)
+    c.fill_random([n], 1)
+    for j in (0, 1):
+        c.head(int(c.pages[0, j]), 0)[2][0] = 2.0 ** 120
+    q = torch.zeros(count, 2, 64, dtype=BF16)
+    lse = torch.full((count, 2), 7.0, device="cuda")
+    out = ac.defrag_kv_attend_terms(c.arena.cuda(), c.pages.cuda(), ints([n]), q.cuda(), 1, INT8, cap=cap, starts=starts_of([count]),
+                                    max_new=count, lse=lse).double().cpu()
+    v = c.numbers(0, n, 0)[1]
+    for t in range(count):
+        see = n - count + t + 1
+        want = v[:see].mean(0)
+        assert abs(float(lse[t, 0]) - math.log(see)) <= 2.0 ** -19
+        # each weight is rounded to float16 alike, and the sum to 32 bits
+        assert ((out[t] - want).abs() <= want.abs() * HALF[BF16] + v[:see].abs().mean(0) * 2.0 ** -10 + 2.0 ** -25).all()
