@@ -147,7 +147,15 @@ int check_append(const defrag_kv_append_args *a) {
         return DEFRAG_EINVAL;
     if (a->tokens && (!a->k_dev || !a->v_dev)) return DEFRAG_EINVAL;
     if ((uint64_t)kv_append_pages(a->max_new, c->page_stride) * 2 * c->dim > 0xFFFFFFFFu) return DEFRAG_EINVAL;
-    return DEFRAG_OK;
+    // (every head writes its own rows of the planes, and reads all of these)
+    const uint64_t rows = (uint64_t)c->batch * c->heads;
+    const Span out[] = {plane(a->weight_dev, rows, a->weight_stride, a->weight_stride),
+                        plane(a->pos_dev, rows, a->weight_stride, a->weight_stride)};
+    const Span in[] = {strided(a->k_dev, a->tokens, a->k_row, c->heads, a->k_head, c->dim),
+                       strided(a->v_dev, a->tokens, a->v_row, c->heads, a->v_head, c->dim),
+                       plane(a->first_pos_dev, 1, 0, c->batch), plane(a->starts_dev, 1, 0, c->batch + 1ull),
+                       plane(c->lens_dev, 1, 0, c->batch), plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
+    return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;
 }
 
 KvAppend append_of(const defrag_kv_append_args *a) {
@@ -170,18 +178,21 @@ int check_rotary(const defrag_kv_rotary_args *r) {
     if (a->tokens && (!r->freq_dev || (r->q_heads && (!r->q_dev || !r->out_dev)))) return DEFRAG_EINVAL;
     if (c->heads + ((uint64_t)r->q_heads + kRotaryHeads - 1) / kRotaryHeads > 65535 || a->tokens * r->q_heads > kMaxRows)
         return DEFRAG_EINVAL;
+    const uint64_t rows = (uint64_t)c->batch * c->heads;
+    const Span planes[] = {plane(a->weight_dev, rows, a->weight_stride, a->weight_stride),
+                           plane(a->pos_dev, rows, a->weight_stride, a->weight_stride)};
+    const Span read[] = {plane(r->freq_dev, 1, 0, r->rotary_dim), plane(r->token_pos_dev, 1, 0, a->tokens),
+                         strided(r->q_dev, a->tokens, r->q_row, r->q_heads, r->q_head, c->dim)};
+    if (any_overlap(planes, read)) return DEFRAG_EINVAL;
     if (!a->tokens || !r->q_heads) return DEFRAG_OK;
     if (!rows_apart(a->tokens, r->out_row, r->q_heads, r->out_head, c->dim)) return DEFRAG_EINVAL;
     const Rows to{r->out_dev, a->tokens, r->out_row, r->q_heads, r->out_head, c->dim};
     const Rows q{r->q_dev, a->tokens, r->q_row, r->q_heads, r->q_head, c->dim};
     const Rows k{a->k_dev, a->tokens, a->k_row, c->heads, a->k_head, c->dim}, v{a->v_dev, a->tokens, a->v_row, c->heads, a->v_head, c->dim};
     const bool same = r->out_dev == r->q_dev && (a->tokens == 1 || r->out_row == r->q_row) && (r->q_heads == 1 || r->out_head == r->q_head);
-    const uint64_t rows = (uint64_t)c->batch * c->heads;
     if ((!same && rows_overlap(to, q)) || rows_overlap(to, k) || rows_overlap(to, v)) return DEFRAG_EINVAL;
     const Span out[] = {to.span()};
-    const Span in[] = {Span{c->arena_dev, c->arena_bytes}, plane(a->weight_dev, rows, a->weight_stride, a->weight_stride),
-                       plane(a->pos_dev, rows, a->weight_stride, a->weight_stride), plane(r->freq_dev, 1, 0, r->rotary_dim),
-                       plane(r->token_pos_dev, 1, 0, a->tokens), plane(a->first_pos_dev, 1, 0, c->batch),
+    const Span in[] = {Span{c->arena_dev, c->arena_bytes}, planes[0], planes[1], read[0], read[1], plane(a->first_pos_dev, 1, 0, c->batch),
                        plane(a->starts_dev, 1, 0, c->batch + 1ull), plane(c->lens_dev, 1, 0, c->batch),
                        plane(c->pages_dev, 1, 0, 2 * c->batch * c->page_stride)};
     return any_overlap(out, in) ? DEFRAG_EINVAL : DEFRAG_OK;

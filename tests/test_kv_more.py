@@ -226,3 +226,33 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         ac.defrag_kv_accept(arena, pages, lens, torch.zeros(2, 4, dtype=torch.int32), lens, lens.clone(), 1, 64, E4M3)
     assert PAGE == ac.KV_PAGE_TOKENS
+
+
+APPEND_FAULTS = [   # rows of 4 x 2 x 8 numbers from 0x800000 on are 0x100 bytes
+    dict(weight_dev=0x800000, pos_dev=0x800000), dict(weight_dev=0x800000, pos_dev=0x8000FC),
+    dict(weight_dev=0x800000, first_pos_dev=0x8000F4), dict(pos_dev=0x800000, first_pos_dev=0x800010),
+    dict(pos_dev=0x20000), dict(weight_dev=0x30008), dict(pos_dev=0x40010), dict(weight_dev=0x50000 - 4),
+    dict(pos_dev=0x800000, starts_dev=0x800000)]
+ROTARY_FAULTS = [
+    dict(pos_dev=0x800000, token_pos_dev=0x8000F0), dict(weight_dev=0x800000, token_pos_dev=0x800000),
+    dict(pos_dev=0x800000, freq_dev=0x800080), dict(weight_dev=0x800000 - 4, freq_dev=0x800000)]
+
+
+@pytest.mark.parametrize("fault", APPEND_FAULTS + [dict(weight_dev=0x30010, weight_stride=1 << 60)])
+def test_append_refuses_planes_over_what_it_reads(fault):
+    a = _args(ac.defrag_kv_append_args, **{"arena_dev": 0x8000000, "weight_stride": 8, **fault})
+    said = ac.lib.defrag_kv_append(ctypes.byref(a), None)
+    assert said == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("queries", [dict(), dict(q_heads=0, q_dev=None, out_dev=None)])
+@pytest.mark.parametrize("fault", APPEND_FAULTS + ROTARY_FAULTS)
+def test_rotary_refuses_planes_over_what_it_reads(fault, queries):
+    r = _rotary(**{"arena_dev": 0x8000000, "weight_stride": 8, **fault, **queries})
+    assert ac.lib.defrag_kv_append_rotary(ctypes.byref(r), None) == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("fault", [dict(pos_dev=0xB0100), dict(weight_dev=0xB0000 + 8 * 64 * 2 * 4 - 4)])
+def test_rotary_refuses_planes_over_queries(fault):
+    r = _rotary(**{"arena_dev": 0x8000000, "weight_stride": 8, **fault})
+    assert ac.lib.defrag_kv_append_rotary(ctypes.byref(r), None) == ac.DEFRAG_EINVAL
