@@ -808,6 +808,8 @@ def defrag_kv_attend_terms(arena, pages, lens, q, heads: int, codes, mask=None, 
     the positions (default: the places), a multiple of 64 of them and at least
     max_len."""
     words = 0
+    if cap and not ctypes.c_float(cap).value:   # the field's 0 is none
+        raise DefragError(DEFRAG_EINVAL, f"cap = {cap}")
     if mask is not None:
         if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
             raise ValueError("mask: int64 [tokens, words] expected")

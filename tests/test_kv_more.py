@@ -256,3 +256,12 @@ def test_rotary_refuses_planes_over_what_it_reads(fault, queries):
 def test_rotary_refuses_planes_over_queries(fault):
     r = _rotary(**{"arena_dev": 0x8000000, "weight_stride": 8, **fault})
     assert ac.lib.defrag_kv_append_rotary(ctypes.byref(r), None) == ac.DEFRAG_EINVAL
+
+
+@pytest.mark.parametrize("cap", [1e-50, -1e-46, 5e-324])
+def test_binding_refuses_a_cap_that_its_field_would_make_none(cap):
+    """Below what a float32 holds: 0 there would mean that there is no cap."""
+    arena, pages, lens = torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ac.DefragError):
+        ac.defrag_kv_attend_terms(arena, pages, lens, q, 1, E4M3, cap=cap)
