@@ -25,16 +25,22 @@ namespace {
 //    768     93    92   119                  342   319   383
 // and of 1000 tokens, 504 units, whole 20 us, in 3 pieces 28; with 32 rows, 504
 // units of 4096, 63 and 79; of 9000 whole and 3 pieces lie within a tenth.
-// With a cap or a bias 2 workgroups share a unit, so that 2 pieces fill them up
-// where the caches are whole otherwise; 8000 tokens, lengths down to a third,
-// with weights:
-//   units           272   320   384   448   512
-//   whole           139   145   163   173   193 us
-//   in 2 pieces     119   133   147   179   192
-// (of 4000 tokens, 384 units, 73 and 68; of 1000 27 and 30).
+// With a cap or a bias, up to 16 rows and 96 or 128 dimensions, 2 pieces even out
+// the second round of workgroups where the caches are whole otherwise; 8000
+// tokens, those with a bias with weights, in two pieces and whole:
+//   units                            264       272       304       336       384       408
+//   128, lengths to a third, bias  106 105   120 139   130 144   136 150   147 163   169 171 us
+//   128, lengths alike, bias       159 186   162 188   168 192   179 197   200 211   226 222
+//   128, lengths to a third, cap    80  73    92 105   101 110   106 115   113 119   130 125
+//    96, lengths to a third, bias   87  73    95 102   103 114   111 122   120 133   140 139
+//    96, lengths to a third, cap    63  48    69  72    78  81    83  87    90  94   107  99
+//    96, lengths alike, cap         95 111    96 112    98 113   101 115   110 118   129 119
+// (at 288 units, lengths to a third, a cap is 2% to 7% longer in pieces).  Of 64
+// dimensions a cap is up to 20% longer in pieces, a bias with weights 7% shorter
+// to 9% longer; 17 to 32 rows of 320 units and more are up to 14% longer.
 uint64_t few_splits(uint64_t units, uint64_t pages, uint32_t rows, uint32_t dim, bool terms) {
     if (units == 0) return 1;
-    if (terms && dim <= 128 && units >= 256 && units < 416 && pages > 60 && pages <= 192) return 2;
+    if (terms && rows == 16 && (dim == 96 || dim == 128) && units >= 272 && units <= 384 && pages > 60 && pages <= 192) return 2;
     if (units >= 256) return pages <= 192 ? 1 : 3;
     return ((rows == 16 ? 1024 : 512) + units - 1) / units;
 }

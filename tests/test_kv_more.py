@@ -265,3 +265,17 @@ def test_binding_refuses_a_cap_that_its_field_would_make_none(cap):
     q = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ac.DefragError):
         ac.defrag_kv_attend_terms(arena, pages, lens, q, 1, E4M3, cap=cap)
+
+
+@pytest.mark.parametrize("batch,max_new,group,dim,pieces", [
+    (34, 1, 4, 128, 2), (48, 1, 4, 96, 2), (33, 1, 4, 128, 1), (49, 1, 4, 128, 1), (40, 1, 4, 64, 1), (40, 5, 4, 128, 1),
+    (40, 5, 4, 96, 1), (40, 1, 4, 192, 1)])
+def test_terms_cut_long_caches_in_two_where_that_was_measured_to_gain(batch, max_new, group, dim, pieces):
+    """8 heads, 8000 tokens: two pieces for 272 to 384 (sequence, head)s of up to 16 rows and 96 or 128 dimensions."""
+    tokens = batch * max_new
+    a = _args(ac.defrag_kv_attend_args, batch=batch, heads=8, dim=dim, page_stride=125, tokens=tokens, starts_dev=0x1000, max_new=max_new,
+              group=group, max_len=8000, q_dev=0x20000000, out_dev=0x30000000, weight_dev=None)
+    need = ac.lib.defrag_kv_attend_terms_workspace_bytes(ctypes.byref(a), ctypes.byref(_terms(mask_dev=None, mask_words=0, slopes_dev=None,
+                                                                                               pos_dev=None)))
+    parts = pieces * tokens * 8 * group * (dim + 2) * 4 if pieces > 1 else 1
+    assert need == (parts + 255) // 256 * 256 if pieces > 1 else need == 1
