@@ -109,6 +109,7 @@ struct KvAttend {
     const uint64_t *mask;  // [tokens][mask_words] bits
     uint64_t mask_words;
     float score_cap;       // natural units
+    float cap_by;          // 2 / score_cap
     const float *slopes;   // [heads * group]
     const int32_t *pos;    // [batch][heads][pos_cap]
     uint64_t pos_cap;

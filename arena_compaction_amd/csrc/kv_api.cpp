@@ -366,6 +366,7 @@ int attend(const defrag_kv_attend_args *a, const defrag_kv_terms *t, const KvAtt
         k.mask = t->mask_dev;
         k.mask_words = t->mask_words;
         k.score_cap = t->cap;
+        k.cap_by = t->cap != 0.0f ? 2.0f / t->cap : 0.0f;
         k.slopes = t->slopes_dev;
         k.pos = t->pos_dev;
         k.pos_cap = t->pos_stride;

@@ -103,32 +103,32 @@ __device__ inline void cap_scores(const KvAttend &a, f32x4 (&w)[4], float f, flo
         // z = 2 x log2(e), so that x = z ln(2) / 2; its factor stays finite, as
         // a sum of 0 is 0 under a small cap over large keys too
         const float c = a.score_cap * kLog2e, top = c + add;
-        const float by = __builtin_amdgcn_fmed3f(f * (1.0f / c) * (2.0f * kLog2e), -__FLT_MAX__, __FLT_MAX__);
+        const float by = __builtin_amdgcn_fmed3f(f * a.cap_by, -__FLT_MAX__, __FLT_MAX__);
         auto large = [&](float z) __attribute__((always_inline)) {
             return __builtin_fmaf(-2.0f * c, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), top);
         };
         if (MODE == kCapped || a.score_cap <= kLowCap) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = large(w[i / 4][i % 4] * by);
-            return;
-        }
-        const float limit = 0.25f * kLog2e, a1 = c * (-0.333327708f * 0.0416280815f), a2 = c * (0.132167363f * 0.00500008430f);
-        auto small = [&](float v, float z) __attribute__((always_inline)) {
-            const float y = z * z;
-            return __builtin_fmaf(__builtin_fmaf(a2, y, a1), y * z, __builtin_fmaf(v, f, add));
-        };
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(w[i / 4][i % 4]));
-        if (__builtin_amdgcn_ballot_w64(!(most * fabsf(by) < limit))) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = w[i / 4][i % 4], z = v * by;
-                w[i / 4][i % 4] = fabsf(z) < limit ? small(v, z) : large(z);
-            }
         } else {
+            const float limit = 0.25f * kLog2e, a1 = c * (-0.333327708f * 0.0416280815f), a2 = c * (0.132167363f * 0.00500008430f);
+            auto small = [&](float v, float z) __attribute__((always_inline)) {
+                const float y = z * z;
+                return __builtin_fmaf(__builtin_fmaf(a2, y, a1), y * z, __builtin_fmaf(v, f, add));
+            };
+            float most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = small(w[i / 4][i % 4], w[i / 4][i % 4] * by);
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(w[i / 4][i % 4]));
+            if (__builtin_amdgcn_ballot_w64(!(most * fabsf(by) < limit))) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float v = w[i / 4][i % 4], z = v * by;
+                    w[i / 4][i % 4] = fabsf(z) < limit ? small(v, z) : large(z);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = small(w[i / 4][i % 4], w[i / 4][i % 4] * by);
+            }
         }
     } else {
 #pragma unroll
