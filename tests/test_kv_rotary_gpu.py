@@ -335,3 +335,39 @@ def test_stream_and_graph(ac):
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (out, q_out, arena)))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,rotary", [(64, 64), (128, 96), (256, 256)])
+def test_queries_by_their_pairs(ac, dim, rotary, interleaved, dtype):
+    """Each query's error beside its own pair's larger number M, among pairs of sizes that lie far apart and some whose
+    products cancel: sine and cosine rounded to 32 bits, (|cos| + |sin|) 2^-24 M <= 1.42 * 2^-24 M; a product, 2^-24 M; their
+    sum, 1.42 * 2^-24 M; together below 2^-22 M.  The angle p f is off by 3 * 2^-53 of itself in the kernel's turns and 2^-53
+    here, which moves a number by that times at most 1.42 M.  Then half a step of the type."""
+    n, heads = 200, 6
+    gen = torch.Generator().manual_seed(dim + interleaved)
+    pos = torch.randint(0, 200_000, (n,), generator=gen)
+    freq = freqs(rotary)
+    q = torch.randn(n, heads, dim, generator=gen, dtype=torch.float64)
+    first, second = (slice(0, rotary, 2), slice(1, rotary, 2)) if interleaved else (slice(0, rotary // 2), slice(rotary // 2, rotary))
+    size = torch.exp2(torch.randint(-6, 7, (n, heads, rotary // 2), generator=gen).double())
+    angle = pos.double()[:, None] * freq
+    near = torch.rand(n, heads, rotary // 2, generator=gen) < 0.5       # these lie where the first number comes to almost 0
+    x, y = q[..., first] * size, q[..., second] * size
+    x = torch.where(near, (size * torch.sin(angle)[:, None]), x)
+    y = torch.where(near, (size * torch.cos(angle)[:, None]), y)
+    q[..., first], q[..., second] = x, y
+    q = q.to(dtype)
+    k = torch.zeros(n, 1, dim, dtype=dtype)
+    c = Cache([-(-n // PAGE)], 1, dim, INT8)
+    out = ac.defrag_kv_append_rotary(c.arena.cuda(), c.pages.cuda(), ints([0]), k.cuda(), k.cuda(), INT8, freq.cuda(), q=q.cuda(),
+                                     interleaved=interleaved, starts=ints([0, n]), token_pos=ints(pos.tolist()))
+    got, want = out.double().cpu(), rotate(q, pos, freq, interleaved)
+    half = torch.finfo(dtype).eps / 2
+    for at in (first, second):
+        most = torch.maximum(q[..., first].double().abs(), q[..., second].double().abs())
+        near = most * (2.0 ** -22 + 1.42 * 2.0 ** -51 * angle[:, None])
+        tol = near + (want[..., at].abs() + near) * half + 2.0 ** -25 * (dtype == FP16)
+        assert ((got[..., at] - want[..., at]).abs() <= tol).all()
+    assert torch.equal(got[..., rotary:], q.double()[..., rotary:])
