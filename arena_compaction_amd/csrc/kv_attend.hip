@@ -50,7 +50,12 @@ uint64_t few_splits(uint64_t units, uint64_t pages, uint32_t rows, uint32_t dim,
 // alone 1.5 (above 128 dimensions it always is); a cut costs 18 us, and 1 us for
 // 40 workgroups, since each writes its sums for the join (one sequence, 16
 // query heads a head, 8 heads of 128, 63 pages: 128 tokens whole 96 us, in 2
-// pieces 75, in 4 64, in 8 74; 256 tokens whole 106, in 4 pieces 113).
+// pieces 75, in 4 64, in 8 74; 256 tokens whole 106, in 4 pieces 113).  For a few
+// short caches that is too much.  Trees of drafts, 8 heads of 128 x 4, with the
+// pieces that this gives, twice and three times as many:
+//   4 x 1000, 30 drafts   37  29  23 us     48 x 2000, 16 drafts    52  62  62 us
+//   8 x 4000, 32          40  49  49        32 x 4000, 32          104  96 113
+//   16 x 10,000, 25      107 116 121        2 x 131,000, 25        184 193 203
 uint64_t prompt_splits(uint64_t units, uint64_t pages, uint32_t max_new, uint32_t dim) {
     const uint64_t slots = dim <= 128 ? 512 : 256;
     uint64_t best = 1, least = ~0ull;
@@ -95,7 +100,9 @@ KvAttendPlan kv_attend_plan(uint32_t batch, uint32_t heads, uint32_t group, uint
     // Small trees: half of 128 rows would be none.  8 heads of 128, 4 query
     // heads each, 16 sequences of 5000-10,000 tokens: 9 drafts 69 us with 64
     // rows and 93 with 128, 16 drafts 82 and 100; 64 sequences of 1200-4000, 16
-    // drafts 103 and 138.
+    // drafts 103 and 138.  (A mask alone: the kernels with a cap or a bias have 128
+    // rows, and take these calls 119, 123 and 168 under a cap, 121, 123 and 171
+    // with a bias; they were not made for 64.)
     if (mode == kMasked && dim <= 128 && p.rows == kKvPromptRows && rows <= kKvTreeRows) p.rows = kKvTreeRows;
     p.row_blocks = (uint32_t)((rows + p.rows - 1) / p.rows);
     const uint64_t units = (uint64_t)batch * heads * p.row_blocks;

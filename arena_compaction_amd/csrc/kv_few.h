@@ -31,7 +31,7 @@
 //
 // Terms (kv_rows.h) add a few instructions a score, which the loads hide, and
 // registers: a cap over 64 x 4096 x 4 heads of 256 takes 72 us where none takes
-// 68; a bias with positions of 48 x 8000 x 8 heads of 128, with weights (536
+// 70; a bias with positions of 48 x 8000 x 8 heads of 128, with weights (536
 // MB), 127 us and a join of 19 (two waves a SIMD, where three without terms;
 // three with 19 registers in memory took 155 for 140).
 #ifndef ARENA_COMPACTION_KV_FEW_H

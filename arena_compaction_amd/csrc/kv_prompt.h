@@ -13,19 +13,26 @@
 // What bounds it: the vector pipe (an exponent, a fused product, an addition
 // and half a conversion a score) and the matrix pipe, which two waves a SIMD
 // overlap only in part.  Chunks of 2000 tokens x 32 heads of 128 behind 2048
-// (169 GFLOP) take 223 us, 0.76 PFLOP/s, where a product of 8192 cubed reaches
-// 1.18: the matrix pipe is busy for 31% of the cycles, the vector pipe for 37%,
+// (169 GFLOP) take 211 us, 0.80 PFLOP/s, where a product of 8192 cubed reaches
+// 1.26: the matrix pipe is busy for 31% of the cycles, the vector pipe for 37%,
 // and 22% are lost to the last rows, which see most.  With 64 dimensions the
-// vector pipe is busy for 83% (8200 tokens x 32 heads, float16: 380 us).
+// vector pipe is busy for 83% (8200 tokens x 32 heads, float16: 366 us).  (All calls named here in
+// turn in one loop; the first after a pause are slower by up to a tenth.)
 //
 // Terms (kv_rows.h): a page's mask words are loaded a page ahead, one a lane,
 // and dealt out where some row misses some token; a wave whose rows see nothing
 // of a page only brings the next one to LDS.  A causal mask costs the prompt of
-// 8200 tokens 408 us for 392, five documents in it 140; a cap the chunks above
-// 286 for 244, with the vector pipe busy for 54% of the cycles.  With a distance
-// bias registers leave two waves a SIMD for 64 dimensions, where the plain
-// kernel has three: 560 us for 392, documents 200 (three, with 60 registers in
-// memory: 630 and 250).
+// 8200 tokens 395 us for 366, five documents in it take 144, behind 1 to 63
+// tokens 231, as no page is then left out before the first one that is seen; a
+// cap costs the chunks above 273 for 211, with the vector pipe busy for 54% of the
+// cycles, and above kLowCap 289.  With a distance bias registers leave two waves
+// a SIMD for 64 dimensions, where the plain kernel has three: 566 us for 366,
+// documents 205 (three, with 60 registers in memory, took an eighth and a quarter more).
+//
+// Registers go to memory where the type of int8 is bfloat16 (20 of 128 dimensions
+// under a cap, 27 under a mask, 98 with all terms; 41 to 107 of 256, the plain
+// kernel's 91 among them), in float16 over e4m3 of 256 under a cap (80), and some
+// 10 of 256 with any term.
 //
 // Workgroups of one key/value head run on one XCD where the heads are a
 // multiple of 8, so that its pages stay in that XCD's L2; the last rows,

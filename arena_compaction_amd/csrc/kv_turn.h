@@ -6,8 +6,10 @@
 // position 100,000 would be off by 2^-8.  Keys stay in 64 bits and are rounded
 // once, to their code: beside the border between two codes, or a page's largest
 // beside that between two scales, 32 bits would fall on either side.  Queries
-// are products in 32 bits, whose rounding, 2^-23 of the pair's larger number,
-// is lost beside the one to 16 bits (2^-11 at least of the result).
+// are products in 32 bits, off by up to 2^-22 of the pair's larger number (sine
+// and cosine rounded, a product, a sum): little beside the 2^-11 at least that
+// their type rounds by, but where the two products cancel it is an absolute
+// error that may exceed the small result's own rounding.
 //
 // The angle is taken in turns, p * (f / 2 pi), of which only the fraction
 // counts; a quarter turn more or less swaps sine and cosine, so that their

@@ -1,5 +1,14 @@
 // kv_weigh.h -- the weight that every cached token receives, from scores that
-// are made again (kv_finish.hip says when and what it costs).
+// are made again (kv_finish.hip says when, and what it costs without terms).
+//
+// With terms an exponent a score is not all: 4 sequences of 500 tokens behind
+// 1000, 8 heads x 4 query heads each, documents, e4m3; the pass over the pages
+// alone and with the weights, without terms, under a mask, with a bias:
+//    64 dimensions   40  72    44  75    52 102 us
+//   128              57 104    60 117    71 140
+//   256             107 178   110 235   124 254
+// Of 256 dimensions 34 registers go to memory under a mask and 51 to 56 with all
+// terms, none without.
 #ifndef ARENA_COMPACTION_KV_WEIGH_H
 #define ARENA_COMPACTION_KV_WEIGH_H
 #include "kv_rows.h"
@@ -19,6 +28,10 @@ __device__ inline bool piece_tiles(const KvAttend &a, const Seq &s, int base, in
 }
 
 // Waves of a workgroup: with terms never 16, whose 128 registers would spill.
+// (Pieces of the rows are sized by the plain kernel's, so that a call's workspace
+// does not depend on its terms.  Sized by 8 waves, twice as many for 64
+// dimensions: 2 x 206 tokens x 3 heads x 16 query heads under a mask 27.7 us for
+// 29.6, under a cap 30.3 for 34.7; 700 behind 300, 2 heads x 8, 37.1 for 35.3.)
 template <int D, int MODE>
 constexpr int kWeighWaves = MODE == kPlain ? (int)kv_weigh_waves(D) : 8;
 

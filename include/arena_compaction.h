@@ -568,8 +568,8 @@ int defrag_kv_append(const defrag_kv_append_args *args, hipStream_t stream);
  * x sin + y cos).  The first rotary_dim dimensions are pairs, of (i, i +
  * rotary_dim / 2), or with interleaved 1 of (2 i, 2 i + 1); the others stay
  * as they are.  Keys are rotated in 64 bits and rounded once, to their code;
- * queries by products in 32 bits (of 64-bit angles), which are rounded to
- * their type; an infinity or a NaN goes by the formula, that is, reaches both
+ * queries by products in 32 bits (of 64-bit angles), off by up to 2^-22 of
+ * their pair's larger number, which are rounded to their type; an infinity or a NaN goes by the formula, that is, reaches both
  * numbers of its pair.  A token's position is
  * token_pos_dev[token], or where that is NULL first_pos_dev[b] + its number
  * (first_pos_dev NULL: its place); pos_dev gets it.  out_dev gets the queries,
