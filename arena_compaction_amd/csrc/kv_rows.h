@@ -89,10 +89,12 @@ __device__ inline void hide(f32x4 (&w)[4], uint32_t bits) {
 // a form that the cap and its own size choose, so that nothing beside it, seen or
 // not, changes a bit of it.
 //   c tanh(x) = c - 2 c / (2^(2 x log2(e)) + 1)
-// is off by up to 2^-22 of c.  Up to kLowCap that is no more than 2^-15 of a
-// weight, beside the 2^-11 that rounding it to float16 costs, and every score
-// goes by it.  Above, those from c / 8 on do (2^-19 of the score), and smaller
-// ones are c x + c x^3 (a1 + a2 x^2), with the a that leave least, 2^-27 of the
+// is off by up to 2^-21 of c (the quotient q by 2^-23 of itself, the sum by 2^-24,
+// the power by 2^-23 and its exponent by 2^-23, which q (1 - q) <= 1/4 and 0.23
+// weigh, all doubled: 2 c (1.5 q + 0.48) 2^-23).  Up to kLowCap that is no more
+// than 2^-14 of a weight, beside the 2^-11 that rounding it to float16 costs, and
+// every score goes by it.  Above, those from c / 8 on do (there 1.3 * 2^-22 of c,
+// less than 2^-18 of the score), and smaller ones are c x + c x^3 (a1 + a2 x^2), with the a that leave least, 2^-27 of the
 // score, so that a large cap is none; pages without any from c / 8 on leave the
 // exponents out.  (Choosing so under every cap costs a prompt a third: chunks of
 // 2000 tokens x 32 heads of 128 under a cap of 30 376 us for 285.)

@@ -635,7 +635,7 @@ int defrag_kv_attend(const defrag_kv_attend_args *args, void *ws_dev, size_t ws_
 /* defrag_kv_attend with terms beside causal softmax; each may be left out.
  * With s = scale * q.k, in this order:
  *   cap    : s becomes cap * tanh(s / cap)                    (0: none), off by
- *            up to 2^-22 of a cap up to 128, and 2^-19 of s under a larger one
+ *            up to 2^-21 of a cap up to 128, and 2^-18 of s under a larger one
  *   slopes : s becomes s + slopes_dev[query head] * (position of the cached
  *            token - position of the query's); positions are pos_dev's at the
  *            tokens' places (which append, evict and accept keep), or where
